@@ -270,6 +270,91 @@ MOBA_API moba_status dense_causal_forward(const moba_params* p, const void* q, c
                                  const void* v, const int32_t* cu_seqlens, void* out, float* lse,
                                  void* stream);
 
+/* Gradient of dense_causal_forward (PaperTrace "2.1.3 MoBA", section 1 eq. (1)
+ * with a causal mask; section 5.3 for the form of the backward pass), for the
+ * layers of a hybrid stack that keep full attention. Gradients of
+ * L = sum(dout * out): with P_ij = exp(q_i.k_j / sqrt(d) - lse_i) over the
+ * keys j <= i of the query's own sequence and D_i = dout_i . out_i,
+ * dS_ij = P_ij (dout_i.v_j - D_i), dq_i = sum_j dS_ij k_j / sqrt(d),
+ * dk_j = sum_i dS_ij q_i / sqrt(d), dv_j = sum_i P_ij dout_i (i also over the
+ * q heads of a kv head's group).
+ *   out [T][Hq][d], lse [T][Hq] (fp32, natural log): the forward's results;
+ *   dout [T][Hq][d]: p->dtype.
+ *   dq [T][Hq][d], dk, dv [T][Hkv][d]: p->dtype (summed in fp32, rounded once),
+ *   overwritten; rows that no sequence owns get zeros.
+ *   ws: dense_causal_backward_workspace_size(p) bytes, 32-byte aligned.
+ * Every gradient row is summed by one CTA in a fixed order: equal calls give
+ * equal bits. block_size and topk in p must be valid but do not change the
+ * result. For bf16 inputs P and dS enter the tensor core rounded to bf16. */
+MOBA_API size_t dense_causal_backward_workspace_size(const moba_params* p);
+MOBA_API moba_status dense_causal_backward(const moba_params* p, const void* q, const void* k,
+                                           const void* v, const int32_t* cu_seqlens,
+                                           const void* out, const float* lse, const void* dout,
+                                           void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                                           void* stream);
+
+/* ---- A paged KV cache in 8 bits ------------------------------------------
+ * (no paper counterpart; section 5.4: a decode step is bound by the KV bytes.)
+ * Pages of page_size tokens, [num_pages][Hkv][page_size][d] in e4m3 for K and
+ * for V, each row (one token, one kv head) with one power-of-two scale
+ * [num_pages][Hkv][page_size] in e8m0: value = code * 2^(byte - 127).
+ *   row exponent e = the smallest integer with max|x| <= 448 * 2^e, at least
+ *   -127; code = x * 2^-e rounded once to e4m3 (ties to even; from e = 120 on
+ *   codes stop at 240, so that values stay finite). A row that holds an
+ *   infinity or a NaN gets byte 255: it reads back as NaN.
+ * Position p of request r stands in row p % page_size of page
+ * page_table[r][p / page_size]. Requests may share pages; pages that one call
+ * writes must not be written by two requests of it, nor read or written by
+ * another call at the same time.
+ * In every call p->batch is the number of requests, p->total_tokens the
+ * number of rows of the call, seqlens[r] request r's length (after the
+ * append), and request r's rows cu[r] .. cu[r+1]-1 stand at its last
+ * positions. Rows at or past cu[batch] (a padded batch) are left alone. A
+ * request with more rows than positions, or longer than p->max_seqlen or its
+ * max_pages pages, is skipped and records MOBA_ERR_INVALID_ARG in the status
+ * word; a table entry that names no page is skipped and records
+ * MOBA_ERR_BAD_INDICES. Page table entries behind a request's length are
+ * not read. */
+typedef struct {
+  int num_pages;
+  int page_size;   /* a power of two, 16 .. 65536 */
+  int max_pages;   /* entries of a request's row of page_table */
+  void* k;         /* e4m3 [num_pages][Hkv][page_size][d] */
+  void* v;
+  void* k_scale;   /* e8m0 [num_pages][Hkv][page_size] */
+  void* v_scale;
+  const int32_t* page_table; /* device [batch][max_pages] */
+  const int32_t* seqlens;    /* device [batch] */
+} moba_cache;
+
+/* Quantises the new rows k, v [total_tokens][Hkv][d] (p->dtype) into the
+ * cache. kbar, if not NULL (fp32 [batch][moba_num_blocks(p)][Hkv][d]): the
+ * mean of every block that these rows complete, over the rows as the cache
+ * holds them (what a decode query of a later position scores); other entries
+ * are left alone. cu_new: device int32 [batch + 1]. */
+MOBA_API moba_status moba_cache_write(const moba_params* p, const moba_cache* c, const void* k,
+                                      const void* v, const int32_t* cu_new, float* kbar,
+                                      void* stream);
+
+/* Reads each request's last cu_rows[r+1] - cu_rows[r] positions back into
+ * k, v [total_tokens][Hkv][d] (p->dtype). cu_rows: device int32 [batch + 1]. */
+MOBA_API moba_status moba_cache_read(const moba_params* p, const moba_cache* c,
+                                     const int32_t* cu_rows, void* k, void* v, void* stream);
+
+/* moba_decode over the 8-bit cache: gate on kbar (fp32
+ * [batch][moba_num_blocks(p)][Hkv][d], kept by moba_cache_write; only complete
+ * blocks before each query's own block are read, and one whose score is NaN
+ * is not chosen), then one softmax over the chosen blocks' keys, causal in
+ * the own block. q, out [total_tokens][Hq][d] (p->dtype); lse fp32
+ * [total_tokens][Hq] or NULL; idx int32 [total_tokens][Hq][k] or NULL;
+ * cu_q: device int32 [batch + 1]; p->own_block must be 0.
+ * ws: moba_decode_cache_workspace_size(p) bytes, 32-byte aligned. */
+MOBA_API size_t moba_decode_cache_workspace_size(const moba_params* p);
+MOBA_API moba_status moba_decode_cache(const moba_params* p, const void* q, const moba_cache* c,
+                                       const int32_t* cu_q, const float* kbar, void* out,
+                                       float* lse, int32_t* idx, void* ws, size_t ws_bytes,
+                                       void* stream);
+
 /* Synchronises `stream`, returns the device status word of the current
  * device (MOBA_OK, MOBA_ERR_TIMEOUT, MOBA_ERR_BAD_INDICES, MOBA_ERR_INVALID_ARG
  * for a sequence longer than max_seqlen, or in the checked build

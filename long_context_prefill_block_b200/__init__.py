@@ -7,8 +7,9 @@ run if the compiled library is missing; there is no fallback of any kind.
 Functions mirror the C ABI of include/moba.h:
     moba_meanpool, moba_meanpool_update, moba_gate_topk, moba_gate_topk_noalloc,
     moba_forward, moba_forward_with_indices, moba_backward, moba_decode,
-    dense_causal_forward, moba_workspace_size, moba_num_blocks, moba_device_status,
-    moba_selftest_bounded_wait.
+    dense_causal_forward, dense_causal_backward, moba_cache_write, moba_cache_read,
+    moba_decode_cache (on a MobaCache, made by moba_cache_alloc), moba_workspace_size,
+    moba_num_blocks, moba_device_status, moba_selftest_bounded_wait.
 Shapes, element types, devices and (when it is on the host) cu_seqlens are
 checked here before the call: the C ABI takes them on trust, and a mismatch
 would make a kernel read or write past a buffer.
@@ -17,7 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -120,6 +121,10 @@ def make_params(q: torch.Tensor, k: torch.Tensor, cu_seqlens: torch.Tensor, bloc
 
 def _ptr(x: Optional[torch.Tensor]):
     return None if x is None else ctypes.c_void_p(x.data_ptr())
+
+
+def _nbytes(x: torch.Tensor) -> int:
+    return x.numel() * x.element_size()
 
 
 def _stream(device) -> ctypes.c_void_p:
@@ -426,6 +431,218 @@ def dense_causal_forward(q, k, v, cu_seqlens, max_seqlen=None, return_lse: bool 
            lib().dense_causal_forward(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(cu),
                                       _ptr(out), _ptr(lse), _stream(q.device)))
     return (out, lse) if return_lse else out
+
+
+def dense_causal_backward(q, k, v, cu_seqlens, out, lse, dout, max_seqlen=None,
+                          ws: Optional[torch.Tensor] = None):
+    """Gradients of sum(dout * out) through dense causal attention: (dq [T,Hq,d], dk, dv
+    [T,Hkv,d]) in the inputs' type, summed in fp32 and rounded once. out, lse: what
+    dense_causal_forward(..., return_lse=True) returned. Rows that no sequence owns get zeros.
+    The sums have a fixed order: equal calls give equal bits."""
+    _check_qkv(q, k, v, out)
+    _check_cu(cu_seqlens, q.shape[0])
+    if dout.shape != q.shape or dout.dtype != q.dtype:
+        raise ValueError(f"dout must be {tuple(q.shape)} {q.dtype}")
+    if lse.shape != q.shape[:2] or lse.dtype != torch.float32:
+        raise ValueError(f"lse must be float32 {tuple(q.shape[:2])}")
+    _check_inputs(q, k, v, out, dout, lse, ws)
+    L = lib()
+    p = make_params(q, k, cu_seqlens, 128, 1, max_seqlen)
+    cu = _dev_i32(cu_seqlens, q.device)
+    size = L.dense_causal_backward_workspace_size
+    size.argtypes, size.restype = [ctypes.POINTER(MobaParams)], ctypes.c_size_t
+    if ws is None:
+        ws = torch.empty(max(int(size(ctypes.byref(p))), 256), dtype=torch.uint8, device=q.device)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    fn = L.dense_causal_backward
+    fn.argtypes = [ctypes.POINTER(MobaParams)] + [ctypes.c_void_p] * 11 + [ctypes.c_size_t,
+                                                                         ctypes.c_void_p]
+    fn.restype = ctypes.c_int
+    with torch.cuda.device(q.device):
+        _check("dense_causal_backward",
+               fn(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(cu), _ptr(out), _ptr(lse),
+                  _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), _nbytes(ws),
+                  _stream(q.device)))
+    return dq, dk, dv
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("max_pages", ctypes.c_int)] + [(n, ctypes.c_void_p) for n in
+                                                ("k", "v", "k_scale", "v_scale", "page_table",
+                                                 "seqlens")]
+
+
+class MobaCache(NamedTuple):
+    """A paged KV cache in 8 bits: codes float8_e4m3fn [pages, Hkv, page_size, d] and one
+    power-of-two scale float8_e8m0fnu [pages, Hkv, page_size] for each row, for K and for V."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def moba_cache_alloc(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
+                     device="cuda") -> MobaCache:
+    """An empty MobaCache (zeros). page_size: a power of two, 16 to 65536."""
+    if page_size < 16 or page_size > 65536 or page_size & (page_size - 1):
+        raise ValueError(f"page_size must be a power of two from 16 to 65536 (got {page_size})")
+    rows = (num_pages, num_kv_heads, page_size)
+    codes = [torch.zeros(rows + (head_dim,), dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.zeros(rows, dtype=torch.uint8, device=device) for _ in range(2)]
+    return MobaCache(*(c.view(torch.float8_e4m3fn) for c in codes),
+                     *(s.view(torch.float8_e8m0fnu) for s in scales))
+
+
+def _check_cache(cache, heads: int, head_dim: int, page_table, seqlens, cu, rows: int):
+    """Shapes, types and devices of a call on a cache; returns its C description."""
+    k, v, ks, vs = cache
+    if k.dim() != 4 or k.shape[1] != heads or k.shape[3] != head_dim or v.shape != k.shape:
+        raise ValueError(f"cache codes {tuple(k.shape)}, {tuple(v.shape)} must be "
+                         f"[pages, {heads}, page_size, {head_dim}]")
+    if k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
+        raise TypeError("cache codes must be float8_e4m3fn")
+    if ks.shape != k.shape[:3] or vs.shape != k.shape[:3]:
+        raise ValueError(f"cache scales must be {tuple(k.shape[:3])}")
+    if ks.dtype != torch.float8_e8m0fnu or vs.dtype != torch.float8_e8m0fnu:
+        raise TypeError("cache scales must be float8_e8m0fnu")
+    page = k.shape[2]
+    if page < 16 or page > 65536 or page & (page - 1):
+        raise ValueError(f"page_size must be a power of two from 16 to 65536 (got {page})")
+    if page_table.dim() != 2 or page_table.dtype != torch.int32:
+        raise ValueError("page_table must be int32 [batch, max_pages]")
+    batch = page_table.shape[0]
+    if seqlens.shape != (batch,) or seqlens.dtype != torch.int32:
+        raise ValueError(f"seqlens must be int32 [{batch}]")
+    if cu.shape != (batch + 1,) or cu.dtype != torch.int32:
+        raise ValueError(f"row offsets must be int32 [{batch + 1}]")
+    _check_inputs(k, v, ks, vs, page_table, seqlens, cu)
+    return _CacheStruct(k.shape[0], page, page_table.shape[1], k.data_ptr(), v.data_ptr(),
+                        ks.data_ptr(), vs.data_ptr(), page_table.data_ptr(), seqlens.data_ptr())
+
+
+def _cache_params(batch, rows, hq, hkv, d, dtype, block_size, topk, max_seqlen,
+                  shared_routing=False) -> MobaParams:
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {dtype}")
+    return MobaParams(batch, rows, max_seqlen, hq, hkv, d, block_size, topk,
+                      MOBA_BF16 if dtype == torch.bfloat16 else MOBA_F32,
+                      1 if shared_routing else 0, 0, 0)
+
+
+def _check_kbar(kbar, batch: int, heads: int, head_dim: int, block_size: int) -> int:
+    """Checks the block means of a cache; returns the longest length they have blocks for."""
+    if kbar.dim() != 4 or kbar.shape[0] != batch or kbar.shape[2:] != (heads, head_dim) or \
+            kbar.dtype != torch.float32:
+        raise ValueError(f"kbar must be float32 [{batch}, num_blocks, {heads}, {head_dim}]")
+    if block_size < 1:
+        raise ValueError("block_size must be at least 1")
+    return min(kbar.shape[1] * block_size, 2**31 - 1)
+
+
+def moba_cache_write(cache: MobaCache, k, v, page_table, seqlens, cu_new,
+                     kbar: Optional[torch.Tensor] = None, block_size: Optional[int] = None) -> None:
+    """Quantise new rows k, v [n, Hkv, d] into the cache: request r's rows cu_new[r] ..
+    cu_new[r+1]-1 go to its last positions (seqlens[r] counts them already) in the pages that
+    page_table [batch, max_pages] names; rows behind cu_new[batch] are ignored. With kbar
+    [batch, num_blocks, Hkv, d] and block_size, the means of the blocks that these rows complete
+    are written too. page_table, seqlens, cu_new: int32 on the cache's device."""
+    _check_qkv(k, k, v)
+    n, hkv, d = k.shape
+    c = _check_cache(cache, hkv, d, page_table, seqlens, cu_new, n)
+    _check_inputs(cache.k, k, v, kbar)
+    batch, longest, B = page_table.shape[0], 2**31 - 1, 1
+    if kbar is not None:
+        if block_size is None:
+            raise ValueError("kbar needs block_size")
+        B = int(block_size)
+        longest = _check_kbar(kbar, batch, hkv, d, B)
+    p = _cache_params(batch, n, hkv, hkv, d, k.dtype, B, 1, longest)
+    fn = lib().moba_cache_write
+    fn.argtypes = [ctypes.POINTER(MobaParams), ctypes.POINTER(_CacheStruct)] + [ctypes.c_void_p] * 5
+    fn.restype = ctypes.c_int
+    with torch.cuda.device(k.device):
+        _check("moba_cache_write", fn(ctypes.byref(p), ctypes.byref(c), _ptr(k), _ptr(v),
+                                      _ptr(cu_new), _ptr(kbar), _stream(k.device)))
+
+
+def moba_cache_read(cache: MobaCache, page_table, seqlens, cu_rows, total_rows: int,
+                    dtype=torch.bfloat16, k: Optional[torch.Tensor] = None,
+                    v: Optional[torch.Tensor] = None):
+    """The last cu_rows[r+1] - cu_rows[r] positions of each request, widened: k, v
+    [total_rows, Hkv, d] in `dtype`, into the given tensors or fresh ones. Rows that no request
+    owns are not written: given tensors keep them, fresh ones hold nothing defined there."""
+    if cache.k.dim() != 4:
+        raise ValueError("cache codes must be [pages, Hkv, page_size, d]")
+    hkv, d = cache.k.shape[1], cache.k.shape[3]
+    c = _check_cache(cache, hkv, d, page_table, seqlens, cu_rows, total_rows)
+    p = _cache_params(page_table.shape[0], total_rows, hkv, hkv, d, dtype, 1, 1, 2**31 - 1)
+    res = []
+    for x in (k, v):
+        if x is None:
+            x = torch.empty((total_rows, hkv, d), dtype=dtype, device=cache.k.device)
+        elif x.shape != (total_rows, hkv, d) or x.dtype != dtype:
+            raise ValueError(f"k and v must be {(total_rows, hkv, d)} {dtype}")
+        res.append(x)
+    _check_inputs(cache.k, *res)
+    fn = lib().moba_cache_read
+    fn.argtypes = [ctypes.POINTER(MobaParams), ctypes.POINTER(_CacheStruct)] + [ctypes.c_void_p] * 4
+    fn.restype = ctypes.c_int
+    with torch.cuda.device(cache.k.device):
+        _check("moba_cache_read", fn(ctypes.byref(p), ctypes.byref(c), _ptr(cu_rows), _ptr(res[0]),
+                                     _ptr(res[1]), _stream(cache.k.device)))
+    return tuple(res)
+
+
+def moba_decode_cache(q, cache: MobaCache, page_table, seqlens, cu_q, kbar, block_size: int,
+                      topk: int, max_seqlen: Optional[int] = None, shared_routing: bool = False,
+                      return_lse: bool = False, return_idx: bool = False,
+                      ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """moba_decode over a MobaCache: request r's queries (rows cu_q[r] .. cu_q[r+1]-1 of q
+    [n, Hq, d]) stand at its last positions; kbar [batch, num_blocks, Hkv, d]: the block means
+    that moba_cache_write keeps. max_seqlen, a bound on the lengths, must have kbar's number of
+    blocks. Rows behind cu_q[batch] are not written: a given out keeps them, fresh results hold
+    nothing defined there. Returns out [n, Hq, d] (and lse [n, Hq], idx [n, Hq, topk])."""
+    if q.dim() != 3 or cache.k.dim() != 4 or q.shape[2] != cache.k.shape[3]:
+        raise ValueError("q must be [n, Hq, d] with the cache's head dim")
+    n, hq, d = q.shape
+    hkv = cache.k.shape[1]
+    if hq % hkv != 0:
+        raise ValueError(f"{hq} q heads are not a multiple of {hkv} kv heads")
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype):
+        raise ValueError(f"out must be {tuple(q.shape)} {q.dtype}")
+    c = _check_cache(cache, hkv, d, page_table, seqlens, cu_q, n)
+    batch = page_table.shape[0]
+    longest = _check_kbar(kbar, batch, hkv, d, block_size)
+    if max_seqlen is None:
+        max_seqlen = longest
+    elif -(-max_seqlen // block_size) != kbar.shape[1]:
+        raise ValueError(f"max_seqlen {max_seqlen} has not the {kbar.shape[1]} blocks of kbar")
+    _check_inputs(q, cache.k, kbar, out, ws)
+    L = lib()
+    p = _cache_params(batch, n, hq, hkv, d, q.dtype, block_size, topk, max_seqlen, shared_routing)
+    size = L.moba_decode_cache_workspace_size
+    size.argtypes, size.restype = [ctypes.POINTER(MobaParams)], ctypes.c_size_t
+    if ws is None:
+        ws = torch.empty(max(int(size(ctypes.byref(p))), 256), dtype=torch.uint8, device=q.device)
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
+    idx = (torch.empty((n, hq, topk), dtype=torch.int32, device=q.device) if return_idx
+           else None)
+    fn, V = L.moba_decode_cache, ctypes.c_void_p
+    fn.argtypes = [ctypes.POINTER(MobaParams), V, ctypes.POINTER(_CacheStruct), V, V, V, V, V, V,
+                   ctypes.c_size_t, V]
+    fn.restype = ctypes.c_int
+    with torch.cuda.device(q.device):
+        _check("moba_decode_cache", fn(ctypes.byref(p), _ptr(q), ctypes.byref(c), _ptr(cu_q),
+                                       _ptr(kbar), _ptr(out), _ptr(lse), _ptr(idx), _ptr(ws),
+                                       _nbytes(ws), _stream(q.device)))
+    res = (out,)
+    if return_lse:
+        res += (lse,)
+    if return_idx:
+        res += (idx,)
+    return res[0] if len(res) == 1 else res
 
 
 def moba_selftest_bounded_wait(device=None) -> int:

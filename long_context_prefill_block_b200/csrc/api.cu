@@ -356,6 +356,50 @@ DecLayout plan_decode(const Dims& dm, int n_queries) {
   return L;
 }
 
+// Split partials (o, then lse), index rows and arrival counters of a decode
+// step on the 8-bit cache.
+DecLayout plan_decode_cache(const Dims& dm) {
+  DecLayout L{};
+  const size_t rows = decode_cache_partial_rows(dm);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  L.idx = take(sizeof(int32_t) * (size_t)dm.T * dm.Hq * dm.topk);
+  L.part_o = take(sizeof(float) * rows * dm.d);
+  L.part_lse = take(sizeof(float) * rows);
+  L.arrivals = take(sizeof(int) * (size_t)dm.T * dm.Hq);
+  L.total = off;
+  return L;
+}
+
+size_t dense_bwd_bytes(const Dims& dm) { return align256(sizeof(float) * 2 * (size_t)dm.T * dm.Hq); }
+
+// Checks a cache description and fills the kernels' view of it.
+moba_status check_cache(const moba_cache* c, Cache& v) {
+  if (!c) return MOBA_ERR_INVALID_ARG;
+  if (c->num_pages <= 0 || c->max_pages <= 0 || c->page_size < 16 || c->page_size > 65536 ||
+      (c->page_size & (c->page_size - 1)))
+    return MOBA_ERR_INVALID_ARG;
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->page_table || !c->seqlens)
+    return MOBA_ERR_INVALID_ARG;
+  if (!aligned32(c->k) || !aligned32(c->v) || !aligned32(c->k_scale) || !aligned32(c->v_scale))
+    return MOBA_ERR_INVALID_ARG;
+  v.k = static_cast<uint8_t*>(c->k);
+  v.v = static_cast<uint8_t*>(c->v);
+  v.ks = static_cast<uint8_t*>(c->k_scale);
+  v.vs = static_cast<uint8_t*>(c->v_scale);
+  v.table = c->page_table;
+  v.lens = c->seqlens;
+  v.pages = c->num_pages;
+  v.max_pages = c->max_pages;
+  v.page_log2 = 0;
+  while ((1 << v.page_log2) < c->page_size) ++v.page_log2;
+  return MOBA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -523,6 +567,105 @@ moba_status dense_causal_forward(const moba_params* p, const void* q, const void
   if (!status) return MOBA_ERR_CUDA;
   if (tc_supported(dm)) return cuda_status(launch_dense_tc(dm, q, k, v, cu_seqlens, out, lse, status, st));
   return cuda_status(launch_dense_simt(dm, q, k, v, cu_seqlens, out, lse, st));
+}
+
+size_t dense_causal_backward_workspace_size(const moba_params* p) {
+  Dims dm;
+  if (validate(p, dm) != MOBA_OK) return 0;
+  return dense_bwd_bytes(dm);
+}
+
+moba_status dense_causal_backward(const moba_params* p, const void* q, const void* k,
+                                  const void* v, const int32_t* cu_seqlens, const void* out,
+                                  const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  Dims dm;
+  moba_status s = validate(p, dm);
+  if (s != MOBA_OK) return s;
+  if (dm.kv_hm) return MOBA_ERR_UNSUPPORTED;
+  if (dm.T == 0 || dm.batch == 0) return MOBA_OK;
+  for (const void* x : {q, k, v, out, static_cast<const void*>(lse), dout,
+                        static_cast<const void*>(dq), static_cast<const void*>(dk),
+                        static_cast<const void*>(dv)})
+    if (!x || !aligned32(x)) return MOBA_ERR_INVALID_ARG;
+  if (!cu_seqlens) return MOBA_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < dense_bwd_bytes(dm) || !aligned32(ws)) return MOBA_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int* status = status_word();
+  if (!status) return MOBA_ERR_CUDA;
+  float* stat = static_cast<float*>(ws);
+  MOBA_TRY(launch_dense_bwd_stat(dm, out, dout, lse, cu_seqlens, stat, dq, dk, dv, st));
+  return cuda_status(
+      launch_dense_bwd_simt(dm, q, k, v, dout, stat, cu_seqlens, dq, dk, dv, status, st));
+}
+
+moba_status moba_cache_write(const moba_params* p, const moba_cache* c, const void* k,
+                             const void* v, const int32_t* cu_new, float* kbar, void* stream) {
+  Dims dm;
+  Cache cv;
+  moba_status s = validate(p, dm);
+  if (s != MOBA_OK) return s;
+  if (dm.T == 0 || dm.batch == 0) return MOBA_OK;
+  if ((s = check_cache(c, cv)) != MOBA_OK) return s;
+  if (!k || !v || !cu_new || !aligned32(k) || !aligned32(v) || (kbar && !aligned32(kbar)))
+    return MOBA_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int* status = status_word();
+  if (!status) return MOBA_ERR_CUDA;
+  MOBA_TRY(launch_cache_write(dm, cv, k, v, cu_new, status, st));
+  if (kbar) MOBA_TRY(launch_cache_means(dm, cv, cu_new, kbar, status, st));
+  return MOBA_OK;
+}
+
+moba_status moba_cache_read(const moba_params* p, const moba_cache* c, const int32_t* cu_rows,
+                            void* k, void* v, void* stream) {
+  Dims dm;
+  Cache cv;
+  moba_status s = validate(p, dm);
+  if (s != MOBA_OK) return s;
+  if (dm.T == 0 || dm.batch == 0) return MOBA_OK;
+  if ((s = check_cache(c, cv)) != MOBA_OK) return s;
+  if (!k || !v || !cu_rows || !aligned32(k) || !aligned32(v)) return MOBA_ERR_INVALID_ARG;
+  int* status = status_word();
+  if (!status) return MOBA_ERR_CUDA;
+  return cuda_status(
+      launch_cache_read(dm, cv, cu_rows, k, v, status, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moba_decode_cache_workspace_size(const moba_params* p) {
+  Dims dm;
+  if (validate(p, dm) != MOBA_OK) return 0;
+  return plan_decode_cache(dm).total;
+}
+
+moba_status moba_decode_cache(const moba_params* p, const void* q, const moba_cache* c,
+                              const int32_t* cu_q, const float* kbar, void* out, float* lse,
+                              int32_t* idx, void* ws, size_t ws_bytes, void* stream) {
+  Dims dm;
+  Cache cv;
+  moba_status s = validate(p, dm);
+  if (s != MOBA_OK) return s;
+  if (dm.prefix) return MOBA_ERR_UNSUPPORTED;
+  if (dm.T == 0 || dm.batch == 0) return MOBA_OK;
+  if ((s = check_cache(c, cv)) != MOBA_OK) return s;
+  if (!q || !cu_q || !kbar || !out || !aligned32(q) || !aligned32(kbar) || !aligned32(out))
+    return MOBA_ERR_INVALID_ARG;
+  const DecLayout L = plan_decode_cache(dm);
+  if (!ws || ws_bytes < L.total || !aligned32(ws)) return MOBA_ERR_WORKSPACE;
+  int* status = status_word();
+  if (!status) return MOBA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* base = static_cast<char*>(ws);
+  int32_t* rows = idx ? idx : reinterpret_cast<int32_t*>(base + L.idx);
+  int* arrivals = reinterpret_cast<int*>(base + L.arrivals);
+  // a request longer than its pages hold is skipped by the gate too
+  const int64_t held = (int64_t)cv.max_pages << cv.page_log2;
+  if (held < dm.max_seqlen) dm.max_seqlen = (int)held;  // dm.nb keeps kbar's layout
+  MOBA_TRY(launch_cache_gate(dm, q, kbar, cv.lens, cu_q, rows, arrivals, status, st));
+  return cuda_status(launch_cache_attn(dm, cv, q, cu_q, rows,
+                                       reinterpret_cast<float*>(base + L.part_o),
+                                       reinterpret_cast<float*>(base + L.part_lse), arrivals, out,
+                                       lse, status, st));
 }
 
 moba_status moba_device_status(void* stream, int clear) {

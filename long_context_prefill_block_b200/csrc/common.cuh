@@ -137,6 +137,62 @@ __device__ __forceinline__ bool seq_bounds(const Dims& dm, const int32_t* cu, in
   return true;
 }
 
+// Largest r in [0, batch] with cu[r] <= i (cu: batch + 1 rising offsets).
+__device__ __forceinline__ int find_request(const int32_t* __restrict__ cu, int batch, int i) {
+  int lo = 0, hi = batch;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Request r and cache position of row i of a call on a paged cache: request
+// r's rows cu[r] .. cu[r+1]-1 stand at the last positions of its seqlens[r].
+// False for a row that no request owns (a padded batch), and, with a status
+// code, for a request whose length does not hold its rows or passes max_len.
+__device__ __forceinline__ bool tail_position(const int32_t* __restrict__ cu,
+                                              const int32_t* __restrict__ seqlens, int batch,
+                                              int max_len, int i, int& r, int& pos, int& len,
+                                              int* status) {
+  r = find_request(cu, batch, i);
+  if (r >= batch || i < cu[r]) return false;
+  const int n = cu[r + 1] - cu[r];
+  len = seqlens[r];
+  if (len < n || len > max_len) {
+    set_status(status, kStInvalidArg);
+    return false;
+  }
+  pos = len - n + (i - cu[r]);
+  return true;
+}
+
+// A paged 8-bit cache: codes [pages][Hkv][page][d] in e4m3 and one scale
+// byte (e8m0: 2^(byte - 127), 255 = NaN) per row [pages][Hkv][page], for K
+// and for V. Request r's position p is in page table[r][p / page].
+struct Cache {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* ks;
+  uint8_t* vs;
+  const int32_t* table;  // [batch][max_pages]
+  const int32_t* lens;   // [batch]
+  int pages, page_log2, max_pages;
+};
+
+// Row index of page slot `page` (an entry of the table) for kv head g, or -1
+// for an entry that names no page.
+__device__ __forceinline__ int64_t cache_page_row(const Cache& c, int Hkv, int page, int g) {
+  if (page < 0 || page >= c.pages) return -1;
+  return ((int64_t)page * Hkv + g) << c.page_log2;
+}
+
+// The value of a scale byte.
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
+}
+
 }  // namespace moba
 
 // ---- launchers (host), one per kernel family -------------------------------
@@ -253,6 +309,33 @@ cudaError_t launch_backward_tc(const Dims& dm, const Chunk& ch, const void* q, c
                                const Regroup& rg, float* dq, float* dk, float* dv, int* status,
                                cudaStream_t st);
 constexpr int kSimtTileM = 32;
+
+// Gradient of dense causal attention. stat: 2 * Hq * T floats of scratch,
+// filled by launch_dense_bwd_stat, which also zeroes the gradients of rows
+// that no sequence owns; the gradients have the inputs' type.
+cudaError_t launch_dense_bwd_stat(const Dims& dm, const void* out, const void* dout,
+                                  const float* lse, const int32_t* cu, float* stat, void* dq,
+                                  void* dk, void* dv, cudaStream_t st);
+cudaError_t launch_dense_bwd_simt(const Dims& dm, const void* q, const void* k, const void* v,
+                                  const void* dout, const float* stat, const int32_t* cu, void* dq,
+                                  void* dk, void* dv, int* status, cudaStream_t st);
+
+// Paged 8-bit cache (cache.cu, decode_cache.cu); dm.T: the call's rows.
+cudaError_t launch_cache_write(const Dims& dm, const Cache& c, const void* k, const void* v,
+                               const int32_t* cu_new, int* status, cudaStream_t st);
+// Means of the blocks that the new rows complete.
+cudaError_t launch_cache_means(const Dims& dm, const Cache& c, const int32_t* cu_new, float* kbar,
+                               int* status, cudaStream_t st);
+cudaError_t launch_cache_read(const Dims& dm, const Cache& c, const int32_t* cu_rows, void* k,
+                              void* v, int* status, cudaStream_t st);
+// The decode gate with cache lengths in place of packed offsets (decode.cu).
+cudaError_t launch_cache_gate(const Dims& dm, const void* q, const float* kbar,
+                              const int32_t* seqlens, const int32_t* cu_q, int32_t* idx,
+                              int* arrivals, int* status, cudaStream_t st);
+size_t decode_cache_partial_rows(const Dims& dm);
+cudaError_t launch_cache_attn(const Dims& dm, const Cache& c, const void* q, const int32_t* cu_q,
+                              const int32_t* idx, float* part_o, float* part_lse, int* arrivals,
+                              void* out, float* lse, int* status, cudaStream_t st);
 
 cudaError_t launch_merge(const Dims& dm, const Chunk& ch, const int32_t* idx, const int32_t* cu,
                          const Partials& pt, void* out, float* lse, cudaStream_t st);

@@ -63,13 +63,7 @@ __device__ __forceinline__ void insert(float (&ts)[KM], int (&ti)[KM], float s, 
 __device__ __forceinline__ bool decode_position(const Dims& dm, const int32_t* __restrict__ cu,
                                                 const int32_t* __restrict__ cu_q, int qi, int& r,
                                                 int64_t& start, int& len, int& p, int* status) {
-  int lo = 0, hi = dm.batch;  // largest r with cu_q[r] <= qi
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu_q[mid] <= qi) lo = mid;
-    else hi = mid - 1;
-  }
-  r = lo;
+  r = find_request(cu_q, dm.batch, qi);
   const int n = r < dm.batch ? cu_q[r + 1] - cu_q[r] : 0;
   if (r >= dm.batch || qi >= cu_q[r + 1] || !seq_bounds(dm, cu, r, start, len, status) || n > len) {
     set_status(status, kStInvalidArg);
@@ -79,7 +73,9 @@ __device__ __forceinline__ bool decode_position(const Dims& dm, const int32_t* _
   return true;
 }
 
-template <typename T, int D, int KM>
+// kPaged: cu holds the requests' cache lengths [batch] (a paged cache) and
+// rows behind the last request are left alone; else the packed cache's offsets.
+template <typename T, int D, int KM, bool kPaged>
 __global__ void __launch_bounds__(kGateWarps * 32)
 decode_gate_kernel(Dims dm, const T* __restrict__ q, const float* __restrict__ kbar,
                    const int32_t* __restrict__ cu, const int32_t* __restrict__ cu_q,
@@ -91,8 +87,12 @@ decode_gate_kernel(Dims dm, const T* __restrict__ q, const float* __restrict__ k
   const int H = dm.shared ? dm.Hkv : dm.Hq;  // routing units per query
   const int qi = blockIdx.x / H, u = blockIdx.x % H;
   int r, len, p;
-  int64_t start;
-  if (!decode_position(dm, cu, cu_q, qi, r, start, len, p, status)) return;  // whole CTA
+  if constexpr (kPaged) {  // whole CTA
+    if (!tail_position(cu_q, cu, dm.batch, dm.max_seqlen, qi, r, p, len, status)) return;
+  } else {
+    int64_t start;
+    if (!decode_position(dm, cu, cu_q, qi, r, start, len, p, status)) return;
+  }
   const int grp = dm.Hq / dm.Hkv;
   const int g = dm.shared ? u : u / grp;
   const int h0 = dm.shared ? u * grp : u, nh = dm.shared ? grp : 1;
@@ -225,8 +225,14 @@ decode_gate_kernel(Dims dm, const T* __restrict__ q, const float* __restrict__ k
   }
   if (lane != 0) return;
   int sel[KM];
+  int chosen = hsel;
 #pragma unroll
   for (int j = 0; j < KM; ++j) sel[j] = j < hsel ? fi[j] : INT_MAX;
+  if constexpr (kPaged) {  // a block whose score is NaN was never inserted
+    chosen = 0;
+#pragma unroll
+    for (int j = 0; j < KM; ++j) chosen += sel[j] != INT_MAX;
+  }
 #pragma unroll
   for (int a = 0; a < KM; ++a)
 #pragma unroll
@@ -240,7 +246,7 @@ decode_gate_kernel(Dims dm, const T* __restrict__ q, const float* __restrict__ k
     int32_t* row = idx + ((int64_t)qi * dm.Hq + h0 + j) * dm.topk;
 #pragma unroll
     for (int rr = 0; rr <= KM; ++rr)
-      if (rr < dm.topk) row[rr] = rr < hsel ? sel[rr < KM ? rr : KM - 1] : (rr == hsel ? c : -1);
+      if (rr < dm.topk) row[rr] = rr < chosen ? sel[rr < KM ? rr : KM - 1] : (rr == chosen ? c : -1);
   }
 }
 
@@ -464,15 +470,28 @@ decode_attn_kernel(Dims dm, const T* __restrict__ q, const T* __restrict__ k,
   }
 }
 
-template <typename T, int D, int KM>
-cudaError_t run_gate(const Dims& dm, int nq, const void* q, const float* kbar, const int32_t* cu,
+template <typename T, int D, int KM, bool kPaged>
+cudaError_t run_gate_km(const Dims& dm, int nq, const void* q, const float* kbar, const int32_t* cu,
                      const int32_t* cu_q, int32_t* idx, int* arrivals, int* status,
                      cudaStream_t st) {
   const int64_t items = (int64_t)nq * (dm.shared ? dm.Hkv : dm.Hq);
   if (items > INT32_MAX) return cudaErrorInvalidValue;
-  decode_gate_kernel<T, D, KM><<<(unsigned)items, kGateWarps * 32, 0, st>>>(
+  decode_gate_kernel<T, D, KM, kPaged><<<(unsigned)items, kGateWarps * 32, 0, st>>>(
       dm, static_cast<const T*>(q), kbar, cu, cu_q, idx, arrivals, status);
   return cudaGetLastError();
+}
+
+template <typename T, int D, bool kPaged>
+cudaError_t run_gate(const Dims& dm, int nq, const void* q, const float* kbar, const int32_t* cu,
+                     const int32_t* cu_q, int32_t* idx, int* arrivals, int* status,
+                     cudaStream_t st) {
+  const int need = dm.topk - 1;
+  if (need <= 1) return run_gate_km<T, D, 1, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
+  if (need <= 2) return run_gate_km<T, D, 2, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
+  if (need <= 4) return run_gate_km<T, D, 4, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
+  if (need <= 8) return run_gate_km<T, D, 8, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
+  if (need <= 16) return run_gate_km<T, D, 16, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
+  return run_gate_km<T, D, 32, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
 }
 
 template <typename T, int D>
@@ -480,14 +499,7 @@ cudaError_t run(const Dims& dm, int nq, const void* q, const void* k, const void
                 const int32_t* cu, const int32_t* cu_q, const float* kbar, int32_t* idx,
                 float* part_o, float* part_lse, int* arrivals, void* out, float* lse, int* status,
                 cudaStream_t st) {
-  cudaError_t e;
-  const int need = dm.topk - 1;
-  if (need <= 1) e = run_gate<T, D, 1>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
-  else if (need <= 2) e = run_gate<T, D, 2>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
-  else if (need <= 4) e = run_gate<T, D, 4>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
-  else if (need <= 8) e = run_gate<T, D, 8>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
-  else if (need <= 16) e = run_gate<T, D, 16>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
-  else e = run_gate<T, D, 32>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
+  cudaError_t e = run_gate<T, D, false>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
   if (e != cudaSuccess) return e;
   if ((int64_t)splits_per_row(dm) * nq > INT32_MAX) return cudaErrorInvalidValue;
   dim3 grid((unsigned)(splits_per_row(dm) * nq), (unsigned)dm.Hq);
@@ -498,6 +510,19 @@ cudaError_t run(const Dims& dm, int nq, const void* q, const void* k, const void
 }
 
 }  // namespace
+
+cudaError_t launch_cache_gate(const Dims& dm, const void* q, const float* kbar,
+                              const int32_t* seqlens, const int32_t* cu_q, int32_t* idx,
+                              int* arrivals, int* status, cudaStream_t st) {
+  if (dm.dtype == kBF16)
+    return dm.d == 128 ? run_gate<__nv_bfloat16, 128, true>(dm, dm.T, q, kbar, seqlens, cu_q, idx,
+                                                            arrivals, status, st)
+                       : run_gate<__nv_bfloat16, 64, true>(dm, dm.T, q, kbar, seqlens, cu_q, idx,
+                                                           arrivals, status, st);
+  return dm.d == 128
+             ? run_gate<float, 128, true>(dm, dm.T, q, kbar, seqlens, cu_q, idx, arrivals, status, st)
+             : run_gate<float, 64, true>(dm, dm.T, q, kbar, seqlens, cu_q, idx, arrivals, status, st);
+}
 
 size_t decode_partial_rows(const Dims& dm, int n_queries) {
   return (size_t)n_queries * dm.Hq * splits_per_row(dm);

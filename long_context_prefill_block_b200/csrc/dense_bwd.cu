@@ -1,0 +1,410 @@
+// Gradient of dense causal attention (PaperTrace "2.1.3 MoBA", section 1
+// eq. (1) with a causal mask; the layers of a hybrid stack that keep full
+// attention). With logits s_ij = q_i . k_j / sqrt(d) over j <= i of one
+// sequence and the forward's lse_i, out_i:
+//   P_ij = exp(s_ij - lse_i)          (recomputed, never stored)
+//   D_i  = dO_i . out_i,  dS_ij = P_ij (dO_i . v_j - D_i)
+//   dq_i = sum_j dS_ij k_j / sqrt(d),  dk_j = sum_i dS_ij q_i / sqrt(d),
+//   dv_j = sum_i P_ij dO_i            (i over every q head of the kv head)
+//
+// Two passes over the tiles, one that owns keys (dk, dv) and one that owns
+// queries (dq). Each result row is summed by one CTA in a fixed order, so
+// equal calls give equal bits and nothing is added atomically; the price is
+// seven products per tile instead of five (S and dO V^T are formed twice).
+//
+// This file: the row statistics both passes read, and the passes for fp32
+// inputs in fp32 FMA. bf16 inputs take dense_bwd_tc.cu.
+#include "common.cuh"
+
+namespace moba {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int BR = 64;  // queries per tile
+constexpr int BK = 64;  // keys per tile
+constexpr int LP = BK + 4;
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// stat[0][h][t] = lse * log2(e), stat[1][h][t] = D = dO . out, laid out head
+// by head so that a tile of one head's queries reads contiguous floats. Also
+// writes the gradients of rows that no sequence owns (t >= cu[batch]): zero.
+// One CTA: 32 tokens of one head; 16 bytes of a row per lane.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+dense_bwd_stat_kernel(Dims dm, const T* __restrict__ out, const T* __restrict__ dout,
+                      const float* __restrict__ lse, const int32_t* __restrict__ cu,
+                      float* __restrict__ stat, T* __restrict__ dq, T* __restrict__ dk,
+                      T* __restrict__ dv) {
+  constexpr int VEC = Vec16<T>::N, LPR = D / VEC, RPS = kThreads / LPR;  // rows per step
+  __shared__ float ds[32];
+  const int h = blockIdx.y, t0 = blockIdx.x * 32;
+  const int sub = threadIdx.x % LPR, rr = threadIdx.x / LPR;
+  for (int r = rr; r < 32; r += RPS) {
+    const int t = t0 + r;
+    float acc = 0.f;
+    if (t < dm.T) {
+      const int64_t at = ((int64_t)t * dm.Hq + h) * D + sub * VEC;
+      float a[VEC], b[VEC];
+      Vec16<T>::load(out + at, a);
+      Vec16<T>::load(dout + at, b);
+#pragma unroll
+      for (int x = 0; x < VEC; ++x) acc = fmaf(a[x], b[x], acc);
+    }
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+    if (sub == 0) ds[r] = acc;
+  }
+  __syncthreads();
+  const int t = t0 + threadIdx.x;
+  if (threadIdx.x < 32 && t < dm.T) {
+    stat[(int64_t)h * dm.T + t] = lse[(int64_t)t * dm.Hq + h] * kLog2e;
+    stat[((int64_t)dm.Hq + h) * dm.T + t] = ds[threadIdx.x];
+  }
+  const int end = min(max(cu[dm.batch], 0), dm.T);
+  if (t0 + 32 > end) {
+    const T zero = from_f32<T>(0.f);
+    for (int e = threadIdx.x; e < 32 * D; e += kThreads) {
+      const int64_t row = t0 + e / D;
+      if (row < end || row >= dm.T) continue;
+      dq[(row * dm.Hq + h) * D + e % D] = zero;
+      if (h < dm.Hkv) {
+        dk[(row * dm.Hkv + h) * D + e % D] = zero;
+        dv[(row * dm.Hkv + h) * D + e % D] = zero;
+      }
+    }
+  }
+}
+
+template <typename T>
+struct Args {
+  Dims dm;
+  const T* q;
+  const T* k;
+  const T* v;
+  const T* dout;
+  const float* stat;
+  const int32_t* cu;
+  T* dq;
+  T* dk;
+  T* dv;
+  int* status;
+};
+
+// CTA x of a grid of tiles x batch x heads, tile-major: the tiles with the
+// most work come first when the tile index grows with falling work.
+struct Place {
+  int tile, b, h;
+};
+__device__ __forceinline__ Place place(int batch, int heads) {
+  const int x = blockIdx.x;
+  return {x / (batch * heads), x / heads % batch, x % heads};
+}
+
+// 64 rows of one head (row stride in elements) into shared memory, rows at
+// or past n as zeros.
+template <typename T, int D>
+__device__ __forceinline__ void load_tile(float (*dst)[D + 4], const T* src, int64_t stride,
+                                          int n) {
+  constexpr int VEC = Vec16<T>::N, TPR = D / VEC;
+  for (int e = threadIdx.x; e < 64 * TPR; e += kThreads) {
+    const int r = e / TPR, c = e % TPR;
+    float x[VEC];
+#pragma unroll
+    for (int u = 0; u < VEC; ++u) x[u] = 0.f;
+    if (r < n) Vec16<T>::load(src + r * stride + c * VEC, x);
+#pragma unroll
+    for (int u = 0; u < VEC; u += 4)
+      *reinterpret_cast<float4*>(&dst[r][c * VEC + u]) = make_float4(x[u], x[u + 1], x[u + 2], x[u + 3]);
+  }
+}
+
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d) {
+  __nv_bfloat162 v[2] = {__floats2bfloat162_rn(a, b), __floats2bfloat162_rn(c, d)};
+  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(v);
+}
+
+template <int D>
+struct Smem {
+  float K[BK][D + 4], V[BK][D + 4], Q[BR][D + 4], O[BR][D + 4];
+  float P[BR][LP], S[BK][LP];  // P [query][key]; dS [query][key], or [key][query] for dq
+  float lse2[BR], D_[BR];
+};
+
+// P and dS of the 64 x 64 tile of queries q0.. and keys k0.. (positions in a
+// sequence of length len) into shared memory. Thread (ty, tx): queries
+// ty * 4 .. + 3, keys tx + 16 u: rows are read 16 bytes at a time along d and
+// the padded stride puts 8 consecutive key rows into distinct bank groups.
+template <int D, bool kTransposed>
+__device__ __forceinline__ void tile_ps(Smem<D>& sm, int q0, int k0, int len) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float s[4][4], dp[4][4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) s[a][b] = dp[a][b] = 0.f;
+#pragma unroll 2
+  for (int x = 0; x < D; x += 4) {
+    float4 q4[4], o4[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      q4[a] = *reinterpret_cast<const float4*>(&sm.Q[ty * 4 + a][x]);
+      o4[a] = *reinterpret_cast<const float4*>(&sm.O[ty * 4 + a][x]);
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const float4 k4 = *reinterpret_cast<const float4*>(&sm.K[tx + 16 * b][x]);
+      const float4 v4 = *reinterpret_cast<const float4*>(&sm.V[tx + 16 * b][x]);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        s[a][b] = fmaf(q4[a].x, k4.x, s[a][b]);
+        s[a][b] = fmaf(q4[a].y, k4.y, s[a][b]);
+        s[a][b] = fmaf(q4[a].z, k4.z, s[a][b]);
+        s[a][b] = fmaf(q4[a].w, k4.w, s[a][b]);
+        dp[a][b] = fmaf(o4[a].x, v4.x, dp[a][b]);
+        dp[a][b] = fmaf(o4[a].y, v4.y, dp[a][b]);
+        dp[a][b] = fmaf(o4[a].z, v4.z, dp[a][b]);
+        dp[a][b] = fmaf(o4[a].w, v4.w, dp[a][b]);
+      }
+    }
+  }
+  const float sl2 = rsqrtf((float)D) * kLog2e;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int qi = ty * 4 + a;
+    const float l2 = sm.lse2[qi], dd = sm.D_[qi];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int kj = tx + 16 * b;
+      // masked places get zeros by selection: whatever their rows hold
+      const bool vis = q0 + qi < len && k0 + kj <= q0 + qi;
+      const float p = vis ? exp2f(fmaf(s[a][b], sl2, -l2)) : 0.f;
+      const float ds = vis ? p * (dp[a][b] - dd) : 0.f;
+      if (kTransposed) {
+        sm.S[kj][qi] = ds;
+      } else {
+        sm.P[qi][kj] = p;
+        sm.S[qi][kj] = ds;
+      }
+    }
+  }
+}
+
+// Rows of the query tile: q, dO and the statistics.
+template <typename T, int D>
+__device__ __forceinline__ void load_queries(const Args<T>& a, Smem<D>& sm, int64_t start, int q0,
+                                             int len, int h) {
+  const int n = min(BR, len - q0);
+  const int64_t row = (start + q0) * a.dm.Hq + h;
+  load_tile<T, D>(sm.Q, a.q + row * D, (int64_t)a.dm.Hq * D, n);
+  load_tile<T, D>(sm.O, a.dout + row * D, (int64_t)a.dm.Hq * D, n);
+  if (threadIdx.x < BR) {
+    const int r = threadIdx.x;
+    const float* st = a.stat + (int64_t)h * a.dm.T + start + q0 + r;
+    sm.lse2[r] = r < n ? st[0] : 0.f;
+    sm.D_[r] = r < n ? st[(int64_t)a.dm.Hq * a.dm.T] : 0.f;
+  }
+}
+
+// dk, dv of 64 keys of one kv head: every later query tile of every q head
+// of the group. Bound by the fp32 FMA rate (shared-memory reads are 6 of
+// every 8 issue slots' wavefronts).
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) dense_bwd_kv_kernel(const Args<T> a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
+  const Dims& dm = a.dm;
+  const Place pl = place(dm.batch, dm.Hkv);
+  const int g = pl.h, b = pl.b;
+  int64_t start;
+  int len;
+  if (!seq_bounds(dm, a.cu, b, start, len, a.status) || !MOBA_CHECK(start + len <= dm.T, a.status))
+    return;
+  const int k0 = pl.tile * BK;
+  if (k0 >= len) return;
+  const int nk = min(BK, len - k0);
+  const int64_t krow = (start + k0) * dm.Hkv + g;
+  load_tile<T, D>(sm.K, a.k + krow * D, (int64_t)dm.Hkv * D, nk);
+  load_tile<T, D>(sm.V, a.v + krow * D, (int64_t)dm.Hkv * D, nk);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // keys ty * 4 .., dims tx * 4 + 64 w
+  constexpr int NW = D / 64;
+  float dk[4][4 * NW], dv[4][4 * NW];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int x = 0; x < 4 * NW; ++x) dk[i][x] = dv[i][x] = 0.f;
+  const int grp = dm.Hq / dm.Hkv;
+  for (int h = g * grp; h < (g + 1) * grp; ++h) {
+    for (int q0 = k0; q0 < len; q0 += BR) {
+      __syncthreads();
+      load_queries<T, D>(a, sm, start, q0, len, h);
+      __syncthreads();
+      tile_ps<D, false>(sm, q0, k0, len);
+      __syncthreads();
+#pragma unroll 2
+      for (int r = 0; r < BR; ++r) {
+        const float4 p4 = *reinterpret_cast<const float4*>(&sm.P[r][ty * 4]);
+        const float4 s4 = *reinterpret_cast<const float4*>(&sm.S[r][ty * 4]);
+        const float p[4] = {p4.x, p4.y, p4.z, p4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float4 o4 = *reinterpret_cast<const float4*>(&sm.O[r][tx * 4 + 64 * w]);
+          const float4 q4 = *reinterpret_cast<const float4*>(&sm.Q[r][tx * 4 + 64 * w]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dv[i][4 * w + 0] = fmaf(p[i], o4.x, dv[i][4 * w + 0]);
+            dv[i][4 * w + 1] = fmaf(p[i], o4.y, dv[i][4 * w + 1]);
+            dv[i][4 * w + 2] = fmaf(p[i], o4.z, dv[i][4 * w + 2]);
+            dv[i][4 * w + 3] = fmaf(p[i], o4.w, dv[i][4 * w + 3]);
+            dk[i][4 * w + 0] = fmaf(s[i], q4.x, dk[i][4 * w + 0]);
+            dk[i][4 * w + 1] = fmaf(s[i], q4.y, dk[i][4 * w + 1]);
+            dk[i][4 * w + 2] = fmaf(s[i], q4.z, dk[i][4 * w + 2]);
+            dk[i][4 * w + 3] = fmaf(s[i], q4.w, dk[i][4 * w + 3]);
+          }
+        }
+      }
+    }
+  }
+  const float scale = rsqrtf((float)D);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int kj = ty * 4 + i;
+    if (kj >= nk) continue;
+    const int64_t at = (krow + (int64_t)kj * dm.Hkv) * D + tx * 4;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      store4(a.dk + at + 64 * w, dk[i][4 * w] * scale, dk[i][4 * w + 1] * scale,
+             dk[i][4 * w + 2] * scale, dk[i][4 * w + 3] * scale);
+      store4(a.dv + at + 64 * w, dv[i][4 * w], dv[i][4 * w + 1], dv[i][4 * w + 2],
+             dv[i][4 * w + 3]);
+    }
+  }
+}
+
+// dq of 64 queries of one head: every key tile up to the diagonal. Blocks
+// are numbered last tile first, the longest work.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) dense_bwd_q_kernel(const Args<T> a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
+  const Dims& dm = a.dm;
+  const Place pl = place(dm.batch, dm.Hq);
+  const int h = pl.h, b = pl.b, g = h / (dm.Hq / dm.Hkv);
+  int64_t start;
+  int len;
+  if (!seq_bounds(dm, a.cu, b, start, len, a.status) || !MOBA_CHECK(start + len <= dm.T, a.status))
+    return;
+  const int q0 = ((dm.max_seqlen + BR - 1) / BR - 1 - pl.tile) * BR;
+  if (q0 >= len) return;
+  load_queries<T, D>(a, sm, start, q0, len, h);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // queries ty * 4 .., dims tx * 4 + 64 w
+  constexpr int NW = D / 64;
+  float dq[4][4 * NW];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int x = 0; x < 4 * NW; ++x) dq[i][x] = 0.f;
+  for (int k0 = 0; k0 <= q0; k0 += BK) {
+    const int64_t krow = (start + k0) * dm.Hkv + g;
+    __syncthreads();
+    load_tile<T, D>(sm.K, a.k + krow * D, (int64_t)dm.Hkv * D, min(BK, len - k0));
+    load_tile<T, D>(sm.V, a.v + krow * D, (int64_t)dm.Hkv * D, min(BK, len - k0));
+    __syncthreads();
+    tile_ps<D, true>(sm, q0, k0, len);
+    __syncthreads();
+#pragma unroll 2
+    for (int j = 0; j < BK; ++j) {
+      const float4 s4 = *reinterpret_cast<const float4*>(&sm.S[j][ty * 4]);
+      const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float4 k4 = *reinterpret_cast<const float4*>(&sm.K[j][tx * 4 + 64 * w]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dq[i][4 * w + 0] = fmaf(s[i], k4.x, dq[i][4 * w + 0]);
+          dq[i][4 * w + 1] = fmaf(s[i], k4.y, dq[i][4 * w + 1]);
+          dq[i][4 * w + 2] = fmaf(s[i], k4.z, dq[i][4 * w + 2]);
+          dq[i][4 * w + 3] = fmaf(s[i], k4.w, dq[i][4 * w + 3]);
+        }
+      }
+    }
+  }
+  const float scale = rsqrtf((float)D);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int qi = ty * 4 + i;
+    if (q0 + qi >= len) continue;
+    const int64_t at = ((start + q0 + qi) * dm.Hq + h) * D + tx * 4;
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+      store4(a.dq + at + 64 * w, dq[i][4 * w] * scale, dq[i][4 * w + 1] * scale,
+             dq[i][4 * w + 2] * scale, dq[i][4 * w + 3] * scale);
+  }
+}
+
+template <typename T, int D>
+cudaError_t run_stat(const Dims& dm, const void* out, const void* dout, const float* lse,
+                     const int32_t* cu, float* stat, void* dq, void* dk, void* dv,
+                     cudaStream_t st) {
+  dense_bwd_stat_kernel<T, D><<<dim3((unsigned)((dm.T + 31) / 32), (unsigned)dm.Hq), kThreads, 0,
+                                st>>>(dm, static_cast<const T*>(out), static_cast<const T*>(dout),
+                                      lse, cu, stat, static_cast<T*>(dq), static_cast<T*>(dk),
+                                      static_cast<T*>(dv));
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t run_simt(const Args<T>& a, cudaStream_t st) {
+  const Dims& dm = a.dm;
+  cudaError_t e;
+  constexpr int smem = (int)sizeof(Smem<D>);
+  if ((e = cudaFuncSetAttribute(dense_bwd_kv_kernel<T, D>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+    return e;
+  if ((e = cudaFuncSetAttribute(dense_bwd_q_kernel<T, D>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+    return e;
+  const int64_t nt = (int64_t)((dm.max_seqlen + BK - 1) / BK) * dm.batch;
+  if (nt * dm.Hq > INT32_MAX) return cudaErrorInvalidValue;
+  dense_bwd_kv_kernel<T, D><<<(unsigned)(nt * dm.Hkv), kThreads, smem, st>>>(a);
+  if ((e = cudaGetLastError())) return e;
+  dense_bwd_q_kernel<T, D><<<(unsigned)(nt * dm.Hq), kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t run_type(const Dims& dm, const void* q, const void* k, const void* v, const void* dout,
+                     const float* stat, const int32_t* cu, void* dq, void* dk, void* dv,
+                     int* status, cudaStream_t st) {
+  const Args<T> a{dm, static_cast<const T*>(q), static_cast<const T*>(k),
+                  static_cast<const T*>(v), static_cast<const T*>(dout), stat, cu,
+                  static_cast<T*>(dq), static_cast<T*>(dk), static_cast<T*>(dv), status};
+  return dm.d == 128 ? run_simt<T, 128>(a, st) : run_simt<T, 64>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_dense_bwd_stat(const Dims& dm, const void* out, const void* dout,
+                                  const float* lse, const int32_t* cu, float* stat, void* dq,
+                                  void* dk, void* dv, cudaStream_t st) {
+  if (dm.dtype == kBF16)
+    return dm.d == 128
+               ? run_stat<__nv_bfloat16, 128>(dm, out, dout, lse, cu, stat, dq, dk, dv, st)
+               : run_stat<__nv_bfloat16, 64>(dm, out, dout, lse, cu, stat, dq, dk, dv, st);
+  return dm.d == 128 ? run_stat<float, 128>(dm, out, dout, lse, cu, stat, dq, dk, dv, st)
+                     : run_stat<float, 64>(dm, out, dout, lse, cu, stat, dq, dk, dv, st);
+}
+
+cudaError_t launch_dense_bwd_simt(const Dims& dm, const void* q, const void* k, const void* v,
+                                  const void* dout, const float* stat, const int32_t* cu, void* dq,
+                                  void* dk, void* dv, int* status, cudaStream_t st) {
+  if (dm.batch == 0 || dm.max_seqlen == 0) return cudaSuccess;
+  if (dm.dtype == kBF16)
+    return run_type<__nv_bfloat16>(dm, q, k, v, dout, stat, cu, dq, dk, dv, status, st);
+  return run_type<float>(dm, q, k, v, dout, stat, cu, dq, dk, dv, status, st);
+}
+
+}  // namespace moba

@@ -1,0 +1,384 @@
+"""The paged 8-bit cache on the GPU: writing, block means, reading back and decoding over it,
+against 64-bit references on the same bits.
+
+Codes, scales and values read back are exact: one rounding, defined by the type. Block means are
+sums of B fp32 values: B * 2^-24 relative to their mean magnitude at worst. Decode, relative
+2-norm: a logit is off by at most 128 * 2^-24 * sum|q k| / sqrt(d) ~ 128 * 6e-8 * 3.6 = 2.8e-5, a
+weight by that relatively, and the sum over n <= 3000 keys by n * 2^-24 = 1.8e-4 at worst: 2.4e-4
+in fp32 (and absolutely for lse); bf16 queries: the weights may be rounded to 11 bits (2^-11) and
+the result is rounded once (2^-8): 2^-8 + 2^-11 + 2.4e-4 = 4.7e-3."""
+import pytest
+import torch
+
+import long_context_prefill_block_b200 as moba
+import reference64 as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TOL = {torch.float32: 2.4e-4, torch.bfloat16: 4.7e-3}
+LSE_TOL = 2.4e-4
+
+
+class Pool:
+    """A cache with shuffled pages, the table of `lens` (positions reserved per request)."""
+
+    def __init__(self, reserve, page, heads, d, seed=0, spare=2):
+        need = [-(-n // page) for n in reserve]
+        total = sum(need) + spare
+        g = torch.Generator().manual_seed(seed)
+        order = torch.randperm(total, generator=g)
+        self.table = torch.full((len(reserve), max(need + [1])), -1, dtype=torch.int32)
+        at = 0
+        for r, n in enumerate(need):
+            self.table[r, :n] = order[at:at + n].to(torch.int32)
+            at += n
+        self.table = self.table.to(DEV)
+        fill = torch.randint(0, 255, (2, total, heads, page, d + 1), generator=g, dtype=torch.uint8)
+        fill[fill == 127] = 0  # the two NaN codes
+        self.cache = moba.MobaCache(*(fill[i, ..., :d].contiguous().to(DEV).view(
+            torch.float8_e4m3fn) for i in range(2)), *(fill[i, ..., d].contiguous().to(DEV).view(
+                torch.float8_e8m0fnu) for i in range(2)))
+
+    def bits(self):
+        return [x.view(torch.uint8).cpu().clone() for x in self.cache]
+
+
+def offsets(n):
+    return torch.tensor([0] + list(torch.cumsum(torch.tensor(n), 0)), dtype=torch.int32, device=DEV)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def expected(pool, before, x, table, new, lens, which):
+    """The bits after writing rows x of K (which 0) or V (1), on the CPU."""
+    codes, scales = before[which].clone(), before[which + 2].clone()
+    c, e, fine = ref.quantise(x.cpu())
+    c = c.float().to(torch.float8_e4m3fn).view(torch.uint8)
+    page, i = codes.shape[2], 0
+    for r in range(len(new)):
+        for j in range(new[r]):
+            pos = lens[r] - new[r] + j
+            p = int(table[r, pos // page])
+            codes[p, :, pos % page] = c[i]
+            scales[p, :, pos % page] = torch.where(fine[i], e[i] + 127, 255).to(torch.uint8)
+            i += 1
+    return codes, scales
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("new,old,heads,d,page,B", [
+    ([1], [0], 1, 64, 16, 16), ([1, 1, 1], [15, 16, 31], 2, 128, 16, 16),
+    ([5, 0, 70, 1], [3, 9, 0, 99], 3, 64, 32, 20), ([300, 129], [0, 7], 2, 128, 64, 100),
+    ([257], [255], 8, 128, 128, 64)])
+def test_write_is_exact_and_touches_nothing_else(new, old, heads, d, page, B, dtype):
+    lens = [a + b for a, b in zip(new, old)]
+    pool = Pool(lens, page, heads, d, seed=len(new))
+    g = torch.Generator().manual_seed(4)
+    n = sum(new)
+    k, v = ((torch.randn(n, heads, d, generator=g) * torch.exp2(torch.randint(
+        -12, 12, (n, heads, 1), generator=g).float())).to(dtype).to(DEV) for _ in range(2))
+    k[0, 0] = 0
+    nb = -(-max(lens) // B)
+    kbar = torch.full((len(new), nb, heads, d), 7.0, device=DEV)
+    before = pool.bits()
+    moba.moba_cache_write(pool.cache, k, v, pool.table, i32(lens), offsets(new), kbar, B)
+    torch.cuda.synchronize()
+    assert moba.moba_device_status() == 0
+    after, table = pool.bits(), pool.table.cpu()
+    for w, x in enumerate((k, v)):
+        codes, scales = expected(pool, before, x, table, new, lens, w)
+        # -0 and 0 are one value: compare what the codes stand for, and untouched bytes as bytes
+        a, b = (t.view(torch.float8_e4m3fn).float() for t in (after[w], codes))
+        assert torch.equal(a, b)
+        same = codes == before[w]
+        assert torch.equal(after[w + 2], scales) and torch.equal(after[w][same], codes[same])
+    for r in range(len(new)):
+        rows = ref.cached_rows(pool.cache.k, pool.cache.k_scale, pool.table[r], lens[r])
+        for i in range(nb):
+            got = kbar[r, i].double().cpu()
+            if old[r] // B <= i < lens[r] // B and new[r]:
+                blk = rows[i * B:(i + 1) * B]
+                tol = B * 2.0 ** -24 * blk.abs().mean(dim=0) + 1e-30
+                # the old rows are drawn bytes: where a sum of their magnitudes passes 2^128 it
+                # is no 32-bit number, and the mean is not either
+                held = blk.abs().sum(dim=0) < 2.0 ** 128
+                assert held.any() and ((got - blk.mean(dim=0)).abs() <= tol)[held].all()
+            else:
+                assert (got == 7.0).all()
+
+
+def test_rows_at_the_ends_of_the_number_range():
+    """Largest, smallest, subnormal, infinite and NaN rows; reading back stays finite where the
+    input was, and NaN rows read back as NaN."""
+    big, tiny, inf, nan = 3.4028234663852886e38, 1e-45, float("inf"), float("nan")
+    rows = [[big, -big, 1.0], [big * 0.86, 2.0 ** 100, 0], [448.0, 447.9, 1e-3], [tiny, 0, -tiny],
+            [2.0 ** -126, 2.0 ** -120, 2.0 ** -140], [inf, 1, 2], [1, nan, 2], [-inf, nan, 0],
+            [1e-38, -2e-38, 3e-39], [0, 0, 0]]
+    x = torch.zeros(len(rows), 1, 64)
+    x[:, 0, :3] = torch.tensor(rows)
+    for dtype in (torch.float32, torch.bfloat16):
+        y = x.to(dtype)
+        if dtype == torch.bfloat16:
+            y[0] = torch.where(torch.isinf(y[0]), torch.finfo(dtype).max * torch.sign(y[0]), y[0])
+        pool = Pool([len(rows)], 16, 1, 64)
+        before = pool.bits()
+        yd = y.to(DEV)
+        moba.moba_cache_write(pool.cache, yd, yd, pool.table, i32([len(rows)]), offsets([len(rows)]))
+        codes, scales = expected(pool, before, y, pool.table.cpu(), [len(rows)], [len(rows)], 0)
+        after = pool.bits()
+        assert torch.equal(after[2], scales)
+        assert torch.equal(after[0].view(torch.float8_e4m3fn).float(),
+                           codes.view(torch.float8_e4m3fn).float())
+        k, v = moba.moba_cache_read(pool.cache, pool.table, i32([len(rows)]), offsets([len(rows)]),
+                                    len(rows), dtype=dtype)
+        want = ref.cached_rows(pool.cache.k, pool.cache.k_scale, pool.table[0], len(rows)).to(dtype)
+        assert torch.equal(k.cpu().isnan(), want.isnan()) and want[5:8].isnan().all()
+        assert torch.equal(torch.nan_to_num(k.cpu()), torch.nan_to_num(want))
+        assert torch.isfinite(k[:5]).all() and torch.equal(k.isnan(), v.isnan())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,lens,heads,d,page", [
+    ([1], [1], 1, 64, 16), ([0, 3, 40], [5, 33, 40], 2, 128, 16), ([200, 77], [300, 77], 4, 64, 64),
+    ([129], [1000], 3, 128, 128)])
+def test_read_is_exact_and_leaves_padding(rows, lens, heads, d, page, dtype):
+    pool = Pool(lens, page, heads, d, seed=3)
+    n = sum(rows)
+    k, v = (torch.full((n + 9, heads, d), 5.0, dtype=dtype, device=DEV) for _ in range(2))
+    a, b = moba.moba_cache_read(pool.cache, pool.table, i32(lens), offsets(rows), n + 9, dtype=dtype,
+                                k=k, v=v)
+    assert a is k and b is v and moba.moba_device_status() == 0
+    at = 0
+    for r, m in enumerate(rows):
+        for x, c, s in ((k, pool.cache.k, pool.cache.k_scale), (v, pool.cache.v, pool.cache.v_scale)):
+            want = ref.cached_rows(c, s, pool.table[r], lens[r])[lens[r] - m:].to(dtype)
+            assert torch.equal(x[at:at + m].cpu(), want)
+        at += m
+    assert (k[n:] == 5).all() and (v[n:] == 5).all()
+
+
+def filled(lens, heads, d, page, B, seed, room=0):
+    """A pool whose requests hold drawn rows with block offsets, its block means and the values."""
+    pool = Pool([n + room for n in lens], page, heads, d, seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    n = sum(lens)
+    k, v = (torch.randn(n, heads, d, generator=g) * 0.7 for _ in range(2))
+    at = 0
+    for L in lens:
+        off = torch.randn(L // B + 1, heads, d, generator=g) * 0.3
+        k[at:at + L] += off[torch.arange(L) // B]
+        at += L
+    nb = max(1, -(-(max(lens + [1]) + room) // B))
+    kbar = torch.zeros((len(lens), nb, heads, d), device=DEV)
+    if n:
+        moba.moba_cache_write(pool.cache, k.to(DEV), v.to(DEV), pool.table, i32(lens),
+                              offsets(lens), kbar, B)
+    return pool, kbar
+
+
+def contents(pool, r, length):
+    c = pool.cache
+    return (ref.cached_rows(c.k, c.k_scale, pool.table[r], length),
+            ref.cached_rows(c.v, c.v_scale, pool.table[r], length))
+
+
+def check_decode(q, pool, lens, nq, B, topk, shared, out, lse, idx):
+    at = 0
+    outs, lses, wants = [], [], []
+    for r in range(len(lens)):
+        if nq[r] == 0:
+            continue
+        keys, values = contents(pool, r, lens[r])
+        o, l, i = ref.decode(q[at:at + nq[r]].cpu(), keys, values, B, topk, shared)
+        outs.append(o), lses.append(l), wants.append(i)
+        at += nq[r]
+    assert torch.equal(idx[:at].cpu().long(), torch.cat(wants))
+    assert ref.off(out[:at], torch.cat(outs)) <= TOL[q.dtype]
+    assert (lse[:at].double().cpu() - torch.cat(lses)).abs().max() <= LSE_TOL
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens,nq,Hq,Hkv,d,page,B,topk", [
+    ([1], [1], 1, 1, 64, 16, 16, 1), ([1, 2, 17], [1, 2, 1], 2, 1, 128, 16, 16, 3),
+    ([100, 0, 257], [1, 0, 3], 4, 2, 64, 32, 20, 4), ([1500, 700], [1, 1], 8, 2, 128, 16, 128, 3),
+    ([3000], [4], 4, 4, 128, 64, 100, 12), ([2999, 1025], [2, 1], 10, 2, 128, 64, 1000, 2),
+    ([1300], [1], 16, 1, 64, 128, 600, 3), ([700], [1], 3, 3, 128, 64, 4096, 8),
+    ([640, 513], [5, 1], 12, 4, 128, 64, 64, 32)])
+def test_decode_matches_the_definition(lens, nq, Hq, Hkv, d, page, B, topk, dtype, shared):
+    pool, kbar = filled(lens, Hkv, d, page, B, seed=sum(lens))
+    g = torch.Generator().manual_seed(1)
+    n = sum(nq)
+    q = (torch.randn(n, Hq, d, generator=g) * 0.7).to(dtype).to(DEV)
+    out, lse, idx = moba.moba_decode_cache(q, pool.cache, pool.table, i32(lens), offsets(nq), kbar,
+                                           B, topk, shared_routing=shared, return_lse=True,
+                                           return_idx=True)
+    torch.cuda.synchronize()
+    assert moba.moba_device_status() == 0
+    check_decode(q, pool, lens, nq, B, topk, shared, out, lse, idx)
+    # without the extra results, into a given tensor with padded rows behind
+    qp = torch.cat([q, q.new_full((2, Hq, d), float("nan"))])
+    mine = torch.full_like(qp, 9.0)
+    got = moba.moba_decode_cache(qp, pool.cache, pool.table, i32(lens), offsets(nq), kbar, B, topk,
+                                 shared_routing=shared, out=mine)
+    assert got is mine and torch.equal(mine[:n], out) and (mine[n:] == 9).all()
+    assert moba.moba_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.bfloat16, 64),
+                                     (torch.float32, 128)])
+def test_decode_never_looks_past_a_request(dtype, d):
+    """Rows behind a request's length in its last page, unused pages and other requests' rows may
+    hold NaN: no bit of the result changes."""
+    lens, nq, B, page = [333, 70], [2, 1], 50, 64
+    pool, kbar = filled(lens, 2, d, page, B, seed=5)
+    q = torch.randn(3, 4, d, generator=torch.Generator().manual_seed(2)).to(dtype).to(DEV)
+    args = (pool.table, i32(lens), offsets(nq), kbar, B, 3)
+    want = moba.moba_decode_cache(q, pool.cache, *args)
+    used = torch.zeros(pool.cache.k.shape[0], page, dtype=torch.bool)
+    for r, L in enumerate(lens):
+        at = torch.arange(L)
+        used[pool.table[r].cpu().long()[at // page], at % page] = True
+    for x in pool.cache[:2]:
+        x.view(torch.uint8).transpose(1, 2)[~used.to(DEV)] = 127
+    for x in pool.cache[2:]:
+        x.view(torch.uint8).transpose(1, 2)[~used.to(DEV)] = 255
+    kbar[0, 6:] = float("nan")  # means of blocks that are not complete
+    kbar[1, 1:] = float("nan")
+    assert torch.equal(moba.moba_decode_cache(q, pool.cache, *args), want)
+    # a NaN row that is read makes its readers NaN
+    pool.cache.k_scale.view(torch.uint8)[int(pool.table[1, 0]), :, 0] = 255
+    got = moba.moba_decode_cache(q, pool.cache, *args)
+    assert torch.equal(got[:2], want[:2]) and got[2].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_extreme_queries_and_scales(dtype):
+    """Queries 2^30 times larger and keys 2^-30 smaller give the same logits; queries of 2^-100
+    give the plain mean of the values. Powers of two: only the weights' own rounding differs."""
+    lens, B = [300], 64
+    pool, kbar = filled(lens, 2, 128, 32, B, seed=8)
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(1, 4, 128, generator=g).to(dtype).to(DEV)
+    args = (pool.table, i32(lens), offsets([1]))
+    a = moba.moba_decode_cache(q, pool.cache, *args, kbar, B, 5, return_lse=True)
+    pool.cache.k_scale.view(torch.uint8).sub_(30)
+    b = moba.moba_decode_cache(q * 2.0 ** 30, pool.cache, *args, kbar * 2.0 ** -30, B, 5,
+                               return_lse=True)
+    assert ref.off(b[0], a[0].double().cpu()) <= TOL[dtype]
+    assert (a[1] - b[1]).abs().max() <= LSE_TOL
+    out = moba.moba_decode_cache(q * 2.0 ** -100, pool.cache, *args, kbar, B, 5)
+    mean = contents(pool, 0, 300)[1].mean(dim=0).repeat_interleave(2, 0)[None]
+    assert ref.off(out, mean) <= TOL[dtype]
+
+
+def test_bad_pages_and_lengths_are_reported_and_skipped():
+    lens, B = [200, 150, 90], 32
+    pool, kbar = filled(lens, 2, 64, 16, B, seed=9)
+    q = torch.randn(3, 4, 64, generator=torch.Generator().manual_seed(2)).to(DEV)
+    cu = offsets([1, 1, 1])
+    want = moba.moba_decode_cache(q, pool.cache, pool.table, i32(lens), cu, kbar, B, 16)
+    assert moba.moba_device_status() == 0
+    table = pool.table.clone()
+    table[0, 1], table[0, 3] = -1, pool.cache.k.shape[0]  # no pages of the pool
+    got = moba.moba_decode_cache(q, pool.cache, table, i32(lens), cu, kbar, B, 16)
+    assert moba.moba_device_status() == moba.MOBA_ERR_BAD_INDICES
+    assert torch.isfinite(got).all() and torch.equal(got[1:], want[1:])
+    table[0] = 1 << 30
+    got = moba.moba_decode_cache(q, pool.cache, table, i32(lens), cu, kbar, B, 16)
+    assert moba.moba_device_status() == moba.MOBA_ERR_BAD_INDICES
+    assert (got[0] == 0).all() and torch.equal(got[1:], want[1:])
+    before = pool.bits()
+    x = torch.ones(200, 2, 64, device=DEV)
+    moba.moba_cache_write(pool.cache, x, x, table, i32(lens), offsets([200, 0, 0]), kbar, B)
+    assert moba.moba_device_status() == moba.MOBA_ERR_BAD_INDICES
+    assert all(torch.equal(a, b) for a, b in zip(pool.bits(), before))
+    k = torch.full((200, 2, 64), 3.0, device=DEV)
+    moba.moba_cache_read(pool.cache, table, i32(lens), offsets([200, 0, 0]), 200,
+                         dtype=torch.float32, k=k, v=k.clone())
+    assert moba.moba_device_status() == moba.MOBA_ERR_BAD_INDICES and (k == 3).all()
+    # more rows than positions, lengths past the pages or kbar, a negative length
+    for bad in ([0, 150, 90], [1 << 20, 150, 90], [-5, 150, 90], [pool.table.shape[1] * 16 + 1, 150, 90]):
+        out = torch.full_like(q, 4.0)
+        moba.moba_decode_cache(q, pool.cache, pool.table, i32(bad), cu, kbar, B, 16, out=out)
+        assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG
+        assert (out[0] == 4).all() and torch.equal(out[1:], want[1:])
+        moba.moba_cache_write(pool.cache, x[:1], x[:1], pool.table, i32(bad), offsets([1, 0, 0]),
+                              kbar, B)
+        assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG
+        assert all(torch.equal(a, b) for a, b in zip(pool.bits(), before))
+        k.fill_(3.0)
+        moba.moba_cache_read(pool.cache, pool.table, i32(bad), offsets([1, 0, 0]), 200,
+                             dtype=torch.float32, k=k, v=k.clone())
+        assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG and (k == 3).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_serving_loop(dtype):
+    """A prompt through the prefill forward and into the cache, then decoding token by token, the
+    first steps eager and the rest as replays of one captured step; each step against the
+    definition on the cache's contents, and the whole cache read back at the end."""
+    Hq, Hkv, d, page, B, topk = 8, 2, 128, 32, 64, 3
+    prompt, steps = [150, 61], 6
+    room = steps + 2
+    pool = Pool([n + room for n in prompt], page, Hkv, d, seed=12)
+    g = torch.Generator().manual_seed(13)
+    mk = lambda n, h: (torch.randn(n, h, d, generator=g) * 0.7).to(dtype).to(DEV)  # noqa: E731
+    n = sum(prompt)
+    q, k, v = mk(n, Hq), mk(n, Hkv), mk(n, Hkv)
+    cu = offsets(prompt)
+    out = moba.moba_forward(q, k, v, cu, B, topk, max_seqlen=max(prompt))
+    nb = -(-(max(prompt) + room) // B)
+    kbar = torch.zeros(2, nb, Hkv, d, device=DEV)
+    lens = i32(prompt)
+    moba.moba_cache_write(pool.cache, k, v, pool.table, lens, cu, kbar, B)
+    assert torch.isfinite(out).all()
+    one = offsets([1, 1])
+    qs, ks, vs = mk(2, Hq), mk(2, Hkv), mk(2, Hkv)
+
+    def step():
+        moba.moba_cache_write(pool.cache, ks, vs, pool.table, lens, one, kbar, B)
+        return moba.moba_decode_cache(qs, pool.cache, pool.table, lens, one, kbar, B, topk,
+                                      return_lse=True, return_idx=True)
+
+    graph = None
+    for t in range(steps):
+        for x, h in ((qs, Hq), (ks, Hkv), (vs, Hkv)):
+            x.copy_(mk(2, h))
+        lens += 1
+        if t < 2:
+            res = step()
+        else:
+            if graph is None:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    res = step()
+            graph.replay()
+        torch.cuda.synchronize()
+        assert moba.moba_device_status() == 0
+        check_decode(qs, pool, lens.tolist(), [1, 1], B, topk, False, *res)
+    full = lens.tolist()
+    rk, rv = moba.moba_cache_read(pool.cache, pool.table, lens, offsets(full), sum(full),
+                                  dtype=dtype)
+    want = torch.cat([torch.stack(contents(pool, r, full[r])) for r in range(2)], dim=1).to(dtype)
+    assert torch.equal(torch.stack([rk, rv]).cpu(), want)
+
+
+def test_two_streams_at_once():
+    """Two decodes over one cache on two streams, each with its own results."""
+    lens, B = [900, 400], 64
+    pool, kbar = filled(lens, 2, 128, 32, B, seed=21)
+    q = torch.randn(2, 2, 8, 128, generator=torch.Generator().manual_seed(5)).bfloat16().to(DEV)
+    args = (pool.cache, pool.table, i32(lens), offsets([1, 1]), kbar, B, 4)
+    want = [moba.moba_decode_cache(q[i], *args) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append(moba.moba_decode_cache(q[i], *args))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

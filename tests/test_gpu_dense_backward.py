@@ -1,0 +1,191 @@
+"""dense_causal_backward on the GPU against the 64-bit formulas (the forward's own out and lse as
+inputs), against differences of the loss, and on the calls its documentation allows.
+
+Tolerances, relative 2-norm. fp32: a logit is a sum of d <= 128 products, off by at most
+d * 2^-24 * sum|q k| / sqrt(d) ~ 128 * 6e-8 * 3.6 = 2.8e-5 for entries of deviation 0.7, which is
+P's relative error; dS has it from P, from dP and from D, and the sum over up to 700 rows adds
+700 * 6e-8 = 4e-5 at worst: 1.3e-4. bf16: P or dS and the result are each rounded once, half a
+step being 2^-8 relative: 2 * 2^-8 = 7.9e-3 (the fp32 part is far below).
+
+To that comes what cancels. dP_ij = dO_i . v_j and D_i = dO_i . out_i are fp32 sums of d products,
+each off by at most d * 2^-24 * sum|dO v| or d * 2^-24 * sum|dO out|, and where their difference
+is near zero that does not shrink with it: a row with one key has P = 1, out = v and the gradient
+0, so no tolerance relative to the gradient holds there. dq is therefore off by at most
+d * 2^-24 * sum_j P_ij (|dO_i|.|v_j| + |dO_i|.|out_i|) |k_j| / sqrt(d) more, dk likewise: `room`
+below, with the gradient's own sum in place of the products' and |.| on every factor."""
+import pytest
+import torch
+
+import long_context_prefill_block_b200 as moba
+import reference64 as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TOL = {torch.float32: 1.3e-4, torch.bfloat16: 7.9e-3}
+
+
+def case(lens, Hq, Hkv, d, dtype, seed=0, scale=0.7):
+    g = torch.Generator().manual_seed(seed)
+    T = sum(lens)
+    q, k, v, do = ((torch.randn(T, H, d, generator=g) * scale).to(dtype) for H in (Hq, Hkv, Hkv, Hq))
+    cu = torch.tensor([0] + list(torch.cumsum(torch.tensor(lens), 0)), dtype=torch.int32)
+    return q, k, v, do, cu
+
+
+def run(q, k, v, do, cu, **kw):
+    q, k, v, do = (x.to(DEV) for x in (q, k, v, do))
+    out, lse = moba.dense_causal_forward(q, k, v, cu, return_lse=True)
+    grads = moba.dense_causal_backward(q, k, v, cu, out, lse, do, **kw)
+    torch.cuda.synchronize()
+    assert moba.moba_device_status() == 0
+    return out, lse, grads
+
+
+def check(q, k, v, do, cu, out, lse, grads):
+    want = ref.dense_backward(q, k, v, cu, out.cpu(), lse.cpu(), do)
+    eps = q.shape[2] * 2.0 ** -24
+    for name, x, y, r in zip(("dq", "dk", "dv"), grads, want, room(q, k, v, cu, out.cpu(),
+                                                                   lse.cpu(), do)):
+        assert x.dtype == q.dtype and x.shape == y.shape
+        err = float((x.double().cpu() - y).norm())
+        assert err <= TOL[q.dtype] * float(y.norm()) + eps * r, name
+
+
+def room(q, k, v, cu, out, lse, do):
+    """Norms of the sums of absolute values that dq and dk cancel from (dv cancels nothing)."""
+    res = ref.dense_backward(q, k, v, cu, out, lse, do, sizes=True)
+    return float(res[0].norm()), float(res[1].norm()), 0.0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens,Hq,Hkv,d", [
+    ((1,), 1, 1, 128), ((2, 1, 3), 2, 1, 64), ((127,), 2, 2, 128), ((128,), 1, 1, 64),
+    ((129, 0, 64), 2, 1, 128), ((255, 257), 4, 2, 64), ((65, 63, 1, 500), 3, 3, 128),
+    ((640,), 6, 2, 128), ((383, 31), 5, 1, 64)])
+def test_gradients_match_the_formulas(lens, Hq, Hkv, d, dtype):
+    q, k, v, do, cu = case(lens, Hq, Hkv, d, dtype)
+    check(q, k, v, do, cu, *run(q, k, v, do, cu))
+
+
+def test_gradients_match_differences_of_the_loss():
+    """Along a random direction u: (loss(x + e u) - loss(x - e u)) / 2e in 64 bits, e = 1e-5 (its
+    own error about e^2), against the kernel's gradient times u: within the fp32 tolerance of the
+    norms' product."""
+    q, k, v, do, cu = case((70, 130), 4, 2, 64, torch.float32, seed=3)
+    _, _, grads = run(q, k, v, do, cu)
+    g = torch.Generator().manual_seed(9)
+    for i in range(3):
+        u = torch.randn((q, k, v)[i].shape, generator=g, dtype=torch.float64)
+        loss = []
+        for e in (1e-5, -1e-5):
+            x = [t.double() for t in (q, k, v)]
+            x[i] = x[i] + e * u
+            loss.append(float((ref.dense_forward(*x, cu)[0] * do.double()).sum()))
+        diff = (loss[0] - loss[1]) / 2e-5
+        got = float((grads[i].double().cpu() * u).sum())
+        assert abs(got - diff) <= TOL[torch.float32] * float(grads[i].double().norm() * u.norm())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_equal_calls_give_equal_bits(dtype):
+    q, k, v, do, cu = case((300, 500), 4, 2, 128, dtype, seed=5)
+    a = run(q, k, v, do, cu)[2]
+    b = run(q, k, v, do, cu)[2]
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.bfloat16, 64),
+                                     (torch.float32, 64)])
+def test_sequences_do_not_see_each_other_nor_the_padding(dtype, d):
+    """A neighbour full of NaN and padding rows of NaN change no bit of a sequence's gradients;
+    padding rows get zeros."""
+    q, k, v, do, cu = case((200, 77), 4, 2, d, dtype, seed=6)
+    out, lse, a = run(q, k, v, do, cu)
+    nan = float("nan")
+    # out and lse of the call without the padding: the gradient alone is looked at here
+    pad = [torch.cat([x, torch.full((50,) + x.shape[1:], nan, dtype=x.dtype, device=x.device)]).to(DEV)
+           for x in (q, k, v, do, out, lse)]
+    out, lse = pad[4:]
+    b = moba.dense_causal_backward(*pad[:3], cu.to(DEV), out, lse, pad[3], max_seqlen=200)
+    for x, y in zip(a, b):
+        assert torch.equal(x, y[:277]) and not y[277:].any()
+    for x in pad:
+        x[200:277] = nan
+    out[200:277], lse[200:277] = nan, nan
+    c = moba.dense_causal_backward(*pad[:3], cu.to(DEV), out, lse, pad[3], max_seqlen=200)
+    for x, y in zip(a, c):
+        assert torch.equal(x[:200], y[:200])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_large_logits_and_peaked_rows(dtype):
+    """Logits up to several hundred: P is 0 or 1 to the last bit in most places. Absolute against
+    the largest gradient, since peaked rows cancel: lse and logits near 500 are off by 500 * 2^-23
+    = 6e-5 each in fp32 and P by twice that relatively; bf16 adds its roundings as above."""
+    q, k, v, do, cu = case((260,), 2, 1, 64, dtype, seed=7, scale=5.0)
+    out, lse, grads = run(q, k, v, do, cu)
+    want = ref.dense_backward(q, k, v, cu, out.cpu(), lse.cpu(), do)
+    for x, y in zip(grads, want):
+        assert torch.isfinite(x).all()
+        tol = TOL[dtype] + 2 * 6e-5 * 2
+        assert ref.off(x, y) <= 2 * tol
+
+
+def test_another_stream_and_a_captured_call():
+    q, k, v, do, cu = case((150, 333), 4, 2, 128, torch.bfloat16, seed=8)
+    out, lse, want = run(q, k, v, do, cu)
+    a = [x.to(DEV) for x in (q, k, v, do)]
+    cud = cu.to(DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = moba.dense_causal_backward(*a[:3], cud, out, lse, a[3], max_seqlen=333)
+    s.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = moba.dense_causal_backward(*a[:3], cud, out, lse, a[3], max_seqlen=333)
+    a[3].mul_(2)  # twice the loss: every step but the roundings doubles, and those are scaled too
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, 2 * y) for x, y in zip(got, want))
+
+
+def test_a_longer_sequence_than_max_seqlen_is_reported():
+    q, k, v, do, cu = case((150, 333), 2, 1, 128, torch.bfloat16, seed=8)
+    out, lse, want = run(q, k, v, do, cu)
+    a = [x.to(DEV) for x in (q, k, v, do)]
+    got = moba.dense_causal_backward(*a[:3], cu.to(DEV), out, lse, a[3], max_seqlen=200)
+    torch.cuda.synchronize()
+    assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG
+    assert all(torch.equal(x[:150], y[:150]) for x, y in zip(got, want))
+
+
+def test_two_layers_trained_together():
+    """A block-attention layer and a dense layer in a row, as a hybrid stack has them: the loss's
+    gradient at the inputs through both, fp32, against 64-bit autograd of the same stack with all
+    blocks chosen (then the first layer is dense as well)."""
+    lens, H, d = (96, 160), 2, 64
+    q, k, v, do, cu = case(lens, H, H, d, torch.float32, seed=11)
+    qd, kd, vd, dd = (x.to(DEV) for x in (q, k, v, do))
+    B, topk = 32, 5  # 160 tokens have 5 blocks
+    o1, l1 = moba.moba_forward(qd, kd, vd, cu, B, topk, return_lse=True)
+    o2, l2 = moba.dense_causal_forward(o1, kd, vd, cu, return_lse=True)
+    g1, gk2, gv2 = moba.dense_causal_backward(o1, kd, vd, cu, o2, l2, dd)
+    gq, gk1, gv1 = moba.moba_backward(qd, kd, vd, cu, o1, l1, g1, B, topk)
+    x = [t.double().requires_grad_() for t in (q, k, v)]
+    h = _autograd_dense(*x, cu)
+    _autograd_dense(h, x[1], x[2], cu).backward(do.double())
+    # two layers' errors, the first's input gradient being off already
+    for got, t in zip((gq, gk1 + gk2, gv1 + gv2), x):
+        assert ref.off(got, t.grad) <= 2 * TOL[torch.float32]
+
+
+def _autograd_dense(q, k, v, cu):
+    res = []
+    for b in range(len(cu) - 1):
+        a, e = int(cu[b]), int(cu[b + 1])
+        s = torch.einsum("ihd,jhd->hij", q[a:e], k[a:e]) / q.shape[2] ** 0.5
+        s = s.masked_fill(torch.ones(e - a, e - a, dtype=torch.bool).triu(1), float("-inf"))
+        res.append(torch.einsum("hij,jhd->ihd", torch.softmax(s, -1), v[a:e]))
+    return torch.cat(res)
