@@ -316,6 +316,10 @@ constexpr int kSimtTileM = 32;
 cudaError_t launch_dense_bwd_stat(const Dims& dm, const void* out, const void* dout,
                                   const float* lse, const int32_t* cu, float* stat, void* dq,
                                   void* dk, void* dv, cudaStream_t st);
+// bf16 inputs (dense_bwd_tc.cu), then fp32 inputs.
+cudaError_t launch_dense_bwd_tc(const Dims& dm, const void* q, const void* k, const void* v,
+                                const void* dout, const float* stat, const int32_t* cu, void* dq,
+                                void* dk, void* dv, int* status, cudaStream_t st);
 cudaError_t launch_dense_bwd_simt(const Dims& dm, const void* q, const void* k, const void* v,
                                   const void* dout, const float* stat, const int32_t* cu, void* dq,
                                   void* dk, void* dv, int* status, cudaStream_t st);

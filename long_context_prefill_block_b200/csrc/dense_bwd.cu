@@ -76,18 +76,17 @@ dense_bwd_stat_kernel(Dims dm, const T* __restrict__ out, const T* __restrict__ 
   }
 }
 
-template <typename T>
 struct Args {
   Dims dm;
-  const T* q;
-  const T* k;
-  const T* v;
-  const T* dout;
+  const float* q;
+  const float* k;
+  const float* v;
+  const float* dout;
   const float* stat;
   const int32_t* cu;
-  T* dq;
-  T* dk;
-  T* dv;
+  float* dq;
+  float* dk;
+  float* dv;
   int* status;
 };
 
@@ -103,28 +102,19 @@ __device__ __forceinline__ Place place(int batch, int heads) {
 
 // 64 rows of one head (row stride in elements) into shared memory, rows at
 // or past n as zeros.
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(float (*dst)[D + 4], const T* src, int64_t stride,
+template <int D>
+__device__ __forceinline__ void load_tile(float (*dst)[D + 4], const float* src, int64_t stride,
                                           int n) {
-  constexpr int VEC = Vec16<T>::N, TPR = D / VEC;
-  for (int e = threadIdx.x; e < 64 * TPR; e += kThreads) {
-    const int r = e / TPR, c = e % TPR;
-    float x[VEC];
-#pragma unroll
-    for (int u = 0; u < VEC; ++u) x[u] = 0.f;
-    if (r < n) Vec16<T>::load(src + r * stride + c * VEC, x);
-#pragma unroll
-    for (int u = 0; u < VEC; u += 4)
-      *reinterpret_cast<float4*>(&dst[r][c * VEC + u]) = make_float4(x[u], x[u + 1], x[u + 2], x[u + 3]);
+  for (int e = threadIdx.x; e < 64 * (D / 4); e += kThreads) {
+    const int r = e / (D / 4), c = e % (D / 4);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < n) x = __ldg(reinterpret_cast<const float4*>(src + r * stride) + c);
+    *reinterpret_cast<float4*>(&dst[r][c * 4]) = x;
   }
 }
 
 __device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
   *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d) {
-  __nv_bfloat162 v[2] = {__floats2bfloat162_rn(a, b), __floats2bfloat162_rn(c, d)};
-  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(v);
 }
 
 template <int D>
@@ -194,13 +184,13 @@ __device__ __forceinline__ void tile_ps(Smem<D>& sm, int q0, int k0, int len) {
 }
 
 // Rows of the query tile: q, dO and the statistics.
-template <typename T, int D>
-__device__ __forceinline__ void load_queries(const Args<T>& a, Smem<D>& sm, int64_t start, int q0,
+template <int D>
+__device__ __forceinline__ void load_queries(const Args& a, Smem<D>& sm, int64_t start, int q0,
                                              int len, int h) {
   const int n = min(BR, len - q0);
   const int64_t row = (start + q0) * a.dm.Hq + h;
-  load_tile<T, D>(sm.Q, a.q + row * D, (int64_t)a.dm.Hq * D, n);
-  load_tile<T, D>(sm.O, a.dout + row * D, (int64_t)a.dm.Hq * D, n);
+  load_tile<D>(sm.Q, a.q + row * D, (int64_t)a.dm.Hq * D, n);
+  load_tile<D>(sm.O, a.dout + row * D, (int64_t)a.dm.Hq * D, n);
   if (threadIdx.x < BR) {
     const int r = threadIdx.x;
     const float* st = a.stat + (int64_t)h * a.dm.T + start + q0 + r;
@@ -212,8 +202,8 @@ __device__ __forceinline__ void load_queries(const Args<T>& a, Smem<D>& sm, int6
 // dk, dv of 64 keys of one kv head: every later query tile of every q head
 // of the group. Bound by the fp32 FMA rate (shared-memory reads are 6 of
 // every 8 issue slots' wavefronts).
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) dense_bwd_kv_kernel(const Args<T> a) {
+template <int D>
+__global__ void __launch_bounds__(kThreads) dense_bwd_kv_kernel(const Args a) {
   extern __shared__ __align__(16) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   const Dims& dm = a.dm;
@@ -227,8 +217,8 @@ __global__ void __launch_bounds__(kThreads) dense_bwd_kv_kernel(const Args<T> a)
   if (k0 >= len) return;
   const int nk = min(BK, len - k0);
   const int64_t krow = (start + k0) * dm.Hkv + g;
-  load_tile<T, D>(sm.K, a.k + krow * D, (int64_t)dm.Hkv * D, nk);
-  load_tile<T, D>(sm.V, a.v + krow * D, (int64_t)dm.Hkv * D, nk);
+  load_tile<D>(sm.K, a.k + krow * D, (int64_t)dm.Hkv * D, nk);
+  load_tile<D>(sm.V, a.v + krow * D, (int64_t)dm.Hkv * D, nk);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // keys ty * 4 .., dims tx * 4 + 64 w
   constexpr int NW = D / 64;
   float dk[4][4 * NW], dv[4][4 * NW];
@@ -240,7 +230,7 @@ __global__ void __launch_bounds__(kThreads) dense_bwd_kv_kernel(const Args<T> a)
   for (int h = g * grp; h < (g + 1) * grp; ++h) {
     for (int q0 = k0; q0 < len; q0 += BR) {
       __syncthreads();
-      load_queries<T, D>(a, sm, start, q0, len, h);
+      load_queries<D>(a, sm, start, q0, len, h);
       __syncthreads();
       tile_ps<D, false>(sm, q0, k0, len);
       __syncthreads();
@@ -286,8 +276,8 @@ __global__ void __launch_bounds__(kThreads) dense_bwd_kv_kernel(const Args<T> a)
 
 // dq of 64 queries of one head: every key tile up to the diagonal. Blocks
 // are numbered last tile first, the longest work.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) dense_bwd_q_kernel(const Args<T> a) {
+template <int D>
+__global__ void __launch_bounds__(kThreads) dense_bwd_q_kernel(const Args a) {
   extern __shared__ __align__(16) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   const Dims& dm = a.dm;
@@ -299,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) dense_bwd_q_kernel(const Args<T> a) 
     return;
   const int q0 = ((dm.max_seqlen + BR - 1) / BR - 1 - pl.tile) * BR;
   if (q0 >= len) return;
-  load_queries<T, D>(a, sm, start, q0, len, h);
+  load_queries<D>(a, sm, start, q0, len, h);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // queries ty * 4 .., dims tx * 4 + 64 w
   constexpr int NW = D / 64;
   float dq[4][4 * NW];
@@ -310,8 +300,8 @@ __global__ void __launch_bounds__(kThreads) dense_bwd_q_kernel(const Args<T> a) 
   for (int k0 = 0; k0 <= q0; k0 += BK) {
     const int64_t krow = (start + k0) * dm.Hkv + g;
     __syncthreads();
-    load_tile<T, D>(sm.K, a.k + krow * D, (int64_t)dm.Hkv * D, min(BK, len - k0));
-    load_tile<T, D>(sm.V, a.v + krow * D, (int64_t)dm.Hkv * D, min(BK, len - k0));
+    load_tile<D>(sm.K, a.k + krow * D, (int64_t)dm.Hkv * D, min(BK, len - k0));
+    load_tile<D>(sm.V, a.v + krow * D, (int64_t)dm.Hkv * D, min(BK, len - k0));
     __syncthreads();
     tile_ps<D, true>(sm, q0, k0, len);
     __syncthreads();
@@ -356,33 +346,23 @@ cudaError_t run_stat(const Dims& dm, const void* out, const void* dout, const fl
   return cudaGetLastError();
 }
 
-template <typename T, int D>
-cudaError_t run_simt(const Args<T>& a, cudaStream_t st) {
+template <int D>
+cudaError_t run_simt(const Args& a, cudaStream_t st) {
   const Dims& dm = a.dm;
   cudaError_t e;
   constexpr int smem = (int)sizeof(Smem<D>);
-  if ((e = cudaFuncSetAttribute(dense_bwd_kv_kernel<T, D>,
+  if ((e = cudaFuncSetAttribute(dense_bwd_kv_kernel<D>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
     return e;
-  if ((e = cudaFuncSetAttribute(dense_bwd_q_kernel<T, D>,
+  if ((e = cudaFuncSetAttribute(dense_bwd_q_kernel<D>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
     return e;
   const int64_t nt = (int64_t)((dm.max_seqlen + BK - 1) / BK) * dm.batch;
   if (nt * dm.Hq > INT32_MAX) return cudaErrorInvalidValue;
-  dense_bwd_kv_kernel<T, D><<<(unsigned)(nt * dm.Hkv), kThreads, smem, st>>>(a);
+  dense_bwd_kv_kernel<D><<<(unsigned)(nt * dm.Hkv), kThreads, smem, st>>>(a);
   if ((e = cudaGetLastError())) return e;
-  dense_bwd_q_kernel<T, D><<<(unsigned)(nt * dm.Hq), kThreads, smem, st>>>(a);
+  dense_bwd_q_kernel<D><<<(unsigned)(nt * dm.Hq), kThreads, smem, st>>>(a);
   return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t run_type(const Dims& dm, const void* q, const void* k, const void* v, const void* dout,
-                     const float* stat, const int32_t* cu, void* dq, void* dk, void* dv,
-                     int* status, cudaStream_t st) {
-  const Args<T> a{dm, static_cast<const T*>(q), static_cast<const T*>(k),
-                  static_cast<const T*>(v), static_cast<const T*>(dout), stat, cu,
-                  static_cast<T*>(dq), static_cast<T*>(dk), static_cast<T*>(dv), status};
-  return dm.d == 128 ? run_simt<T, 128>(a, st) : run_simt<T, 64>(a, st);
 }
 
 }  // namespace
@@ -402,9 +382,18 @@ cudaError_t launch_dense_bwd_simt(const Dims& dm, const void* q, const void* k, 
                                   const void* dout, const float* stat, const int32_t* cu, void* dq,
                                   void* dk, void* dv, int* status, cudaStream_t st) {
   if (dm.batch == 0 || dm.max_seqlen == 0) return cudaSuccess;
-  if (dm.dtype == kBF16)
-    return run_type<__nv_bfloat16>(dm, q, k, v, dout, stat, cu, dq, dk, dv, status, st);
-  return run_type<float>(dm, q, k, v, dout, stat, cu, dq, dk, dv, status, st);
+  const Args a{dm,
+               static_cast<const float*>(q),
+               static_cast<const float*>(k),
+               static_cast<const float*>(v),
+               static_cast<const float*>(dout),
+               stat,
+               cu,
+               static_cast<float*>(dq),
+               static_cast<float*>(dk),
+               static_cast<float*>(dv),
+               status};
+  return dm.d == 128 ? run_simt<128>(a, st) : run_simt<64>(a, st);
 }
 
 }  // namespace moba

@@ -1,0 +1,649 @@
+// Tensor-core gradient of dense causal attention, bf16 inputs (formulas and
+// the choice of two passes: dense_bwd.cu). 128 x 128 tiles of (keys, queries),
+// tcgen05 products with fp32 accumulators in TMEM, operands by TMA.
+//
+//   kv pass  one CTA per (128 keys, kv head): per item (q head of the group,
+//            128 queries at or after the keys)
+//              S^T = K Q^T, dP^T = V dO^T        (K, V stay in shared memory)
+//              P^T = exp2(S^T * c - lse2), dS^T = P^T (dP^T - D)
+//              dV += P^T dO, dK += dS^T Q         (A operands from TMEM)
+//   q pass   one CTA per (128 queries, q head): per 128 keys up to the diagonal
+//              S = Q K^T, dP = dO V^T, dS as above, dQ += dS K
+//
+// P^T and dS^T come out of the products with the lanes (keys, or queries in
+// the q pass) that the next product's A operand needs, so they go from
+// registers straight back to TMEM as bf16 and never through shared memory.
+// Shared-memory reads of the products bound the kv pass: 64 KB for each of S
+// and dP (two operands), 32 KB for each of dV and dK (one), 64 KB of TMA
+// writes, at 128 B/clock 2048 clocks an item, exactly the 2048 clocks of its
+// four products.
+//
+// Roles (12 warps): warp 0 loads tiles by TMA; lane 0 of warp 1 issues the
+// products; warp 2 brings the row statistics (kv pass). Rows of a last,
+// partial tile that lie behind the sequence are cleared in shared memory (by
+// warp 2, or warp 0 in the q pass): they are summed over, and zeros of P or
+// dS would not silence an infinity or NaN in them. Warps 4 to 11 do the element-wise work, two threads a TMEM lane with 64 columns each.
+// The products of one thread run in issue order, which is what lets S of the
+// next item overwrite P of this one as soon as dV has been issued.
+//
+// Every wait is bounded (tc::mbar_wait); on expiry the CTA records kStTimeout,
+// drains the copies and products it issued, frees its TMEM and exits.
+#include <mutex>
+
+#include "tc_ptx.cuh"
+
+namespace moba {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 384;
+constexpr int TT = 128;  // keys and queries per tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kHalf = 128 * 128;  // bytes of one 64-column half of a tile
+constexpr uint32_t kTmemCols = 512;
+constexpr int NA = 3;  // ring of the tiles used first and last in an item (Q; K in the q pass)
+constexpr int NB = 2;  // ring of the others (dO; V)
+
+template <int D>
+struct Cfg {
+  static constexpr int NH = D / 64;
+  static constexpr uint32_t kTile = NH * kHalf;
+  static constexpr uint32_t kSmem = (2 + NA + NB) * kTile;
+  static constexpr uint32_t kIdescNN = idesc_bf16(TT, TT, false, false);
+  static constexpr uint32_t kIdescTN = idesc_bf16(TT, D, false, true);  // A in TMEM, B N-major
+};
+
+struct Args {
+  Dims dm;
+  const float* stat;
+  const int32_t* cu;
+  __nv_bfloat16* dq;
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  int* status;
+};
+
+// Static shared memory, padded so that the dynamic part starts on a
+// 1024-byte boundary (the swizzle's period).
+struct alignas(1024) Shared {
+  float lse2[2][TT], D[2][TT];
+  uint64_t fixed_full;           // the resident pair of tiles
+  uint64_t a_full[NA], a_empty[NA], b_full[NB], b_empty[NB];
+  uint64_t clear_full[2];        // a partial tile's rows are cleared
+  uint64_t stat_full[2], stat_empty[2];
+  uint64_t s_full[2], p_ready, dp_full, ds_ready, acc_full, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Shared) == 3072, "static shared memory");
+
+// One 128-row tile of one head, from token z.
+template <int D>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                          int head, int z) {
+#pragma unroll
+  for (int x = 0; x < Cfg<D>::NH; ++x) tma_load_3d(dst + x * kHalf, map, bar, x * 64, head, z);
+}
+
+// D[tmem] = A B^T over d: two tiles in shared memory, both K-major.
+template <int D>
+__device__ __forceinline__ void mma_nn(uint32_t d, uint32_t a, uint32_t b) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+    mma_ss(d, desc_sw128(a + off, 16, 1024), desc_sw128(b + off, 16, 1024), Cfg<D>::kIdescNN,
+           kk > 0 ? 1u : 0u);
+  }
+}
+
+// D[tmem] += A B over the tile's 128 rows: A as bf16 pairs in TMEM, in two
+// halves of 64 rows at columns 0 and 64 (each element-wise half writes where
+// it read), B a tile in shared memory, N-major.
+template <int D>
+__device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, uint32_t b, bool add) {
+#pragma unroll
+  for (int kk = 0; kk < TT / 16; ++kk)
+    mma_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, desc_sw128(b + kk * 16 * 128, kHalf, 1024),
+           Cfg<D>::kIdescTN, (add || kk > 0) ? 1u : 0u);
+}
+
+// Zeros rows n .. 127 of a tile (a warp's lanes together).
+template <int D>
+__device__ __forceinline__ void clear_rows(uint32_t tile, int n) {
+  const int lane = threadIdx.x & 31;
+  for (int e = n * 8 + lane; e < TT * 8; e += 32)
+#pragma unroll
+    for (int x = 0; x < Cfg<D>::NH; ++x)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + x * kHalf + e * 16),
+                   "r"(0)
+                   : "memory");
+}
+
+// One warp's arrival, after every lane's work.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ void init_shared(Shared& sh) {
+  if (threadIdx.x == 0) {
+    mbar_init(&sh.fixed_full, 1);
+    for (int i = 0; i < NA; ++i) {
+      mbar_init(&sh.a_full[i], 1);
+      mbar_init(&sh.a_empty[i], 1);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&sh.b_full[i], 1);
+      mbar_init(&sh.b_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.clear_full[i], 1);
+      mbar_init(&sh.stat_full[i], 1);
+      mbar_init(&sh.stat_empty[i], 8);
+      mbar_init(&sh.s_full[i], 1);
+    }
+    mbar_init(&sh.p_ready, 8);
+    mbar_init(&sh.dp_full, 1);
+    mbar_init(&sh.ds_ready, 8);
+    mbar_init(&sh.acc_full, 1);
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    mbar_fence_init();
+  }
+  if ((threadIdx.x >> 5) == 1) {
+    tmem_alloc(&sh.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+}
+
+__device__ __forceinline__ void finish(Shared& sh) {
+  fence_before_sync();
+  __syncthreads();
+  if ((threadIdx.x >> 5) == 1) {
+    fence_after_sync();
+    tmem_dealloc(sh.tmem_base, kTmemCols);
+  }
+}
+
+// 32 columns of an accumulator, times f, rounded to bf16, to 32 elements of a row.
+__device__ __forceinline__ void store_cols(__nv_bfloat16* dst, uint32_t taddr, float f, bool on) {
+  uint32_t r[32];
+  tmem_ld32(taddr, r);
+  tmem_wait_ld();
+  if (!on) return;
+#pragma unroll
+  for (int x = 0; x < 32; x += 16) {
+    uint32_t w[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      w[u] = pack_bf16x2(__uint_as_float(r[x + 2 * u]) * f, __uint_as_float(r[x + 2 * u + 1]) * f);
+    st_global_v8_b32(dst + x, w);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
+                const Args a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Shared sh;
+  constexpr uint32_t kTile = Cfg<D>::kTile;
+  const Dims& dm = a.dm;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // heads outermost: the CTAs that run together read the same Q and dO, and
+  // within a head the tiles with the most queries come first
+  const int nt = (dm.max_seqlen + TT - 1) / TT;
+  const int kt = blockIdx.x % nt, g = blockIdx.x / nt % dm.Hkv, b = blockIdx.x / nt / dm.Hkv;
+  int64_t start;
+  int len;
+  if (!seq_bounds(dm, a.cu, b, start, len, a.status) || !MOBA_CHECK(start + len <= dm.T, a.status))
+    return;
+  const int k0 = kt * TT;
+  if (k0 >= len) return;
+  const uint32_t sb = smem_u32(smem);
+  if (sb & 1023u) {  // the layout above did not hold: nothing can be right
+    if (threadIdx.x == 0) set_status(a.status, kStCheck);
+    return;
+  }
+  const uint32_t sK = sb, sV = sb + kTile, sQ = sb + 2 * kTile, sO = sQ + NA * kTile;
+  const int grp = dm.Hq / dm.Hkv, per = (len - k0 + TT - 1) / TT, n_items = grp * per;
+  const int last_rows = len - (k0 + (per - 1) * TT);  // queries of each head's last tile
+  init_shared(sh);
+  const uint32_t tmem = sh.tmem_base, tS = tmem, tP = tmem + 128, tV = tmem + 256,
+                 tK = tmem + 256 + D;
+  volatile int* abort = &sh.abort;
+  int* status = a.status;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      mbar_expect_tx(&sh.fixed_full, 2 * kTile);
+      load_tile<D>(sK, &tmk, &sh.fixed_full, g, (int)start + k0);
+      load_tile<D>(sV, &tmv, &sh.fixed_full, g, (int)start + k0);
+      int na = 0, nb = 0;
+      bool ok = true;
+      for (int it = 0, h = g * grp, i = 0; it < n_items; ++it) {
+        const int z = (int)start + k0 + i * TT;
+        if (it >= NA && !(ok = mbar_wait(&sh.a_empty[it % NA], (it / NA - 1) & 1, abort, status)))
+          break;
+        mbar_expect_tx(&sh.a_full[it % NA], kTile);
+        load_tile<D>(sQ + it % NA * kTile, &tmq, &sh.a_full[it % NA], h, z);
+        ++na;
+        if (it >= NB && !(ok = mbar_wait(&sh.b_empty[it % NB], (it / NB - 1) & 1, abort, status)))
+          break;
+        mbar_expect_tx(&sh.b_full[it % NB], kTile);
+        load_tile<D>(sO + it % NB * kTile, &tmo, &sh.b_full[it % NB], h, z);
+        ++nb;
+        if (++i == per) {
+          i = 0;
+          ++h;
+        }
+      }
+      if (!ok || *abort) {  // let the copies already issued land before the CTA exits
+        mbar_drain(&sh.fixed_full, 0);
+        for (int x = na > NA ? na - NA : 0; x < na; ++x) mbar_drain(&sh.a_full[x % NA], x / NA & 1);
+        for (int x = nb > NB ? nb - NB : 0; x < nb; ++x) mbar_drain(&sh.b_full[x % NB], x / NB & 1);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int cleared = 0;
+      bool ok = mbar_wait(&sh.fixed_full, 0, abort, status);
+      // Q and dO of an item are in shared memory, and cleared where partial
+      auto landed = [&](int it) {
+        bool w = mbar_wait(&sh.a_full[it % NA], it / NA & 1, abort, status);
+        if (w && last_rows < TT && it % per == per - 1) {
+          w = mbar_wait(&sh.clear_full[cleared & 1], cleared / 2 & 1, abort, status);
+          ++cleared;
+        }
+        return w;
+      };
+      if (ok) ok = landed(0);
+      if (ok) {
+        fence_after_sync();
+        mma_nn<D>(tS, sK, sQ);
+        commit(&sh.s_full[0]);
+        ok = mbar_wait(&sh.b_full[0], 0, abort, status);
+      }
+      if (ok) {
+        mma_nn<D>(tP, sV, sO);
+        commit(&sh.dp_full);
+      }
+      for (int it = 0; ok && it < n_items; ++it) {
+        const uint32_t q = sQ + it % NA * kTile, o = sO + it % NB * kTile;
+        if (!(ok = mbar_wait(&sh.p_ready, it & 1, abort, status))) break;
+        fence_after_sync();
+        mma_tn<D>(tV, tS, o, it > 0);
+        commit(&sh.b_empty[it % NB]);
+        if (it + 1 < n_items) {
+          if (!(ok = landed(it + 1))) break;
+          mma_nn<D>(tS, sK, sQ + (it + 1) % NA * kTile);
+          commit(&sh.s_full[0]);
+        }
+        if (!(ok = mbar_wait(&sh.ds_ready, it & 1, abort, status))) break;
+        fence_after_sync();
+        mma_tn<D>(tK, tP, q, it > 0);
+        commit(&sh.a_empty[it % NA]);
+        if (it + 1 < n_items) {
+          if (!(ok = mbar_wait(&sh.b_full[(it + 1) % NB], (it + 1) / NB & 1, abort, status))) break;
+          mma_nn<D>(tP, sV, sO + (it + 1) % NB * kTile);
+          commit(&sh.dp_full);
+        }
+      }
+      if (ok) {
+        commit(&sh.acc_full);
+      } else {  // wait until every product issued has finished
+        commit(&sh.drain);
+        mbar_drain(&sh.drain, 0);
+      }
+    }
+  } else if (warp == 2) {
+    // clear_full has two slots: dO of item it + 2 lands only after dV of item
+    // it, so this warp is at most one partial tile ahead of the issuer
+    const float* st = a.stat + start + k0;
+    int cleared = 0;
+    for (int it = 0, h = g * grp, i = 0; it < n_items; ++it) {
+      const int s = it & 1, n = i == per - 1 ? last_rows : TT;
+      bool ok = it < 2 || mbar_wait(&sh.stat_empty[s], (it / 2 - 1) & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const float* src = st + (int64_t)h * dm.T + i * TT;
+#pragma unroll
+      for (int r = lane; r < TT; r += 32) {
+        sh.lse2[s][r] = r < n ? __ldg(src + r) : 0.f;
+        sh.D[s][r] = r < n ? __ldg(src + (int64_t)dm.Hq * dm.T + r) : 0.f;
+      }
+      warp_arrive(&sh.stat_full[s]);
+      if (n < TT) {
+        ok = mbar_wait(&sh.a_full[it % NA], it / NA & 1, abort, status) &&
+             mbar_wait(&sh.b_full[it % NB], it / NB & 1, abort, status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        clear_rows<D>(sQ + it % NA * kTile, n);
+        clear_rows<D>(sO + it % NB * kTile, n);
+        fence_proxy_async_smem();
+        warp_arrive(&sh.clear_full[cleared++ & 1]);
+      }
+      if (++i == per) {
+        i = 0;
+        ++h;
+      }
+    }
+  } else if (warp >= 4) {
+    const int half = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t at = (static_cast<uint32_t>(quarter * 32) << 16) + half * 64;
+    const float sl2 = rsqrtf((float)D) * kLog2e;
+    bool ok = true;
+    for (int it = 0, i = 0; it < n_items; ++it) {
+      const int s = it & 1;
+      // keys after a query and queries behind the sequence: only in each
+      // head's first and last tile. Column x is visible in [lo, hi).
+      const bool masked = i == 0 || (i == per - 1 && last_rows < TT);
+      const int lo = (i == 0 ? r : 0) - half * 64;
+      const int hi = (i == per - 1 ? last_rows : TT) - half * 64;
+      if (++i == per) i = 0;
+      ok = mbar_wait(&sh.stat_full[s], it / 2 & 1, abort, status) &&
+           mbar_wait(&sh.s_full[0], it & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      fence_after_sync();
+      float p[64];
+      {
+        uint32_t v0[32], v1[32];
+        tmem_ld32(tS + at, v0);
+        tmem_ld32(tS + at + 32, v1);
+        tmem_wait_ld();
+        const float4* l4 = reinterpret_cast<const float4*>(&sh.lse2[s][half * 64]);
+#pragma unroll
+        for (int x = 0; x < 64; x += 4) {
+          const float4 l = l4[x / 4];
+          const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t sv = x < 32 ? v0[(x + u) & 31] : v1[(x + u) & 31];
+            p[x + u] = ex2(fmaf(__uint_as_float(sv), sl2, -lv[u]));
+          }
+        }
+      }
+      if (masked) {
+#pragma unroll
+        for (int x = 0; x < 64; ++x) p[x] = x >= lo && x < hi ? p[x] : 0.f;
+      }
+      {
+        // P in bf16 (half a step of 2^-8: the weights of dV's sum); the
+        // products of dS keep the unrounded P
+        uint32_t w[32];
+#pragma unroll
+        for (int x = 0; x < 32; ++x) w[x] = pack_bf16x2(p[2 * x], p[2 * x + 1]);
+        tmem_st32(tS + at, w);
+      }
+      tmem_wait_st();
+      fence_before_sync();
+      warp_arrive(&sh.p_ready);
+      ok = mbar_wait(&sh.dp_full, it & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      fence_after_sync();
+      uint32_t w[32];
+      const float4* d4 = reinterpret_cast<const float4*>(&sh.D[s][half * 64]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tP + at + c * 32, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 32; x += 4) {
+          const float4 dd = d4[c * 8 + x / 4];
+          float ds[4] = {p[c * 32 + x] * (__uint_as_float(v[x]) - dd.x),
+                         p[c * 32 + x + 1] * (__uint_as_float(v[x + 1]) - dd.y),
+                         p[c * 32 + x + 2] * (__uint_as_float(v[x + 2]) - dd.z),
+                         p[c * 32 + x + 3] * (__uint_as_float(v[x + 3]) - dd.w)};
+          if (masked) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int y = c * 32 + x + u;
+              ds[u] = y >= lo && y < hi ? ds[u] : 0.f;
+            }
+          }
+          w[c * 16 + x / 2] = pack_bf16x2(ds[0], ds[1]);
+          w[c * 16 + x / 2 + 1] = pack_bf16x2(ds[2], ds[3]);
+        }
+      }
+      tmem_st32(tP + at, w);
+      tmem_wait_st();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.stat_empty[s]);
+        mbar_arrive(&sh.ds_ready);
+      }
+    }
+    // dK and dV of key r: this thread's half of the columns
+    if (ok) ok = mbar_wait(&sh.acc_full, 0, abort, status);
+    if (__all_sync(0xffffffffu, ok)) {
+      fence_after_sync();
+      const bool on = k0 + r < len;
+      const int64_t row = ((start + k0 + (on ? r : 0)) * dm.Hkv + g) * D;
+      const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+#pragma unroll 1
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+        store_cols(a.dk + row + c, tK + lanes + c, rsqrtf((float)D), on);
+        store_cols(a.dv + row + c, tV + lanes + c, 1.f, on);
+      }
+    }
+  }
+  finish(sh);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+               const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
+               const Args a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Shared sh;
+  constexpr uint32_t kTile = Cfg<D>::kTile;
+  const Dims& dm = a.dm;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the heads of a group outermost but one: CTAs that run together read the
+  // same K and V; the longest tiles of a head come first
+  const int nt = (dm.max_seqlen + TT - 1) / TT;
+  const int qt = nt - 1 - blockIdx.x % nt, h = blockIdx.x / nt % dm.Hq, b = blockIdx.x / nt / dm.Hq;
+  int64_t start;
+  int len;
+  if (!seq_bounds(dm, a.cu, b, start, len, a.status) || !MOBA_CHECK(start + len <= dm.T, a.status))
+    return;
+  const int q0 = qt * TT;
+  if (q0 >= len) return;
+  const int g = h / (dm.Hq / dm.Hkv), n_items = qt + 1;
+  const int last_keys = min(len - q0, TT);  // keys of the diagonal tile
+  const uint32_t sb = smem_u32(smem);
+  if (sb & 1023u) {  // the layout above did not hold: nothing can be right
+    if (threadIdx.x == 0) set_status(a.status, kStCheck);
+    return;
+  }
+  const uint32_t sQ = sb, sO = sb + kTile, sK = sb + 2 * kTile, sV = sK + NA * kTile;
+  init_shared(sh);
+  const uint32_t tmem = sh.tmem_base, tP = tmem + 256, tQ = tmem + 384;
+  volatile int* abort = &sh.abort;
+  int* status = a.status;
+
+  if (warp == 0) {
+    bool ok = true;
+    if (lane == 0) {
+      mbar_expect_tx(&sh.fixed_full, 2 * kTile);
+      load_tile<D>(sQ, &tmq, &sh.fixed_full, h, (int)start + q0);
+      load_tile<D>(sO, &tmo, &sh.fixed_full, h, (int)start + q0);
+      int na = 0, nb = 0;
+      for (int j = 0; j < n_items; ++j) {
+        const int z = (int)start + j * TT;
+        if (j >= NA && !(ok = mbar_wait(&sh.a_empty[j % NA], (j / NA - 1) & 1, abort, status)))
+          break;
+        mbar_expect_tx(&sh.a_full[j % NA], kTile);
+        load_tile<D>(sK + j % NA * kTile, &tmk, &sh.a_full[j % NA], g, z);
+        ++na;
+        if (j >= NB && !(ok = mbar_wait(&sh.b_empty[j % NB], (j / NB - 1) & 1, abort, status)))
+          break;
+        mbar_expect_tx(&sh.b_full[j % NB], kTile);
+        load_tile<D>(sV + j % NB * kTile, &tmv, &sh.b_full[j % NB], g, z);
+        ++nb;
+      }
+      if (!ok || *abort) {
+        mbar_drain(&sh.fixed_full, 0);
+        for (int x = na > NA ? na - NA : 0; x < na; ++x) mbar_drain(&sh.a_full[x % NA], x / NA & 1);
+        for (int x = nb > NB ? nb - NB : 0; x < nb; ++x) mbar_drain(&sh.b_full[x % NB], x / NB & 1);
+      }
+    }
+    if (last_keys < TT) {  // the diagonal tile's keys behind the sequence
+      const int j = n_items - 1;
+      if (lane == 0 && ok) ok = mbar_wait(&sh.a_full[j % NA], j / NA & 1, abort, status);
+      if (__all_sync(0xffffffffu, ok)) {
+        clear_rows<D>(sK + j % NA * kTile, last_keys);
+        fence_proxy_async_smem();
+        warp_arrive(&sh.clear_full[0]);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = mbar_wait(&sh.fixed_full, 0, abort, status);
+      auto s_product = [&](int j) {
+        bool w = mbar_wait(&sh.a_full[j % NA], j / NA & 1, abort, status);
+        if (w && j == n_items - 1 && last_keys < TT)
+          w = mbar_wait(&sh.clear_full[0], 0, abort, status);
+        if (!w) return false;
+        fence_after_sync();
+        mma_nn<D>(tmem + (j & 1) * 128, sQ, sK + j % NA * kTile);
+        commit(&sh.s_full[j & 1]);
+        return true;
+      };
+      auto dp_product = [&](int j) {
+        if (!mbar_wait(&sh.b_full[j % NB], j / NB & 1, abort, status)) return false;
+        fence_after_sync();
+        mma_nn<D>(tP, sO, sV + j % NB * kTile);
+        commit(&sh.dp_full);
+        commit(&sh.b_empty[j % NB]);
+        return true;
+      };
+      ok = ok && s_product(0) && dp_product(0);
+      for (int j = 0; ok && j < n_items; ++j) {
+        // S of the next keys goes into the other buffer, whose dS the last
+        // dQ product has been issued for
+        if (j + 1 < n_items && !(ok = s_product(j + 1))) break;
+        if (!(ok = mbar_wait(&sh.ds_ready, j & 1, abort, status))) break;
+        fence_after_sync();
+        if (j + 1 < n_items && !(ok = dp_product(j + 1))) break;
+        mma_tn<D>(tQ, tmem + (j & 1) * 128, sK + j % NA * kTile, j > 0);
+        commit(&sh.a_empty[j % NA]);
+      }
+      if (ok) {
+        commit(&sh.acc_full);
+      } else {
+        commit(&sh.drain);
+        mbar_drain(&sh.drain, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    const int half = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, at = lanes + half * 64;
+    const float sl2 = rsqrtf((float)D) * kLog2e;
+    const bool on = q0 + r < len;
+    float l2 = 0.f, dd = 0.f;
+    if (on) {
+      const float* st = a.stat + (int64_t)h * dm.T + start + q0 + r;
+      l2 = __ldg(st);
+      dd = __ldg(st + (int64_t)dm.Hq * dm.T);
+    }
+    bool ok = true;
+    for (int j = 0; j < n_items; ++j) {
+      const uint32_t tS = tmem + (j & 1) * 128 + at;
+      ok = mbar_wait(&sh.s_full[j & 1], j / 2 & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      fence_after_sync();
+      float p[64];
+      {
+        uint32_t v0[32], v1[32];
+        tmem_ld32(tS, v0);
+        tmem_ld32(tS + 32, v1);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          p[x] = ex2(fmaf(__uint_as_float(v0[x]), sl2, -l2));
+          p[32 + x] = ex2(fmaf(__uint_as_float(v1[x]), sl2, -l2));
+        }
+      }
+      ok = mbar_wait(&sh.dp_full, j & 1, abort, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      fence_after_sync();
+      const bool masked = j == n_items - 1;  // the diagonal: keys up to the query
+      const int hi = min(r + 1, last_keys) - half * 64;
+      uint32_t w[32];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tP + at + c * 32, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          float d0 = p[c * 32 + x] * (__uint_as_float(v[x]) - dd);
+          float d1 = p[c * 32 + x + 1] * (__uint_as_float(v[x + 1]) - dd);
+          if (masked) {
+            d0 = c * 32 + x < hi ? d0 : 0.f;
+            d1 = c * 32 + x + 1 < hi ? d1 : 0.f;
+          }
+          w[c * 16 + x / 2] = pack_bf16x2(d0, d1);
+        }
+      }
+      tmem_st32(tS, w);
+      tmem_wait_st();
+      fence_before_sync();
+      warp_arrive(&sh.ds_ready);
+    }
+    if (ok) ok = mbar_wait(&sh.acc_full, 0, abort, status);
+    if (__all_sync(0xffffffffu, ok)) {
+      fence_after_sync();
+      const int64_t row = ((start + q0 + (on ? r : 0)) * dm.Hq + h) * D;
+#pragma unroll 1
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32)
+        store_cols(a.dq + row + c, tQ + lanes + c, rsqrtf((float)D), on);
+    }
+  }
+  finish(sh);
+}
+
+template <int D>
+cudaError_t run(const Args& a, const void* q, const void* k, const void* v, const void* dout,
+                cudaStream_t st) {
+  const Dims& dm = a.dm;
+  CUtensorMap mq, mk, mv, mo;
+  cudaError_t e;
+  if ((e = make_head_map(&mq, q, dm.T, dm.Hq, TT, D))) return e;
+  if ((e = make_head_map(&mk, k, dm.T, dm.Hkv, TT, D))) return e;
+  if ((e = make_head_map(&mv, v, dm.T, dm.Hkv, TT, D))) return e;
+  if ((e = make_head_map(&mo, dout, dm.T, dm.Hq, TT, D))) return e;
+  constexpr int smem = (int)Cfg<D>::kSmem;
+  if ((e = cudaFuncSetAttribute(dense_bwd_kv_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                smem)))
+    return e;
+  if ((e = cudaFuncSetAttribute(dense_bwd_q_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                smem)))
+    return e;
+  const int64_t nt = (int64_t)((dm.max_seqlen + TT - 1) / TT) * dm.batch;
+  if (nt * dm.Hq > INT32_MAX) return cudaErrorInvalidValue;
+  dense_bwd_kv_tc<D><<<(unsigned)(nt * dm.Hkv), kThreads, smem, st>>>(mq, mk, mv, mo, a);
+  if ((e = cudaGetLastError())) return e;
+  dense_bwd_q_tc<D><<<(unsigned)(nt * dm.Hq), kThreads, smem, st>>>(mq, mk, mv, mo, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_dense_bwd_tc(const Dims& dm, const void* q, const void* k, const void* v,
+                                const void* dout, const float* stat, const int32_t* cu, void* dq,
+                                void* dk, void* dv, int* status, cudaStream_t st) {
+  if (dm.batch == 0 || dm.max_seqlen == 0) return cudaSuccess;
+  const Args a{dm, stat, cu, static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk),
+               static_cast<__nv_bfloat16*>(dv), status};
+  return dm.d == 128 ? run<128>(a, q, k, v, dout, st) : run<64>(a, q, k, v, dout, st);
+}
+
+}  // namespace moba

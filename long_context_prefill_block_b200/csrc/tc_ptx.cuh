@@ -13,10 +13,10 @@ namespace moba {
 namespace tc {
 
 // ---- host side (tma_host.cu) ------------------------------------------------
-// TMA descriptor of a [T][H][128] bf16 tensor viewed as (x = d, y = head,
-// z = token), 128-byte swizzle, box 64 x 1 x rows: one 64-column half of
-// `rows` consecutive tokens of one head.
-cudaError_t make_head_map(CUtensorMap* map, const void* base, int T, int H, int rows);
+// TMA descriptor of a [T][H][d] bf16 tensor (d = 128 or 64) viewed as (x = d,
+// y = head, z = token), 128-byte swizzle, box 64 x 1 x rows: one 64-column
+// half of `rows` consecutive tokens of one head.
+cudaError_t make_head_map(CUtensorMap* map, const void* base, int T, int H, int rows, int d = 128);
 int sm_count();
 constexpr int kMaxDevices = 64;  // host-side per-device caches
 

@@ -24,11 +24,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 }  // namespace
 
-cudaError_t make_head_map(CUtensorMap* map, const void* base, int T, int H, int rows) {
+cudaError_t make_head_map(CUtensorMap* map, const void* base, int T, int H, int rows, int d) {
   auto fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {128, (cuuint64_t)H, (cuuint64_t)T};
-  const cuuint64_t strides[2] = {128 * 2, (cuuint64_t)H * 128 * 2};
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2};
   const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
