@@ -18,11 +18,12 @@
 // writes, at 128 B/clock 2048 clocks an item, exactly the 2048 clocks of its
 // four products.
 //
-// Roles (12 warps): warp 0 loads tiles by TMA; lane 0 of warp 1 issues the
-// products; warp 2 brings the row statistics (kv pass). Rows of a last,
+// Roles (20 warps): warp 0 loads tiles by TMA; one lane of warp 1 issues
+// the products; warp 2 brings the row statistics (kv pass). Rows of a last,
 // partial tile that lie behind the sequence are cleared in shared memory (by
 // warp 2, or warp 0 in the q pass): they are summed over, and zeros of P or
-// dS would not silence an infinity or NaN in them. Warps 4 to 11 do the element-wise work, two threads a TMEM lane with 64 columns each.
+// dS would not silence an infinity or NaN in them. Warps 4 to 19 do the
+// element-wise work, four threads a TMEM lane with 32 columns each.
 // The products of one thread run in issue order, which is what lets S of the
 // next item overwrite P of this one as soon as dV has been issued.
 //
@@ -37,8 +38,13 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
 constexpr int TT = 128;  // keys and queries per tile
+constexpr int kWarpsE = 16;                   // element-wise warps, four threads a TMEM lane
+constexpr int kThreads = 128 + kWarpsE * 32;
+constexpr int CW = TT * 4 / kWarpsE;          // columns of a tile per element-wise thread
+// Columns whose P the q pass forms before dP arrives; it forms the others
+// with dS, where the exponential unit would idle.
+constexpr int kAhead = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kHalf = 128 * 128;  // bytes of one 64-column half of a tile
 constexpr uint32_t kTmemCols = 512;
@@ -88,24 +94,26 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 
 // D[tmem] = A B^T over d: two tiles in shared memory, both K-major.
 template <int D>
-__device__ __forceinline__ void mma_nn(uint32_t d, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void mma_nn(uint32_t on, uint32_t d, uint32_t a, uint32_t b) {
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-    mma_ss(d, desc_sw128(a + off, 16, 1024), desc_sw128(b + off, 16, 1024), Cfg<D>::kIdescNN,
-           kk > 0 ? 1u : 0u);
+    mma_ss_on(on, d, desc_sw128(a + off, 16, 1024), desc_sw128(b + off, 16, 1024),
+              Cfg<D>::kIdescNN, kk > 0 ? 1u : 0u);
   }
 }
 
-// D[tmem] += A B over the tile's 128 rows: A as bf16 pairs in TMEM, in two
-// halves of 64 rows at columns 0 and 64 (each element-wise half writes where
-// it read), B a tile in shared memory, N-major.
+// D[tmem] += A B over the tile's 128 rows: A as bf16 pairs in TMEM, every CW
+// rows' pairs at the columns their fp32 values had (each element-wise thread
+// writes where it read), B a tile in shared memory, N-major.
 template <int D>
-__device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, uint32_t b, bool add) {
+__device__ __forceinline__ void mma_tn(uint32_t on, uint32_t d, uint32_t a, uint32_t b,
+                                       bool add) {
 #pragma unroll
   for (int kk = 0; kk < TT / 16; ++kk)
-    mma_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, desc_sw128(b + kk * 16 * 128, kHalf, 1024),
-           Cfg<D>::kIdescTN, (add || kk > 0) ? 1u : 0u);
+    mma_ts_on(on, d, a + kk * 16 / CW * CW + kk * 16 % CW / 2,
+              desc_sw128(b + kk * 16 * 128, kHalf, 1024), Cfg<D>::kIdescTN,
+              (add || kk > 0) ? 1u : 0u);
 }
 
 // Zeros rows n .. 127 of a tile (a warp's lanes together).
@@ -126,7 +134,18 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-__device__ __forceinline__ void init_shared(Shared& sh) {
+__device__ __forceinline__ void finish(Shared& sh) {
+  fence_before_sync();
+  __syncthreads();
+  if ((threadIdx.x >> 5) == 1) {
+    fence_after_sync();
+    tmem_dealloc(sh.tmem_base, kTmemCols);
+  }
+}
+
+// Barriers and TMEM. A CTA has the SM's tensor memory to itself and takes all
+// of it, so its columns start at 0, which the kernels use as a constant.
+__device__ __forceinline__ bool init_shared(Shared& sh, int* status) {
   if (threadIdx.x == 0) {
     mbar_init(&sh.fixed_full, 1);
     for (int i = 0; i < NA; ++i) {
@@ -140,12 +159,12 @@ __device__ __forceinline__ void init_shared(Shared& sh) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.clear_full[i], 1);
       mbar_init(&sh.stat_full[i], 1);
-      mbar_init(&sh.stat_empty[i], 8);
+      mbar_init(&sh.stat_empty[i], kWarpsE);
       mbar_init(&sh.s_full[i], 1);
     }
-    mbar_init(&sh.p_ready, 8);
+    mbar_init(&sh.p_ready, kWarpsE);
     mbar_init(&sh.dp_full, 1);
-    mbar_init(&sh.ds_ready, 8);
+    mbar_init(&sh.ds_ready, kWarpsE);
     mbar_init(&sh.acc_full, 1);
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
@@ -158,15 +177,10 @@ __device__ __forceinline__ void init_shared(Shared& sh) {
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-}
-
-__device__ __forceinline__ void finish(Shared& sh) {
-  fence_before_sync();
-  __syncthreads();
-  if ((threadIdx.x >> 5) == 1) {
-    fence_after_sync();
-    tmem_dealloc(sh.tmem_base, kTmemCols);
-  }
+  if (sh.tmem_base == 0) return true;
+  if (threadIdx.x == 0) set_status(status, kStCheck);
+  finish(sh);
+  return false;
 }
 
 // 32 columns of an accumulator, times f, rounded to bf16, to 32 elements of a row.
@@ -194,7 +208,7 @@ dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__
   __shared__ Shared sh;
   constexpr uint32_t kTile = Cfg<D>::kTile;
   const Dims& dm = a.dm;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // heads outermost: the CTAs that run together read the same Q and dO, and
   // within a head the tiles with the most queries come first
   const int nt = (dm.max_seqlen + TT - 1) / TT;
@@ -213,9 +227,8 @@ dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__
   const uint32_t sK = sb, sV = sb + kTile, sQ = sb + 2 * kTile, sO = sQ + NA * kTile;
   const int grp = dm.Hq / dm.Hkv, per = (len - k0 + TT - 1) / TT, n_items = grp * per;
   const int last_rows = len - (k0 + (per - 1) * TT);  // queries of each head's last tile
-  init_shared(sh);
-  const uint32_t tmem = sh.tmem_base, tS = tmem, tP = tmem + 128, tV = tmem + 256,
-                 tK = tmem + 256 + D;
+  if (!init_shared(sh, a.status)) return;
+  constexpr uint32_t tS = 0, tP = 128, tV = 256, tK = 256 + D;  // TMEM columns
   volatile int* abort = &sh.abort;
   int* status = a.status;
 
@@ -250,56 +263,58 @@ dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int cleared = 0;
-      bool ok = mbar_wait(&sh.fixed_full, 0, abort, status);
-      // Q and dO of an item are in shared memory, and cleared where partial
-      auto landed = [&](int it) {
-        bool w = mbar_wait(&sh.a_full[it % NA], it / NA & 1, abort, status);
-        if (w && last_rows < TT && it % per == per - 1) {
-          w = mbar_wait(&sh.clear_full[cleared & 1], cleared / 2 & 1, abort, status);
-          ++cleared;
-        }
-        return w;
-      };
-      if (ok) ok = landed(0);
-      if (ok) {
-        fence_after_sync();
-        mma_nn<D>(tS, sK, sQ);
-        commit(&sh.s_full[0]);
-        ok = mbar_wait(&sh.b_full[0], 0, abort, status);
+    const uint32_t on = elect_one();
+    int cleared = 0;
+    // a wait of the whole warp; false in every lane if one gave up
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status)) != 0;
+    };
+    bool ok = wait(&sh.fixed_full, 0);
+    // Q and dO of an item are in shared memory, and cleared where partial
+    auto landed = [&](int it) {
+      bool w = wait(&sh.a_full[it % NA], it / NA & 1);
+      if (w && last_rows < TT && it % per == per - 1) {
+        w = wait(&sh.clear_full[cleared & 1], cleared / 2 & 1);
+        ++cleared;
       }
-      if (ok) {
-        mma_nn<D>(tP, sV, sO);
-        commit(&sh.dp_full);
+      return w;
+    };
+    if (ok) ok = landed(0);
+    if (ok) {
+      mma_nn<D>(on, tS, sK, sQ);
+      commit_on(on, &sh.s_full[0]);
+      ok = wait(&sh.b_full[0], 0);
+    }
+    if (ok) {
+      mma_nn<D>(on, tP, sV, sO);
+      commit_on(on, &sh.dp_full);
+    }
+    for (int it = 0; ok && it < n_items; ++it) {
+      const uint32_t q = sQ + it % NA * kTile, o = sO + it % NB * kTile;
+      if (!(ok = wait(&sh.p_ready, it & 1))) break;
+      fence_after_sync();
+      mma_tn<D>(on, tV, tS, o, it > 0);
+      commit_on(on, &sh.b_empty[it % NB]);
+      if (it + 1 < n_items) {
+        if (!(ok = landed(it + 1))) break;
+        mma_nn<D>(on, tS, sK, sQ + (it + 1) % NA * kTile);
+        commit_on(on, &sh.s_full[0]);
       }
-      for (int it = 0; ok && it < n_items; ++it) {
-        const uint32_t q = sQ + it % NA * kTile, o = sO + it % NB * kTile;
-        if (!(ok = mbar_wait(&sh.p_ready, it & 1, abort, status))) break;
-        fence_after_sync();
-        mma_tn<D>(tV, tS, o, it > 0);
-        commit(&sh.b_empty[it % NB]);
-        if (it + 1 < n_items) {
-          if (!(ok = landed(it + 1))) break;
-          mma_nn<D>(tS, sK, sQ + (it + 1) % NA * kTile);
-          commit(&sh.s_full[0]);
-        }
-        if (!(ok = mbar_wait(&sh.ds_ready, it & 1, abort, status))) break;
-        fence_after_sync();
-        mma_tn<D>(tK, tP, q, it > 0);
-        commit(&sh.a_empty[it % NA]);
-        if (it + 1 < n_items) {
-          if (!(ok = mbar_wait(&sh.b_full[(it + 1) % NB], (it + 1) / NB & 1, abort, status))) break;
-          mma_nn<D>(tP, sV, sO + (it + 1) % NB * kTile);
-          commit(&sh.dp_full);
-        }
+      if (!(ok = wait(&sh.ds_ready, it & 1))) break;
+      fence_after_sync();
+      mma_tn<D>(on, tK, tP, q, it > 0);
+      commit_on(on, &sh.a_empty[it % NA]);
+      if (it + 1 < n_items) {
+        if (!(ok = wait(&sh.b_full[(it + 1) % NB], (it + 1) / NB & 1))) break;
+        mma_nn<D>(on, tP, sV, sO + (it + 1) % NB * kTile);
+        commit_on(on, &sh.dp_full);
       }
-      if (ok) {
-        commit(&sh.acc_full);
-      } else {  // wait until every product issued has finished
-        commit(&sh.drain);
-        mbar_drain(&sh.drain, 0);
-      }
+    }
+    if (ok) {
+      commit_on(on, &sh.acc_full);
+    } else {  // wait until every product issued has finished
+      commit_on(on, &sh.drain);
+      mbar_drain(&sh.drain, 0);
     }
   } else if (warp == 2) {
     // clear_full has two slots: dO of item it + 2 lands only after dV of item
@@ -332,8 +347,8 @@ dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__
       }
     }
   } else if (warp >= 4) {
-    const int half = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t at = (static_cast<uint32_t>(quarter * 32) << 16) + half * 64;
+    const int c0 = ((warp - 4) >> 2) * CW, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, at = lanes + c0;
     const float sl2 = rsqrtf((float)D) * kLog2e;
     bool ok = true;
     for (int it = 0, i = 0; it < n_items; ++it) {
@@ -341,42 +356,39 @@ dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__
       // keys after a query and queries behind the sequence: only in each
       // head's first and last tile. Column x is visible in [lo, hi).
       const bool masked = i == 0 || (i == per - 1 && last_rows < TT);
-      const int lo = (i == 0 ? r : 0) - half * 64;
-      const int hi = (i == per - 1 ? last_rows : TT) - half * 64;
+      const int lo = (i == 0 ? r : 0) - c0;
+      const int hi = (i == per - 1 ? last_rows : TT) - c0;
       if (++i == per) i = 0;
       ok = mbar_wait(&sh.stat_full[s], it / 2 & 1, abort, status) &&
            mbar_wait(&sh.s_full[0], it & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after_sync();
-      float p[64];
+      float p[CW];
       {
-        uint32_t v0[32], v1[32];
-        tmem_ld32(tS + at, v0);
-        tmem_ld32(tS + at + 32, v1);
+        uint32_t v[CW];
+        tmem_ld32(tS + at, v);
         tmem_wait_ld();
-        const float4* l4 = reinterpret_cast<const float4*>(&sh.lse2[s][half * 64]);
+        const float4* l4 = reinterpret_cast<const float4*>(&sh.lse2[s][c0]);
 #pragma unroll
-        for (int x = 0; x < 64; x += 4) {
+        for (int x = 0; x < CW; x += 4) {
           const float4 l = l4[x / 4];
-          const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint32_t sv = x < 32 ? v0[(x + u) & 31] : v1[(x + u) & 31];
-            p[x + u] = ex2(fmaf(__uint_as_float(sv), sl2, -lv[u]));
-          }
+          p[x] = ex2(fmaf(__uint_as_float(v[x]), sl2, -l.x));
+          p[x + 1] = ex2(fmaf(__uint_as_float(v[x + 1]), sl2, -l.y));
+          p[x + 2] = ex2(fmaf(__uint_as_float(v[x + 2]), sl2, -l.z));
+          p[x + 3] = ex2(fmaf(__uint_as_float(v[x + 3]), sl2, -l.w));
         }
       }
       if (masked) {
 #pragma unroll
-        for (int x = 0; x < 64; ++x) p[x] = x >= lo && x < hi ? p[x] : 0.f;
+        for (int x = 0; x < CW; ++x) p[x] = x >= lo && x < hi ? p[x] : 0.f;
       }
       {
         // P in bf16 (half a step of 2^-8: the weights of dV's sum); the
         // products of dS keep the unrounded P
-        uint32_t w[32];
+        uint32_t w[CW / 2];
 #pragma unroll
-        for (int x = 0; x < 32; ++x) w[x] = pack_bf16x2(p[2 * x], p[2 * x + 1]);
-        tmem_st32(tS + at, w);
+        for (int x = 0; x < CW / 2; ++x) w[x] = pack_bf16x2(p[2 * x], p[2 * x + 1]);
+        tmem_st16(tS + at, w);
       }
       tmem_wait_st();
       fence_before_sync();
@@ -384,32 +396,25 @@ dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__
       ok = mbar_wait(&sh.dp_full, it & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after_sync();
-      uint32_t w[32];
-      const float4* d4 = reinterpret_cast<const float4*>(&sh.D[s][half * 64]);
+      uint32_t v[CW], w[CW / 2];
+      tmem_ld32(tP + at, v);
+      tmem_wait_ld();
+      const float4* d4 = reinterpret_cast<const float4*>(&sh.D[s][c0]);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[32];
-        tmem_ld32(tP + at + c * 32, v);
-        tmem_wait_ld();
+      for (int x = 0; x < CW; x += 4) {
+        const float4 dd = d4[x / 4];
+        float ds[4] = {p[x] * (__uint_as_float(v[x]) - dd.x),
+                       p[x + 1] * (__uint_as_float(v[x + 1]) - dd.y),
+                       p[x + 2] * (__uint_as_float(v[x + 2]) - dd.z),
+                       p[x + 3] * (__uint_as_float(v[x + 3]) - dd.w)};
+        if (masked) {
 #pragma unroll
-        for (int x = 0; x < 32; x += 4) {
-          const float4 dd = d4[c * 8 + x / 4];
-          float ds[4] = {p[c * 32 + x] * (__uint_as_float(v[x]) - dd.x),
-                         p[c * 32 + x + 1] * (__uint_as_float(v[x + 1]) - dd.y),
-                         p[c * 32 + x + 2] * (__uint_as_float(v[x + 2]) - dd.z),
-                         p[c * 32 + x + 3] * (__uint_as_float(v[x + 3]) - dd.w)};
-          if (masked) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int y = c * 32 + x + u;
-              ds[u] = y >= lo && y < hi ? ds[u] : 0.f;
-            }
-          }
-          w[c * 16 + x / 2] = pack_bf16x2(ds[0], ds[1]);
-          w[c * 16 + x / 2 + 1] = pack_bf16x2(ds[2], ds[3]);
+          for (int u = 0; u < 4; ++u) ds[u] = x + u >= lo && x + u < hi ? ds[u] : 0.f;
         }
+        w[x / 2] = pack_bf16x2(ds[0], ds[1]);
+        w[x / 2 + 1] = pack_bf16x2(ds[2], ds[3]);
       }
-      tmem_st32(tP + at, w);
+      tmem_st16(tP + at, w);
       tmem_wait_st();
       fence_before_sync();
       __syncwarp();
@@ -418,17 +423,17 @@ dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__
         mbar_arrive(&sh.ds_ready);
       }
     }
-    // dK and dV of key r: this thread's half of the columns
+    // dK (the first half of the warps) and dV of key r, 32 columns at a time
     if (ok) ok = mbar_wait(&sh.acc_full, 0, abort, status);
     if (__all_sync(0xffffffffu, ok)) {
       fence_after_sync();
       const bool on = k0 + r < len;
       const int64_t row = ((start + k0 + (on ? r : 0)) * dm.Hkv + g) * D;
-      const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
 #pragma unroll 1
-      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
-        store_cols(a.dk + row + c, tK + lanes + c, rsqrtf((float)D), on);
-        store_cols(a.dv + row + c, tV + lanes + c, 1.f, on);
+      for (int c = c0; c < 2 * D; c += TT) {
+        const bool is_v = c >= D;
+        store_cols((is_v ? a.dv - D : a.dk) + row + c, (is_v ? tV - D : tK) + lanes + c,
+                   is_v ? 1.f : rsqrtf((float)D), on);
       }
     }
   }
@@ -444,7 +449,7 @@ dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   __shared__ Shared sh;
   constexpr uint32_t kTile = Cfg<D>::kTile;
   const Dims& dm = a.dm;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // the heads of a group outermost but one: CTAs that run together read the
   // same K and V; the longest tiles of a head come first
   const int nt = (dm.max_seqlen + TT - 1) / TT;
@@ -463,8 +468,8 @@ dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     return;
   }
   const uint32_t sQ = sb, sO = sb + kTile, sK = sb + 2 * kTile, sV = sK + NA * kTile;
-  init_shared(sh);
-  const uint32_t tmem = sh.tmem_base, tP = tmem + 256, tQ = tmem + 384;
+  if (!init_shared(sh, a.status)) return;
+  constexpr uint32_t tP = 256, tQ = 384;  // TMEM columns; S at 0 and 128
   volatile int* abort = &sh.abort;
   int* status = a.status;
 
@@ -504,47 +509,45 @@ dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      bool ok = mbar_wait(&sh.fixed_full, 0, abort, status);
-      auto s_product = [&](int j) {
-        bool w = mbar_wait(&sh.a_full[j % NA], j / NA & 1, abort, status);
-        if (w && j == n_items - 1 && last_keys < TT)
-          w = mbar_wait(&sh.clear_full[0], 0, abort, status);
-        if (!w) return false;
-        fence_after_sync();
-        mma_nn<D>(tmem + (j & 1) * 128, sQ, sK + j % NA * kTile);
-        commit(&sh.s_full[j & 1]);
-        return true;
-      };
-      auto dp_product = [&](int j) {
-        if (!mbar_wait(&sh.b_full[j % NB], j / NB & 1, abort, status)) return false;
-        fence_after_sync();
-        mma_nn<D>(tP, sO, sV + j % NB * kTile);
-        commit(&sh.dp_full);
-        commit(&sh.b_empty[j % NB]);
-        return true;
-      };
-      ok = ok && s_product(0) && dp_product(0);
-      for (int j = 0; ok && j < n_items; ++j) {
-        // S of the next keys goes into the other buffer, whose dS the last
-        // dQ product has been issued for
-        if (j + 1 < n_items && !(ok = s_product(j + 1))) break;
-        if (!(ok = mbar_wait(&sh.ds_ready, j & 1, abort, status))) break;
-        fence_after_sync();
-        if (j + 1 < n_items && !(ok = dp_product(j + 1))) break;
-        mma_tn<D>(tQ, tmem + (j & 1) * 128, sK + j % NA * kTile, j > 0);
-        commit(&sh.a_empty[j % NA]);
-      }
-      if (ok) {
-        commit(&sh.acc_full);
-      } else {
-        commit(&sh.drain);
-        mbar_drain(&sh.drain, 0);
-      }
+    const uint32_t on = elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status)) != 0;
+    };
+    bool ok = wait(&sh.fixed_full, 0);
+    auto s_product = [&](int j) {
+      if (!wait(&sh.a_full[j % NA], j / NA & 1)) return false;
+      if (j == n_items - 1 && last_keys < TT && !wait(&sh.clear_full[0], 0)) return false;
+      mma_nn<D>(on, (j & 1) * 128, sQ, sK + j % NA * kTile);
+      commit_on(on, &sh.s_full[j & 1]);
+      return true;
+    };
+    auto dp_product = [&](int j) {
+      if (!wait(&sh.b_full[j % NB], j / NB & 1)) return false;
+      mma_nn<D>(on, tP, sO, sV + j % NB * kTile);
+      commit_on(on, &sh.dp_full);
+      commit_on(on, &sh.b_empty[j % NB]);
+      return true;
+    };
+    ok = ok && s_product(0) && dp_product(0);
+    for (int j = 0; ok && j < n_items; ++j) {
+      // S of the next keys goes into the other buffer, whose dS the last
+      // dQ product has been issued for
+      if (j + 1 < n_items && !(ok = s_product(j + 1))) break;
+      if (!(ok = wait(&sh.ds_ready, j & 1))) break;
+      fence_after_sync();
+      if (j + 1 < n_items && !(ok = dp_product(j + 1))) break;
+      mma_tn<D>(on, tQ, (j & 1) * 128, sK + j % NA * kTile, j > 0);
+      commit_on(on, &sh.a_empty[j % NA]);
+    }
+    if (ok) {
+      commit_on(on, &sh.acc_full);
+    } else {
+      commit_on(on, &sh.drain);
+      mbar_drain(&sh.drain, 0);
     }
   } else if (warp >= 4) {
-    const int half = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, at = lanes + half * 64;
+    const int c0 = ((warp - 4) >> 2) * CW, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, at = lanes + c0;
     const float sl2 = rsqrtf((float)D) * kLog2e;
     const bool on = q0 + r < len;
     float l2 = 0.f, dd = 0.f;
@@ -555,45 +558,36 @@ dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     }
     bool ok = true;
     for (int j = 0; j < n_items; ++j) {
-      const uint32_t tS = tmem + (j & 1) * 128 + at;
+      const uint32_t tS = (j & 1) * 128 + at;
       ok = mbar_wait(&sh.s_full[j & 1], j / 2 & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after_sync();
-      float p[64];
-      {
-        uint32_t v0[32], v1[32];
-        tmem_ld32(tS, v0);
-        tmem_ld32(tS + 32, v1);
-        tmem_wait_ld();
+      uint32_t sv[CW], v[CW], w[CW / 2];
+      float p[kAhead];
+      tmem_ld32(tS, sv);
+      tmem_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          p[x] = ex2(fmaf(__uint_as_float(v0[x]), sl2, -l2));
-          p[32 + x] = ex2(fmaf(__uint_as_float(v1[x]), sl2, -l2));
-        }
-      }
+      for (int x = 0; x < kAhead; ++x) p[x] = ex2(fmaf(__uint_as_float(sv[x]), sl2, -l2));
       ok = mbar_wait(&sh.dp_full, j & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after_sync();
       const bool masked = j == n_items - 1;  // the diagonal: keys up to the query
-      const int hi = min(r + 1, last_keys) - half * 64;
-      uint32_t w[32];
+      const int hi = min(r + 1, last_keys) - c0;
+      tmem_ld32(tP + at, v);
+      tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[32];
-        tmem_ld32(tP + at + c * 32, v);
-        tmem_wait_ld();
+      for (int x = 0; x < CW; x += 2) {
+        float ds[2];
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          float d0 = p[c * 32 + x] * (__uint_as_float(v[x]) - dd);
-          float d1 = p[c * 32 + x + 1] * (__uint_as_float(v[x + 1]) - dd);
-          if (masked) {
-            d0 = c * 32 + x < hi ? d0 : 0.f;
-            d1 = c * 32 + x + 1 < hi ? d1 : 0.f;
-          }
-          w[c * 16 + x / 2] = pack_bf16x2(d0, d1);
+        for (int u = 0; u < 2; ++u) {
+          const float pu = x + u < kAhead ? p[(x + u) % kAhead]
+                                          : ex2(fmaf(__uint_as_float(sv[x + u]), sl2, -l2));
+          ds[u] = pu * (__uint_as_float(v[x + u]) - dd);
+          if (masked) ds[u] = x + u < hi ? ds[u] : 0.f;
         }
+        w[x / 2] = pack_bf16x2(ds[0], ds[1]);
       }
-      tmem_st32(tS, w);
+      tmem_st16(tS, w);
       tmem_wait_st();
       fence_before_sync();
       warp_arrive(&sh.ds_ready);
@@ -602,9 +596,7 @@ dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     if (__all_sync(0xffffffffu, ok)) {
       fence_after_sync();
       const int64_t row = ((start + q0 + (on ? r : 0)) * dm.Hq + h) * D;
-#pragma unroll 1
-      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32)
-        store_cols(a.dq + row + c, tQ + lanes + c, rsqrtf((float)D), on);
+      if (c0 < D) store_cols(a.dq + row + c0, tQ + lanes + c0, rsqrtf((float)D), on);
     }
   }
   finish(sh);
