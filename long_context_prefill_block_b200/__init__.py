@@ -131,15 +131,66 @@ def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("max_pages", ctypes.c_int)] + [(n, ctypes.c_void_p) for n in
+                                                ("k", "v", "k_scale", "v_scale", "page_table",
+                                                 "seqlens")]
+
+
+_PARAMS, _CACHE, _V = ctypes.POINTER(MobaParams), ctypes.POINTER(_CacheStruct), ctypes.c_void_p
+_SIGNATURES = {
+    "dense_causal_backward": [_PARAMS] + [_V] * 11 + [ctypes.c_size_t, _V],
+    "moba_cache_write": [_PARAMS, _CACHE] + [_V] * 5,
+    "moba_cache_read": [_PARAMS, _CACHE] + [_V] * 4,
+    "moba_decode_cache": [_PARAMS, _V, _CACHE] + [_V] * 6 + [ctypes.c_size_t, _V],
+    "dense_causal_backward_workspace_size": [_PARAMS],
+    "moba_decode_cache_workspace_size": [_PARAMS],
+}
+_bound = {}  # entry points with their signatures set, by name
+
+
+def _entry(name: str):
+    fn = _bound.get(name)
+    if fn is None:
+        # a function object of its own: what others set on the library's is not seen here
+        fn = ctypes.CFUNCTYPE(ctypes.c_size_t if name.endswith("size") else ctypes.c_int,
+                              *_SIGNATURES[name])((name, lib()))
+        _bound[name] = fn
+    return fn
+
+
+def _call(name: str, device, *args) -> None:
+    """Calls an entry point on the device's current stream, with the device current."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        code = _entry(name)(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            code = _entry(name)(*args, stream)
+    _check(name, code)
+
+
+def _workspace(name: str, p: MobaParams, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
+    if ws is None:
+        ws = torch.empty(max(_entry(name)(p), 256), dtype=torch.uint8, device=device)
+    return ws
+
+
+def _at(x: Optional[torch.Tensor]):
+    return None if x is None else x.data_ptr()
+
+
 def _dev_i32(cu: torch.Tensor, device) -> torch.Tensor:
     return cu.to(device=device, dtype=torch.int32).contiguous()
 
 
 def _check_inputs(*ts):
+    ts = [t for t in ts if t is not None]
     for t in ts:
-        if t is not None and (not t.is_cuda or not t.is_contiguous()):
+        if not t.is_cuda or not t.is_contiguous():
             raise ValueError("tensors must be contiguous CUDA tensors")
-    devs = {t.device for t in ts if t is not None}
+    devs = {t.device for t in ts}
     if len(devs) > 1:
         raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
 
@@ -446,31 +497,13 @@ def dense_causal_backward(q, k, v, cu_seqlens, out, lse, dout, max_seqlen=None,
     if lse.shape != q.shape[:2] or lse.dtype != torch.float32:
         raise ValueError(f"lse must be float32 {tuple(q.shape[:2])}")
     _check_inputs(q, k, v, out, dout, lse, ws)
-    L = lib()
     p = make_params(q, k, cu_seqlens, 128, 1, max_seqlen)
     cu = _dev_i32(cu_seqlens, q.device)
-    size = L.dense_causal_backward_workspace_size
-    size.argtypes, size.restype = [ctypes.POINTER(MobaParams)], ctypes.c_size_t
-    if ws is None:
-        ws = torch.empty(max(int(size(ctypes.byref(p))), 256), dtype=torch.uint8, device=q.device)
+    ws = _workspace("dense_causal_backward_workspace_size", p, q.device, ws)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    fn = L.dense_causal_backward
-    fn.argtypes = [ctypes.POINTER(MobaParams)] + [ctypes.c_void_p] * 11 + [ctypes.c_size_t,
-                                                                         ctypes.c_void_p]
-    fn.restype = ctypes.c_int
-    with torch.cuda.device(q.device):
-        _check("dense_causal_backward",
-               fn(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(cu), _ptr(out), _ptr(lse),
-                  _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), _nbytes(ws),
-                  _stream(q.device)))
+    _call("dense_causal_backward", q.device, p, _at(q), _at(k), _at(v), _at(cu), _at(out), _at(lse),
+          _at(dout), _at(dq), _at(dk), _at(dv), _at(ws), _nbytes(ws))
     return dq, dk, dv
-
-
-class _CacheStruct(ctypes.Structure):
-    _fields_ = [("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
-                ("max_pages", ctypes.c_int)] + [(n, ctypes.c_void_p) for n in
-                                                ("k", "v", "k_scale", "v_scale", "page_table",
-                                                 "seqlens")]
 
 
 class MobaCache(NamedTuple):
@@ -494,31 +527,33 @@ def moba_cache_alloc(num_pages: int, page_size: int, num_kv_heads: int, head_dim
                      *(s.view(torch.float8_e8m0fnu) for s in scales))
 
 
-def _check_cache(cache, heads: int, head_dim: int, page_table, seqlens, cu, rows: int):
-    """Shapes, types and devices of a call on a cache; returns its C description."""
+def _check_cache(cache, heads: int, head_dim: int, page_table, seqlens, cu, *others):
+    """Shapes, types and devices of a call on a cache (`others` share its device); returns its C
+    description."""
     k, v, ks, vs = cache
-    if k.dim() != 4 or k.shape[1] != heads or k.shape[3] != head_dim or v.shape != k.shape:
-        raise ValueError(f"cache codes {tuple(k.shape)}, {tuple(v.shape)} must be "
+    shape = k.shape
+    if len(shape) != 4 or shape[1] != heads or shape[3] != head_dim or v.shape != shape:
+        raise ValueError(f"cache codes {tuple(shape)}, {tuple(v.shape)} must be "
                          f"[pages, {heads}, page_size, {head_dim}]")
     if k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
         raise TypeError("cache codes must be float8_e4m3fn")
-    if ks.shape != k.shape[:3] or vs.shape != k.shape[:3]:
-        raise ValueError(f"cache scales must be {tuple(k.shape[:3])}")
+    if ks.shape != shape[:3] or vs.shape != shape[:3]:
+        raise ValueError(f"cache scales must be {tuple(shape[:3])}")
     if ks.dtype != torch.float8_e8m0fnu or vs.dtype != torch.float8_e8m0fnu:
         raise TypeError("cache scales must be float8_e8m0fnu")
-    page = k.shape[2]
+    page = shape[2]
     if page < 16 or page > 65536 or page & (page - 1):
         raise ValueError(f"page_size must be a power of two from 16 to 65536 (got {page})")
     if page_table.dim() != 2 or page_table.dtype != torch.int32:
         raise ValueError("page_table must be int32 [batch, max_pages]")
-    batch = page_table.shape[0]
+    batch, max_pages = page_table.shape
     if seqlens.shape != (batch,) or seqlens.dtype != torch.int32:
         raise ValueError(f"seqlens must be int32 [{batch}]")
     if cu.shape != (batch + 1,) or cu.dtype != torch.int32:
         raise ValueError(f"row offsets must be int32 [{batch + 1}]")
-    _check_inputs(k, v, ks, vs, page_table, seqlens, cu)
-    return _CacheStruct(k.shape[0], page, page_table.shape[1], k.data_ptr(), v.data_ptr(),
-                        ks.data_ptr(), vs.data_ptr(), page_table.data_ptr(), seqlens.data_ptr())
+    _check_inputs(k, v, ks, vs, page_table, seqlens, cu, *others)
+    return _CacheStruct(shape[0], page, max_pages, k.data_ptr(), v.data_ptr(), ks.data_ptr(),
+                        vs.data_ptr(), page_table.data_ptr(), seqlens.data_ptr())
 
 
 def _cache_params(batch, rows, hq, hkv, d, dtype, block_size, topk, max_seqlen,
@@ -549,8 +584,7 @@ def moba_cache_write(cache: MobaCache, k, v, page_table, seqlens, cu_new,
     are written too. page_table, seqlens, cu_new: int32 on the cache's device."""
     _check_qkv(k, k, v)
     n, hkv, d = k.shape
-    c = _check_cache(cache, hkv, d, page_table, seqlens, cu_new, n)
-    _check_inputs(cache.k, k, v, kbar)
+    c = _check_cache(cache, hkv, d, page_table, seqlens, cu_new, k, v, kbar)
     batch, longest, B = page_table.shape[0], 2**31 - 1, 1
     if kbar is not None:
         if block_size is None:
@@ -558,12 +592,7 @@ def moba_cache_write(cache: MobaCache, k, v, page_table, seqlens, cu_new,
         B = int(block_size)
         longest = _check_kbar(kbar, batch, hkv, d, B)
     p = _cache_params(batch, n, hkv, hkv, d, k.dtype, B, 1, longest)
-    fn = lib().moba_cache_write
-    fn.argtypes = [ctypes.POINTER(MobaParams), ctypes.POINTER(_CacheStruct)] + [ctypes.c_void_p] * 5
-    fn.restype = ctypes.c_int
-    with torch.cuda.device(k.device):
-        _check("moba_cache_write", fn(ctypes.byref(p), ctypes.byref(c), _ptr(k), _ptr(v),
-                                      _ptr(cu_new), _ptr(kbar), _stream(k.device)))
+    _call("moba_cache_write", k.device, p, c, _at(k), _at(v), _at(cu_new), _at(kbar))
 
 
 def moba_cache_read(cache: MobaCache, page_table, seqlens, cu_rows, total_rows: int,
@@ -575,23 +604,16 @@ def moba_cache_read(cache: MobaCache, page_table, seqlens, cu_rows, total_rows: 
     if cache.k.dim() != 4:
         raise ValueError("cache codes must be [pages, Hkv, page_size, d]")
     hkv, d = cache.k.shape[1], cache.k.shape[3]
-    c = _check_cache(cache, hkv, d, page_table, seqlens, cu_rows, total_rows)
-    p = _cache_params(page_table.shape[0], total_rows, hkv, hkv, d, dtype, 1, 1, 2**31 - 1)
-    res = []
     for x in (k, v):
-        if x is None:
-            x = torch.empty((total_rows, hkv, d), dtype=dtype, device=cache.k.device)
-        elif x.shape != (total_rows, hkv, d) or x.dtype != dtype:
+        if x is not None and (x.shape != (total_rows, hkv, d) or x.dtype != dtype):
             raise ValueError(f"k and v must be {(total_rows, hkv, d)} {dtype}")
-        res.append(x)
-    _check_inputs(cache.k, *res)
-    fn = lib().moba_cache_read
-    fn.argtypes = [ctypes.POINTER(MobaParams), ctypes.POINTER(_CacheStruct)] + [ctypes.c_void_p] * 4
-    fn.restype = ctypes.c_int
-    with torch.cuda.device(cache.k.device):
-        _check("moba_cache_read", fn(ctypes.byref(p), ctypes.byref(c), _ptr(cu_rows), _ptr(res[0]),
-                                     _ptr(res[1]), _stream(cache.k.device)))
-    return tuple(res)
+    c = _check_cache(cache, hkv, d, page_table, seqlens, cu_rows, k, v)
+    dev = cache.k.device
+    p = _cache_params(page_table.shape[0], total_rows, hkv, hkv, d, dtype, 1, 1, 2**31 - 1)
+    k = torch.empty((total_rows, hkv, d), dtype=dtype, device=dev) if k is None else k
+    v = torch.empty((total_rows, hkv, d), dtype=dtype, device=dev) if v is None else v
+    _call("moba_cache_read", dev, p, c, _at(cu_rows), _at(k), _at(v))
+    return k, v
 
 
 def moba_decode_cache(q, cache: MobaCache, page_table, seqlens, cu_q, kbar, block_size: int,
@@ -611,32 +633,21 @@ def moba_decode_cache(q, cache: MobaCache, page_table, seqlens, cu_q, kbar, bloc
         raise ValueError(f"{hq} q heads are not a multiple of {hkv} kv heads")
     if out is not None and (out.shape != q.shape or out.dtype != q.dtype):
         raise ValueError(f"out must be {tuple(q.shape)} {q.dtype}")
-    c = _check_cache(cache, hkv, d, page_table, seqlens, cu_q, n)
+    c = _check_cache(cache, hkv, d, page_table, seqlens, cu_q, q, kbar, out, ws)
     batch = page_table.shape[0]
     longest = _check_kbar(kbar, batch, hkv, d, block_size)
     if max_seqlen is None:
         max_seqlen = longest
     elif -(-max_seqlen // block_size) != kbar.shape[1]:
         raise ValueError(f"max_seqlen {max_seqlen} has not the {kbar.shape[1]} blocks of kbar")
-    _check_inputs(q, cache.k, kbar, out, ws)
-    L = lib()
+    dev = q.device
     p = _cache_params(batch, n, hq, hkv, d, q.dtype, block_size, topk, max_seqlen, shared_routing)
-    size = L.moba_decode_cache_workspace_size
-    size.argtypes, size.restype = [ctypes.POINTER(MobaParams)], ctypes.c_size_t
-    if ws is None:
-        ws = torch.empty(max(int(size(ctypes.byref(p))), 256), dtype=torch.uint8, device=q.device)
+    ws = _workspace("moba_decode_cache_workspace_size", p, dev, ws)
     out = torch.empty_like(q) if out is None else out
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
-    idx = (torch.empty((n, hq, topk), dtype=torch.int32, device=q.device) if return_idx
-           else None)
-    fn, V = L.moba_decode_cache, ctypes.c_void_p
-    fn.argtypes = [ctypes.POINTER(MobaParams), V, ctypes.POINTER(_CacheStruct), V, V, V, V, V, V,
-                   ctypes.c_size_t, V]
-    fn.restype = ctypes.c_int
-    with torch.cuda.device(q.device):
-        _check("moba_decode_cache", fn(ctypes.byref(p), _ptr(q), ctypes.byref(c), _ptr(cu_q),
-                                       _ptr(kbar), _ptr(out), _ptr(lse), _ptr(idx), _ptr(ws),
-                                       _nbytes(ws), _stream(q.device)))
+    lse = torch.empty((n, hq), dtype=torch.float32, device=dev) if return_lse else None
+    idx = torch.empty((n, hq, topk), dtype=torch.int32, device=dev) if return_idx else None
+    _call("moba_decode_cache", dev, p, _at(q), c, _at(cu_q), _at(kbar), _at(out), _at(lse), _at(idx),
+          _at(ws), _nbytes(ws))
     res = (out,)
     if return_lse:
         res += (lse,)

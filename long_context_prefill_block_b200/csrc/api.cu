@@ -356,8 +356,8 @@ DecLayout plan_decode(const Dims& dm, int n_queries) {
   return L;
 }
 
-// Split partials (o, then lse), index rows and arrival counters of a decode
-// step on the 8-bit cache.
+// Index rows and split partials (o, then lse) of a decode step on the 8-bit
+// cache.
 DecLayout plan_decode_cache(const Dims& dm) {
   DecLayout L{};
   const size_t rows = decode_cache_partial_rows(dm);
@@ -370,7 +370,6 @@ DecLayout plan_decode_cache(const Dims& dm) {
   L.idx = take(sizeof(int32_t) * (size_t)dm.T * dm.Hq * dm.topk);
   L.part_o = take(sizeof(float) * rows * dm.d);
   L.part_lse = take(sizeof(float) * rows);
-  L.arrivals = take(sizeof(int) * (size_t)dm.T * dm.Hq);
   L.total = off;
   return L;
 }
@@ -378,7 +377,7 @@ DecLayout plan_decode_cache(const Dims& dm) {
 size_t dense_bwd_bytes(const Dims& dm) { return align256(sizeof(float) * 2 * (size_t)dm.T * dm.Hq); }
 
 // Checks a cache description and fills the kernels' view of it.
-moba_status check_cache(const moba_cache* c, Cache& v) {
+moba_status check_cache(const moba_cache* c, int heads, Cache& v) {
   if (!c) return MOBA_ERR_INVALID_ARG;
   if (c->num_pages <= 0 || c->max_pages <= 0 || c->page_size < 16 || c->page_size > 65536 ||
       (c->page_size & (c->page_size - 1)))
@@ -397,6 +396,9 @@ moba_status check_cache(const moba_cache* c, Cache& v) {
   v.max_pages = c->max_pages;
   v.page_log2 = 0;
   while ((1 << v.page_log2) < c->page_size) ++v.page_log2;
+  // row numbers are 31-bit (2^31 rows would be 137 GB of K alone)
+  if (((int64_t)c->num_pages * heads) << v.page_log2 >= (int64_t(1) << 31))
+    return MOBA_ERR_UNSUPPORTED;
   return MOBA_OK;
 }
 
@@ -606,7 +608,7 @@ moba_status moba_cache_write(const moba_params* p, const moba_cache* c, const vo
   moba_status s = validate(p, dm);
   if (s != MOBA_OK) return s;
   if (dm.T == 0 || dm.batch == 0) return MOBA_OK;
-  if ((s = check_cache(c, cv)) != MOBA_OK) return s;
+  if ((s = check_cache(c, dm.Hkv, cv)) != MOBA_OK) return s;
   if (!k || !v || !cu_new || !aligned32(k) || !aligned32(v) || (kbar && !aligned32(kbar)))
     return MOBA_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -624,7 +626,7 @@ moba_status moba_cache_read(const moba_params* p, const moba_cache* c, const int
   moba_status s = validate(p, dm);
   if (s != MOBA_OK) return s;
   if (dm.T == 0 || dm.batch == 0) return MOBA_OK;
-  if ((s = check_cache(c, cv)) != MOBA_OK) return s;
+  if ((s = check_cache(c, dm.Hkv, cv)) != MOBA_OK) return s;
   if (!k || !v || !cu_rows || !aligned32(k) || !aligned32(v)) return MOBA_ERR_INVALID_ARG;
   int* status = status_word();
   if (!status) return MOBA_ERR_CUDA;
@@ -647,7 +649,7 @@ moba_status moba_decode_cache(const moba_params* p, const void* q, const moba_ca
   if (s != MOBA_OK) return s;
   if (dm.prefix) return MOBA_ERR_UNSUPPORTED;
   if (dm.T == 0 || dm.batch == 0) return MOBA_OK;
-  if ((s = check_cache(c, cv)) != MOBA_OK) return s;
+  if ((s = check_cache(c, dm.Hkv, cv)) != MOBA_OK) return s;
   if (!q || !cu_q || !kbar || !out || !aligned32(q) || !aligned32(kbar) || !aligned32(out))
     return MOBA_ERR_INVALID_ARG;
   const DecLayout L = plan_decode_cache(dm);
@@ -657,15 +659,10 @@ moba_status moba_decode_cache(const moba_params* p, const void* q, const moba_ca
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(ws);
   int32_t* rows = idx ? idx : reinterpret_cast<int32_t*>(base + L.idx);
-  int* arrivals = reinterpret_cast<int*>(base + L.arrivals);
-  // a request longer than its pages hold is skipped by the gate too
-  const int64_t held = (int64_t)cv.max_pages << cv.page_log2;
-  if (held < dm.max_seqlen) dm.max_seqlen = (int)held;  // dm.nb keeps kbar's layout
-  MOBA_TRY(launch_cache_gate(dm, q, kbar, cv.lens, cu_q, rows, arrivals, status, st));
-  return cuda_status(launch_cache_attn(dm, cv, q, cu_q, rows,
-                                       reinterpret_cast<float*>(base + L.part_o),
-                                       reinterpret_cast<float*>(base + L.part_lse), arrivals, out,
-                                       lse, status, st));
+  return cuda_status(launch_decode_cache(dm, cv, q, kbar, cu_q, rows,
+                                         reinterpret_cast<float*>(base + L.part_o),
+                                         reinterpret_cast<float*>(base + L.part_lse), out, lse,
+                                         status, st));
 }
 
 moba_status moba_device_status(void* stream, int clear) {

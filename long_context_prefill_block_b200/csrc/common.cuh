@@ -335,11 +335,13 @@ cudaError_t launch_cache_read(const Dims& dm, const Cache& c, const int32_t* cu_
 // The decode gate with cache lengths in place of packed offsets (decode.cu).
 cudaError_t launch_cache_gate(const Dims& dm, const void* q, const float* kbar,
                               const int32_t* seqlens, const int32_t* cu_q, int32_t* idx,
-                              int* arrivals, int* status, cudaStream_t st);
+                              int max_len, int* status, cudaStream_t st);
+// Decode over the cache: gate into idx, split attention into partials
+// [decode_cache_partial_rows] x (d + 1), their merge into out and lse.
 size_t decode_cache_partial_rows(const Dims& dm);
-cudaError_t launch_cache_attn(const Dims& dm, const Cache& c, const void* q, const int32_t* cu_q,
-                              const int32_t* idx, float* part_o, float* part_lse, int* arrivals,
-                              void* out, float* lse, int* status, cudaStream_t st);
+cudaError_t launch_decode_cache(const Dims& dm, const Cache& c, const void* q, const float* kbar,
+                                const int32_t* cu_q, int32_t* idx, float* part_o, float* part_lse,
+                                void* out, float* lse, int* status, cudaStream_t st);
 
 cudaError_t launch_merge(const Dims& dm, const Chunk& ch, const int32_t* idx, const int32_t* cu,
                          const Partials& pt, void* out, float* lse, cudaStream_t st);

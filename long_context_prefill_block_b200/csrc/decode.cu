@@ -79,7 +79,8 @@ template <typename T, int D, int KM, bool kPaged>
 __global__ void __launch_bounds__(kGateWarps * 32)
 decode_gate_kernel(Dims dm, const T* __restrict__ q, const float* __restrict__ kbar,
                    const int32_t* __restrict__ cu, const int32_t* __restrict__ cu_q,
-                   int32_t* __restrict__ idx, int* __restrict__ arrivals, int* status) {
+                   int32_t* __restrict__ idx, int* __restrict__ arrivals, int max_len,
+                   int* status) {
   __shared__ __align__(16) float qs[D];
   __shared__ float ws[kGateWarps][KM];
   __shared__ int wi[kGateWarps][KM];
@@ -88,7 +89,7 @@ decode_gate_kernel(Dims dm, const T* __restrict__ q, const float* __restrict__ k
   const int qi = blockIdx.x / H, u = blockIdx.x % H;
   int r, len, p;
   if constexpr (kPaged) {  // whole CTA
-    if (!tail_position(cu_q, cu, dm.batch, dm.max_seqlen, qi, r, p, len, status)) return;
+    if (!tail_position(cu_q, cu, dm.batch, max_len, qi, r, p, len, status)) return;
   } else {
     int64_t start;
     if (!decode_position(dm, cu, cu_q, qi, r, start, len, p, status)) return;
@@ -104,7 +105,7 @@ decode_gate_kernel(Dims dm, const T* __restrict__ q, const float* __restrict__ k
     qs[x] = s;
   }
   // the attention kernel's split counters of these rows start at zero
-  if (tid < nh) arrivals[(int64_t)qi * dm.Hq + h0 + tid] = 0;
+  if (!kPaged && tid < nh) arrivals[(int64_t)qi * dm.Hq + h0 + tid] = 0;
   __syncthreads();
   const int c = p / dm.B;
   float ts[KM];
@@ -472,26 +473,26 @@ decode_attn_kernel(Dims dm, const T* __restrict__ q, const T* __restrict__ k,
 
 template <typename T, int D, int KM, bool kPaged>
 cudaError_t run_gate_km(const Dims& dm, int nq, const void* q, const float* kbar, const int32_t* cu,
-                     const int32_t* cu_q, int32_t* idx, int* arrivals, int* status,
-                     cudaStream_t st) {
+                     const int32_t* cu_q, int32_t* idx, int* arrivals, int max_len,
+                     int* status, cudaStream_t st) {
   const int64_t items = (int64_t)nq * (dm.shared ? dm.Hkv : dm.Hq);
   if (items > INT32_MAX) return cudaErrorInvalidValue;
   decode_gate_kernel<T, D, KM, kPaged><<<(unsigned)items, kGateWarps * 32, 0, st>>>(
-      dm, static_cast<const T*>(q), kbar, cu, cu_q, idx, arrivals, status);
+      dm, static_cast<const T*>(q), kbar, cu, cu_q, idx, arrivals, max_len, status);
   return cudaGetLastError();
 }
 
 template <typename T, int D, bool kPaged>
 cudaError_t run_gate(const Dims& dm, int nq, const void* q, const float* kbar, const int32_t* cu,
-                     const int32_t* cu_q, int32_t* idx, int* arrivals, int* status,
-                     cudaStream_t st) {
+                     const int32_t* cu_q, int32_t* idx, int* arrivals, int max_len,
+                     int* status, cudaStream_t st) {
   const int need = dm.topk - 1;
-  if (need <= 1) return run_gate_km<T, D, 1, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
-  if (need <= 2) return run_gate_km<T, D, 2, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
-  if (need <= 4) return run_gate_km<T, D, 4, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
-  if (need <= 8) return run_gate_km<T, D, 8, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
-  if (need <= 16) return run_gate_km<T, D, 16, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
-  return run_gate_km<T, D, 32, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
+  if (need <= 1) return run_gate_km<T, D, 1, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, max_len, status, st);
+  if (need <= 2) return run_gate_km<T, D, 2, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, max_len, status, st);
+  if (need <= 4) return run_gate_km<T, D, 4, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, max_len, status, st);
+  if (need <= 8) return run_gate_km<T, D, 8, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, max_len, status, st);
+  if (need <= 16) return run_gate_km<T, D, 16, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, max_len, status, st);
+  return run_gate_km<T, D, 32, kPaged>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, max_len, status, st);
 }
 
 template <typename T, int D>
@@ -499,7 +500,7 @@ cudaError_t run(const Dims& dm, int nq, const void* q, const void* k, const void
                 const int32_t* cu, const int32_t* cu_q, const float* kbar, int32_t* idx,
                 float* part_o, float* part_lse, int* arrivals, void* out, float* lse, int* status,
                 cudaStream_t st) {
-  cudaError_t e = run_gate<T, D, false>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, status, st);
+  cudaError_t e = run_gate<T, D, false>(dm, nq, q, kbar, cu, cu_q, idx, arrivals, 0, status, st);
   if (e != cudaSuccess) return e;
   if ((int64_t)splits_per_row(dm) * nq > INT32_MAX) return cudaErrorInvalidValue;
   dim3 grid((unsigned)(splits_per_row(dm) * nq), (unsigned)dm.Hq);
@@ -513,15 +514,12 @@ cudaError_t run(const Dims& dm, int nq, const void* q, const void* k, const void
 
 cudaError_t launch_cache_gate(const Dims& dm, const void* q, const float* kbar,
                               const int32_t* seqlens, const int32_t* cu_q, int32_t* idx,
-                              int* arrivals, int* status, cudaStream_t st) {
-  if (dm.dtype == kBF16)
-    return dm.d == 128 ? run_gate<__nv_bfloat16, 128, true>(dm, dm.T, q, kbar, seqlens, cu_q, idx,
-                                                            arrivals, status, st)
-                       : run_gate<__nv_bfloat16, 64, true>(dm, dm.T, q, kbar, seqlens, cu_q, idx,
-                                                           arrivals, status, st);
-  return dm.d == 128
-             ? run_gate<float, 128, true>(dm, dm.T, q, kbar, seqlens, cu_q, idx, arrivals, status, st)
-             : run_gate<float, 64, true>(dm, dm.T, q, kbar, seqlens, cu_q, idx, arrivals, status, st);
+                              int max_len, int* status, cudaStream_t st) {
+  const auto run = dm.dtype == kBF16
+                       ? (dm.d == 128 ? run_gate<__nv_bfloat16, 128, true>
+                                      : run_gate<__nv_bfloat16, 64, true>)
+                       : (dm.d == 128 ? run_gate<float, 128, true> : run_gate<float, 64, true>);
+  return run(dm, dm.T, q, kbar, seqlens, cu_q, idx, nullptr, max_len, status, st);
 }
 
 size_t decode_partial_rows(const Dims& dm, int n_queries) {

@@ -1,32 +1,618 @@
-// Decode attention over the paged 8-bit cache (cache.cu): the decode step of
-// PaperTrace "2.1.3 MoBA", section 5.4, for the blocks that the gate chose
-// (launch_cache_gate). A query at position p reads the chosen earlier blocks
-// whole and its own block up to p, as one softmax (eq. 4-8); a key's scale
-// multiplies its logit and a value's scale its weight, so codes are widened
-// once and never rescaled.
+// Decode step over the paged 8-bit cache (cache.cu): PaperTrace "2.1.3 MoBA",
+// section 5.4. A query at position p reads the blocks that the gate chose and
+// its own block up to p, as one softmax (eq. 4-8); a key's scale multiplies
+// its logit and a value's scale its weight, so codes are widened once and
+// never rescaled.
 //
-// Split over the chosen keys: one CTA per (query, q head, chosen block, chunk
-// of at most 512 keys); the last split of a row to finish merges the row's
-// partials (no CTA waits for another).
+//   cache_gate_kernel  scores and top-k, a cluster of CTAs per (query, kv head)
+//   cache_attn_tc      bf16 queries: split over the chosen keys, codes by TMA
+//                      into each warp's own ring, products on the tensor core
+//   cache_attn_kernel  fp32 queries: the same split, fp32 FMA
+//
+// Bound by the bytes of the chosen rows: 2 (d + 1) a key. The last split of a
+// row to finish merges the row's partials (no CTA waits for another).
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <climits>
 #include <cmath>
 
-#include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace moba {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kSplit = 512;  // keys per split at most
-constexpr int kMaxPages = kSplit / 16 + 1;
+constexpr int kMaxSplit = 2048;  // keys per split at most
+constexpr int kMaxPages = kMaxSplit / 16 + 1;
 constexpr float kLog2e = 1.4426950408889634f;
 
-__host__ __device__ inline int split_keys(const Dims& dm) { return dm.B < kSplit ? dm.B : kSplit; }
-__host__ __device__ inline int splits_per_block(const Dims& dm) {
-  return (dm.B + split_keys(dm) - 1) / split_keys(dm);
+// Keys per split: small enough for two splits an SM, large enough that a
+// CTA's start (about 3 us) is small beside its keys.
+int split_keys(const Dims& dm) {
+  int k = 128;
+  while (k < kMaxSplit && k < dm.B &&
+         (int64_t)dm.T * dm.Hq * dm.topk * ((dm.B + 2 * k - 1) / (2 * k)) >= 4 * tc::sm_count())
+    k *= 2;
+  return k < dm.B ? k : dm.B;
 }
+
+// How a row's keys are divided: slot j (a chosen earlier block, or the own
+// block in the last slot) in spb splits of sk keys.
+struct Split {
+  int sk, spb, per_row;
+};
+Split split_of(const Dims& dm) {
+  const int sk = split_keys(dm), spb = (dm.B + sk - 1) / sk;
+  return {sk, spb, dm.topk * spb};
+}
+
+// A call's fixed facts, and where a query's row stands.
+struct Step {
+  Dims dm;
+  Cache c;
+  Split sp;
+  const int32_t* cu_q;
+  const int32_t* idx;
+  float* part_o;    // [row][split][d], normalised
+  float* part_lse;  // [row][split], base 2
+  int max_len;
+  int* status;
+};
+
+// Keys [lo, hi) of split s of a row at position p (empty: lo >= hi). Slots
+// before the last hold the chosen earlier blocks, the last one the own block.
+__device__ __forceinline__ void split_range(const Step& a, int64_t row, int s, int p, int& lo,
+                                            int& hi) {
+  const int B = a.dm.B, own = p / B, slot = s / a.sp.spb;
+  const int e = slot == a.dm.topk - 1 ? own : a.idx[row * a.dm.topk + slot];
+  lo = hi = 0;
+  if (slot == a.dm.topk - 1 || (e >= 0 && e < own)) {
+    lo = e * B + (s % a.sp.spb) * a.sp.sk;
+    hi = min(min(lo + a.sp.sk, (e + 1) * B), p + 1);
+  }
+}
+
+// First rows of the pages that hold keys [lo, hi) of request r, kv head g: -1
+// (and a status code) where the table names no page.
+template <int kThreads>
+__device__ __forceinline__ void load_pages(const Step& a, int r, int g, int lo, int hi,
+                                           int* page_row) {
+  const Cache& c = a.c;
+  const int p0 = lo >> c.page_log2, np = ((hi - 1) >> c.page_log2) - p0 + 1;
+  for (int i = threadIdx.x; i < np; i += kThreads) {
+    const int64_t row =
+        cache_page_row(c, a.dm.Hkv, c.table[(int64_t)r * c.max_pages + p0 + i], g);
+    page_row[i] = (int)row;  // rows of a cache fit 31 bits (checked on the host)
+    if (row < 0) set_status(a.status, kStBadIndices);
+  }
+}
+
+// ---- gate --------------------------------------------------------------------
+// Scores of the complete earlier blocks by their means, and the best k - 1 of
+// them (ties to the lower index, a NaN score never), in ascending order, then
+// the own block, then -1.
+//
+// One cluster per (query, kv head): its CTAs take equal ranges of the blocks, a
+// warp reads a mean as 16 bytes a lane and forms its product with every q row
+// of the group (one row, their sum, with shared routing), and the scores meet
+// in the first CTA's shared memory, where a warp a row picks the best by rounds
+// of arg-max. A mean is read once for the group's rows, not once a row, and no
+// thread walks a list alone: 39 -> GATE_US us for four queries at the
+// million-token cache (1 MB of means: latency, not bandwidth).
+constexpr int kGateThreads = 256;
+constexpr int kGateRows = 16;      // q rows of a group at a time
+constexpr int kGateBlocks = 1024;  // blocks whose scores fit: 64 KB
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// A float into the shared memory of CTA 0 of the cluster, at this CTA's address.
+__device__ __forceinline__ void store_first(float* p, float x) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(tc::smem_u32(p)));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kGateThreads)
+cache_gate_kernel(const Step a, const T* __restrict__ q, const float* __restrict__ kbar,
+                  int32_t* __restrict__ idx, const int cs) {
+  extern __shared__ __align__(16) float score[];  // [rows][c]
+  __shared__ __align__(16) float qs[kGateRows][D];
+  __shared__ uint32_t chosen[kGateRows][kGateBlocks / 32];
+  tc::grid_let_next();
+  const Dims& dm = a.dm;
+  const int grp = dm.Hq / dm.Hkv, chunks = dm.shared ? 1 : (grp + kGateRows - 1) / kGateRows;
+  const int rank = (int)cluster_rank(), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int unit = blockIdx.x / cs;
+  const int h_first = unit % chunks * kGateRows;
+  unit /= chunks;
+  const int g = unit % dm.Hkv, qi = unit / dm.Hkv;
+  int r, len, p;
+  if (!tail_position(a.cu_q, a.c.lens, dm.batch, a.max_len, qi, r, p, len, a.status)) return;
+  const int h0 = g * grp + h_first;
+  const int rows = dm.shared ? 1 : min(kGateRows, grp - h_first);
+  const int c = p / dm.B, need = min(dm.topk - 1, c);
+  if (need > 0) {
+    for (int e = tid; e < rows * D; e += kGateThreads) {
+      const T* src = q + ((int64_t)qi * dm.Hq + h0 + e / D) * D + e % D;
+      float s = to_f32(*src);
+      if (dm.shared)
+        for (int j = 1; j < grp; ++j) s += to_f32(src[j * D]);
+      qs[e / D][e % D] = s;
+    }
+    cluster_sync();  // also: CTA 0 runs, so its shared memory can be written
+    constexpr int LPB = D / 4, BPW = 32 / LPB, U = 4;  // lanes a mean, means a warp, steps in flight
+    const int sub = lane % LPB, per = (c + cs - 1) / cs;
+    const int first = rank * per, end = min(c, first + per), stride = kGateThreads / 32 * BPW;
+    for (int i0 = first + warp * BPW + lane / LPB; __any_sync(0xffffffffu, i0 < end);
+         i0 += stride * U) {
+      float4 kv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * stride;
+        kv[u] = i < end ? __ldg(reinterpret_cast<const float4*>(
+                                    kbar + (((int64_t)r * dm.nb + i) * dm.Hkv + g) * D) + sub)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      for (int j = 0; j < rows; ++j) {
+        const float4 qv = reinterpret_cast<const float4*>(qs[j])[sub];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float acc = fmaf(kv[u].w, qv.w, fmaf(kv[u].z, qv.z, fmaf(kv[u].y, qv.y, kv[u].x * qv.x)));
+#pragma unroll
+          for (int off = LPB / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+          if (sub == 0 && i0 + u * stride < end) store_first(&score[j * c + i0 + u * stride], acc);
+        }
+      }
+    }
+  }
+  cluster_sync();
+  if (rank != 0) return;
+  for (int j = warp; j < rows; j += kGateThreads / 32) {
+    const int words = (c + 31) / 32;
+    chosen[j][lane] = 0;  // kGateBlocks / 32 words, one a lane
+    __syncwarp();
+    float* sc = score + j * c;
+    int n = 0;
+    for (int k = 0; k < need; ++k) {
+      float bs = -INFINITY;
+      int bi = INT_MAX;
+      for (int i = lane; i < c; i += 32) {
+        const float s = sc[i];
+        if (s > bs || (s == bs && i < bi)) {
+          bs = s;
+          bi = i;
+        }
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        const float os = __shfl_xor_sync(0xffffffffu, bs, off);
+        const int oi = __shfl_xor_sync(0xffffffffu, bi, off);
+        if (os > bs || (os == bs && oi < bi)) {
+          bs = os;
+          bi = oi;
+        }
+      }
+      if (bi == INT_MAX) break;  // only NaN scores are left
+      if (lane == bi % 32) {
+        sc[bi] = NAN;
+        chosen[j][bi / 32] |= 1u << lane;
+      }
+      ++n;
+      __syncwarp();
+    }
+    // lane w holds the flags of blocks 32 w ..: write them in ascending order
+    uint32_t f = lane < words ? chosen[j][lane] : 0u;
+    int at = __popc(f);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, at, off);
+      if (lane >= off) at += o;
+    }
+    at -= __popc(f);
+    const int copies = dm.shared ? grp : 1;
+    for (int x = 0; x < copies; ++x) {
+      int32_t* row = idx + ((int64_t)qi * dm.Hq + h0 + (dm.shared ? x : j)) * dm.topk;
+      int o = at;
+      for (uint32_t m = f; m; m &= m - 1) row[o++] = lane * 32 + __ffs(m) - 1;
+      if (n + lane < dm.topk) row[n + lane] = lane == 0 ? c : -1;
+    }
+  }
+}
+
+// ---- bf16 queries ------------------------------------------------------------
+// One CTA per split: of one head for the chosen blocks (each head has its own),
+// of up to 8 heads of a kv head for the own block, which they share, and for
+// every block with shared routing. A warp owns steps of 32 keys, w, w + 4, ...;
+// codes come by TMA in tiles of 16 rows (never across a page: pages are 16 or
+// more, tiles are aligned to 16 positions) into the warp's ring of three
+// steps, so the bytes in flight do not cost registers.
+//
+// The products run on m16n8k16 f16 instructions: e4m3 widens to f16 exactly in
+// one conversion for two values, half of what fp32 FMA needs with its second
+// widening, and the 8 columns take the group's heads at no cost. (A tcgen05
+// product would want 64 or 128 query rows; a step here has 1 to 8.)
+//   S^T = K Q^T   A: 16 keys; a lane's 16-byte pieces of two rows are its A
+//                 registers as they come, d being permuted alike in Q
+//   O^T = V^T P^T A: 16 dims; pairs of keys interleaved by byte permutes; P
+//                 reaches the B layout by two 8 x 8 transposes
+// q is scaled to [1, 2) by a power of two a head, since f16 has a narrower
+// range than bf16: what drops out is 2^-24 of the largest entry. Weights are
+// rounded to f16 (half a step of 2^-11) relative to the largest weight times
+// value scale of the warp's keys so far; sums of weights stay fp32.
+constexpr int kW = 4;        // warps
+constexpr int kStages = 3;   // steps in a warp's ring
+constexpr int kStep = 32;    // keys a step
+constexpr int kHeads = 8;    // columns
+
+template <int D>
+struct Ring {
+  static constexpr int kTile = 16 * D;             // 16 rows of codes
+  static constexpr int kStage = 4 * kTile;         // K and V of a step
+  static constexpr int kBytes = kW * kStages * kStage;
+};
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float max_over_keys(float x) {  // over the 8 lanes of a column
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+// 2^(x - ref), ref being the largest x or -inf where there is none yet.
+__device__ __forceinline__ float weight(float x, float ref) {
+  return tc::ex2(x - (ref == -INFINITY ? 0.f : ref));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kW * 32)
+cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+              const Step a, const __nv_bfloat16* __restrict__ q) {
+  extern __shared__ __align__(1024) uint8_t ring[];
+  __shared__ uint64_t full[kW][kStages];
+  __shared__ __align__(16) uint8_t scales[kW][kStages][2][kStep];
+  __shared__ int page_row[kMaxPages + 1];
+  __shared__ float wm[kW][kHeads], wo[kW][kHeads], wl[kW][kHeads];
+  __shared__ int abort_flag;
+  constexpr int NC = D / 64;  // 16-byte pieces of a row a lane holds
+  using R = Ring<D>;
+  tc::grid_let_next();
+  const Dims& dm = a.dm;
+  const Cache& cc = a.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r8 = lane >> 2, c4 = lane & 3;
+  if (warp == 0 && lane < 2) tc::prefetch_map(lane ? &tmv : &tmk);
+  // ---- which split, of which heads
+  const int grp = dm.Hq / dm.Hkv, hc = (grp + kHeads - 1) / kHeads;
+  const int n_hist = dm.shared ? 0 : dm.Hq * (dm.topk - 1) * a.sp.spb;
+  const int n_group = dm.Hkv * hc * (dm.shared ? a.sp.per_row : a.sp.spb);
+  const int qi = blockIdx.x / (n_hist + n_group);
+  int u = blockIdx.x % (n_hist + n_group), h0, nh, s;
+  if (u < n_group) {
+    const int per = dm.shared ? a.sp.per_row : a.sp.spb;
+    s = u % per + (a.sp.per_row - per);
+    u /= per;
+    h0 = u / hc * grp + u % hc * kHeads;
+    nh = min(kHeads, grp - u % hc * kHeads);
+  } else {
+    u -= n_group;
+    s = u % ((dm.topk - 1) * a.sp.spb);
+    h0 = u / ((dm.topk - 1) * a.sp.spb);
+    nh = 1;
+  }
+  const int g = h0 / grp;
+  const int64_t row0 = (int64_t)qi * dm.Hq + h0;
+  int r, len, p;
+  const bool valid =
+      tail_position(a.cu_q, cc.lens, dm.batch, a.max_len, qi, r, p, len, nullptr);
+  // ---- q of head r8: this lane's pieces, f16, scaled into [1, 2)
+  uint32_t qf[NC * 8];
+  float qe = 0.f;  // what head r8's logits are multiplied by
+  {
+    float x[NC * 16], top = 0.f;
+#pragma unroll
+    for (int m = 0; m < NC; ++m) {
+      const __nv_bfloat16* src = q + (row0 + (r8 < nh ? r8 : 0)) * D + (c4 * NC + m) * 16;
+      Vec16<__nv_bfloat16>::load(src, x + m * 16);
+      Vec16<__nv_bfloat16>::load(src + 8, x + m * 16 + 8);
+    }
+#pragma unroll
+    for (int i = 0; i < NC * 16; ++i) {
+      if (r8 >= nh) x[i] = 0.f;
+      top = fmaxf(top, fabsf(x[i]));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    int e = (int)(__float_as_uint(top) >> 23) - 127;
+    e = e == 128 || top == 0.f ? 0 : min(max(e, -126), 126);  // infinite, or nothing to scale
+    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+    qe = __uint_as_float((uint32_t)(127 + e) << 23) * (kLog2e * rsqrtf((float)D));
+#pragma unroll
+    for (int i = 0; i < NC * 8; ++i) {
+      const __half2 h = __floats2half2_rn(x[2 * i] * f, x[2 * i + 1] * f);
+      qf[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  // of this lane's two columns
+  const float qe0 = __shfl_sync(0xffffffffu, qe, c4 * 8), qe1 = __shfl_sync(0xffffffffu, qe, c4 * 8 + 4);
+  if (lane == 0)
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[warp][i], 1);
+  if (tid == 0) abort_flag = 0;
+  tc::mbar_fence_init();
+  tc::grid_wait();  // the chosen blocks
+  int lo = 0, hi = 0;
+  if (valid) split_range(a, row0, s, p, lo, hi);
+  if (lo >= hi) {  // no keys (uniform over the CTA)
+    if (valid && tid < nh) a.part_lse[(row0 + tid) * a.sp.per_row + s] = -INFINITY;
+    return;
+  }
+  const int t0 = lo & ~15;
+  load_pages<kW * 32>(a, r, g, t0, hi, page_row);
+  __syncthreads();
+  const uint32_t base = tc::smem_u32(ring) + warp * kStages * R::kStage;
+  const int n_steps = (hi - t0 + kStep - 1) / kStep, p0 = t0 >> cc.page_log2;
+  const int mask = (1 << cc.page_log2) - 1;
+  // the cache row that 16 keys from pos begin at, or -1: nothing to read
+  auto tile_row = [&](int pos) {
+    if (pos >= hi) return -1;
+    const int pr = page_row[(pos >> cc.page_log2) - p0];
+    return pr < 0 ? -1 : pr + (pos & mask);
+  };
+  auto request = [&](int i, int st) {  // lane 0: the loads of step i
+    int at[2];
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      at[t] = tile_row(t0 + i * kStep + t * 16);
+      if (at[t] >= 0) bytes += 2 * R::kTile + 32;
+    }
+    uint64_t* bar = &full[warp][st];
+    tc::mbar_expect_tx(bar, bytes);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (at[t] < 0) continue;
+      const uint32_t dst = base + st * R::kStage + t * R::kTile;
+      tc::tma_load_2d(dst, &tmk, bar, 0, at[t]);
+      tc::tma_load_2d(dst + 2 * R::kTile, &tmv, bar, 0, at[t]);
+      tc::bulk_load(tc::smem_u32(&scales[warp][st][0][t * 16]), cc.ks + at[t], 16, bar);
+      tc::bulk_load(tc::smem_u32(&scales[warp][st][1][t * 16]), cc.vs + at[t], 16, bar);
+    }
+  };
+  if (lane == 0)
+    for (int x = 0; x < kStages && warp + x * kW < n_steps; ++x) request(warp + x * kW, x);
+  volatile int* abort = &abort_flag;
+  float m0 = -INFINITY, m1 = -INFINITY, o0 = -INFINITY, o1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  float acc[D / 16][4];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc[i][x] = 0.f;
+  int n = 0;  // steps of this warp so far
+  bool ok = true;
+  for (int i = warp; i < n_steps; i += kW, ++n) {
+    const int st = n % kStages;
+    ok = tc::mbar_wait(&full[warp][st], n / kStages & 1, abort, a.status);
+    if (!__all_sync(0xffffffffu, ok)) {
+      ok = false;
+      break;
+    }
+    const uint32_t sK = base + st * R::kStage, sV = sK + 2 * R::kTile;
+    const uint8_t* ksb = scales[warp][st][0];
+    const uint8_t* vsb = scales[warp][st][1];
+    // ---- logits, base 2: keys r8 and r8 + 8 of two tiles, columns 2 c4 and 2 c4 + 1
+    float x[2][2][2], ev[2][2];
+    bool on[2][2];
+    bool whole = true;  // every key of the step counts (uniform over the warp)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int pos = t0 + i * kStep + t * 16;
+      const bool there = tile_row(pos) >= 0;
+      whole = whole && there && pos >= lo && pos + 16 <= hi;
+      float sc[4] = {0.f, 0.f, 0.f, 0.f};
+      uint4 k0[NC], k1[NC];
+#pragma unroll
+      for (int m = 0; m < NC; ++m) {
+        const int piece = c4 * NC + m;
+        const uint32_t at = sK + t * R::kTile + r8 * D +
+                            ((D == 128 ? piece ^ r8 : piece ^ (r8 >> 1 & 3)) << 4);
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(k0[m].x), "=r"(k0[m].y), "=r"(k0[m].z), "=r"(k0[m].w)
+                     : "r"(at));
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(k1[m].x), "=r"(k1[m].y), "=r"(k1[m].z), "=r"(k1[m].w)
+                     : "r"(at + 8 * D));
+      }
+#pragma unroll
+      for (int m = 0; m < NC; ++m) {
+        const uint32_t w0[4] = {k0[m].x, k0[m].y, k0[m].z, k0[m].w};
+        const uint32_t w1[4] = {k1[m].x, k1[m].y, k1[m].z, k1[m].w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t fa[4] = {e4m3x2_to_f16x2(w0[w] & 0xffff), e4m3x2_to_f16x2(w1[w] & 0xffff),
+                                  e4m3x2_to_f16x2(w0[w] >> 16), e4m3x2_to_f16x2(w1[w] >> 16)};
+          mma16816(sc, fa, qf[m * 8 + w * 2], qf[m * 8 + w * 2 + 1]);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int kp = pos + r8 + 8 * y;
+        on[t][y] = there && kp >= lo && kp < hi;
+        const float ks = e8m0_value(ksb[t * 16 + r8 + 8 * y]);
+        const uint32_t vb = vsb[t * 16 + r8 + 8 * y];
+        ev[t][y] = vb == 255 ? NAN : (float)((int)vb - 127);
+        x[t][y][0] = on[t][y] ? sc[2 * y] * qe0 * ks : -INFINITY;
+        x[t][y][1] = on[t][y] ? sc[2 * y + 1] * qe1 * ks : -INFINITY;
+      }
+    }
+    // ---- running maxima: of the logits, and of logit + value exponent
+    float n0 = -INFINITY, n1 = -INFINITY, y0 = -INFINITY, y1 = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        n0 = fmaxf(n0, x[t][y][0]);
+        n1 = fmaxf(n1, x[t][y][1]);
+        if (on[t][y]) {
+          y0 = fmaxf(y0, x[t][y][0] + ev[t][y]);
+          y1 = fmaxf(y1, x[t][y][1] + ev[t][y]);
+        }
+      }
+    n0 = fmaxf(m0, max_over_keys(n0));
+    n1 = fmaxf(m1, max_over_keys(n1));
+    y0 = fmaxf(o0, max_over_keys(y0));
+    y1 = fmaxf(o1, max_over_keys(y1));
+    if (m0 != -INFINITY) l0 *= tc::ex2(m0 - n0);
+    if (m1 != -INFINITY) l1 *= tc::ex2(m1 - n1);
+    if (__any_sync(0xffffffffu, (y0 != o0 && o0 != -INFINITY) || (y1 != o1 && o1 != -INFINITY))) {
+      const float f0 = o0 == -INFINITY ? 1.f : tc::ex2(o0 - y0);
+      const float f1 = o1 == -INFINITY ? 1.f : tc::ex2(o1 - y1);
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        acc[d][0] *= f0;
+        acc[d][1] *= f1;
+        acc[d][2] *= f0;
+        acc[d][3] *= f1;
+      }
+    }
+    m0 = n0;
+    m1 = n1;
+    o0 = y0;
+    o1 = y1;
+    // ---- weights, and their products with the values
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      uint32_t b[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        l0 += on[t][y] ? weight(x[t][y][0], m0) : 0.f;
+        l1 += on[t][y] ? weight(x[t][y][1], m1) : 0.f;
+        const float p0f = on[t][y] ? weight(x[t][y][0] + ev[t][y], o0) : 0.f;
+        const float p1f = on[t][y] ? weight(x[t][y][1] + ev[t][y], o1) : 0.f;
+        const __half2 h = __floats2half2_rn(p0f, p1f);
+        b[y] = transpose8(*reinterpret_cast<const uint32_t*>(&h));
+      }
+      // keys 2 c4, 2 c4 + 1 and 8 further; dims r8 * D / 8 ..
+      uint32_t v[4][NC * 2];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int key = 2 * c4 + (y & 1) + (y >> 1) * 8;
+        const uint32_t at = sV + t * R::kTile + key * D;
+        if constexpr (D == 128)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[y][0]), "=r"(v[y][1]), "=r"(v[y][2]), "=r"(v[y][3])
+                       : "r"(at + ((r8 ^ (key & 7)) << 4)));
+        else
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                       : "=r"(v[y][0]), "=r"(v[y][1])
+                       : "r"(at + (((r8 >> 1) ^ (key >> 1 & 3)) << 4) + (r8 & 1) * 8));
+        if (!whole) {  // zero weights do not silence NaN codes behind a request
+          const int kp = t0 + i * kStep + t * 16 + key;
+          const bool in = kp >= lo && kp < hi && tile_row(t0 + i * kStep + t * 16) >= 0;
+#pragma unroll
+          for (int w = 0; w < NC * 2; ++w) v[y][w] = in ? v[y][w] : 0u;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < NC * 2; ++w) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const uint32_t pick = z ? 0x7362u : 0x5140u;
+          const uint32_t ab = __byte_perm(v[0][w], v[1][w], pick);
+          const uint32_t cd = __byte_perm(v[2][w], v[3][w], pick);
+          const uint32_t fa[4] = {e4m3x2_to_f16x2(ab & 0xffff), e4m3x2_to_f16x2(ab >> 16),
+                                  e4m3x2_to_f16x2(cd & 0xffff), e4m3x2_to_f16x2(cd >> 16)};
+          mma16816(acc[w * 2 + z], fa, b[0], b[1]);
+        }
+      }
+    }
+    __syncwarp();  // the step's buffers are free
+    const int next = i + kStages * kW;
+    if (lane == 0 && next < n_steps) request(next, st);
+  }
+  if (!ok) {  // let the copies already issued land before the CTA exits
+    for (int x = 0; x < kStages; ++x)
+      if (warp + (n + x) * kW < n_steps)
+        tc::mbar_drain(&full[warp][(n + x) % kStages], (n + x) / kStages & 1);
+  }
+  // ---- the warps' results, in their own rings
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 4);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 4);
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 8);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 8);
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 16);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 16);
+  float* res = reinterpret_cast<float*>(ring + warp * kStages * R::kStage);  // [head][D]
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d) {
+    const int dim = r8 * (D / 8) + 2 * d;
+    if (2 * c4 < nh)
+      *reinterpret_cast<float2*>(res + 2 * c4 * D + dim) = make_float2(acc[d][0], acc[d][2]);
+    if (2 * c4 + 1 < nh)
+      *reinterpret_cast<float2*>(res + (2 * c4 + 1) * D + dim) = make_float2(acc[d][1], acc[d][3]);
+  }
+  if (r8 == 0) {
+    wm[warp][2 * c4] = m0;
+    wm[warp][2 * c4 + 1] = m1;
+    wo[warp][2 * c4] = o0;
+    wo[warp][2 * c4 + 1] = o1;
+    wl[warp][2 * c4] = l0;
+    wl[warp][2 * c4 + 1] = l1;
+  }
+  __syncthreads();
+  if (*abort) return;
+  for (int e = tid; e < nh * (D / 4); e += kW * 32) {
+    const int h = e / (D / 4), d4 = e % (D / 4);
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) M = fmaxf(M, wm[w][h]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      // a warp without keys has sums 0 (or NaN, which has to show)
+      L += wl[w][h] * (wm[w][h] == -INFINITY ? 1.f : tc::ex2(wm[w][h] - M));
+      const float f = wo[w][h] == -INFINITY ? 1.f : exp2f(wo[w][h] - M);
+      const float4 v = reinterpret_cast<const float4*>(
+          ring + w * kStages * R::kStage)[h * (D / 4) + d4];
+      o.x = fmaf(v.x, f, o.x);
+      o.y = fmaf(v.y, f, o.y);
+      o.z = fmaf(v.z, f, o.z);
+      o.w = fmaf(v.w, f, o.w);
+    }
+    const int64_t at = (row0 + h) * a.sp.per_row + s;
+    const bool none = M == -INFINITY && L == 0.f;  // bad pages only
+    const float inv = 1.f / L;
+    if (!none)
+      reinterpret_cast<float4*>(a.part_o + at * D)[d4] =
+          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (d4 == 0) a.part_lse[at] = none ? -INFINITY : L != L ? L : M + log2f(L);
+  }
+}
+
+// ---- fp32 queries ------------------------------------------------------------
+// One CTA per (query, q head, split), a row's 16 codes a lane, fp32 FMA.
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 
 __device__ __forceinline__ void decode16(const uint4& r, float (&x)[16]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -42,223 +628,291 @@ __device__ __forceinline__ void decode16(const uint4& r, float (&x)[16]) {
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
-cache_attn_kernel(Dims dm, Cache c, const T* __restrict__ q, const int32_t* __restrict__ cu_q,
-                  const int32_t* __restrict__ idx, float* __restrict__ part_o,
-                  float* __restrict__ part_lse, int* __restrict__ arrivals, T* __restrict__ out,
-                  float* __restrict__ lse_out, int* status) {
+cache_attn_kernel(const Step a, const float* __restrict__ q) {
   constexpr int LPK = D / 16, GPW = 32 / LPK, G = GPW * kWarps, U = 4;
   __shared__ float wm[kWarps], wl[kWarps];
   __shared__ __align__(16) float wo[kWarps][D];
-  __shared__ int64_t page_row[kMaxPages];
-  __shared__ int last;
-  const int spb = splits_per_block(dm), S = dm.topk * spb;
+  __shared__ int page_row[kMaxPages + 1];
+  tc::grid_let_next();
+  const Dims& dm = a.dm;
+  const Cache& c = a.c;
+  const int S = a.sp.per_row;
   const int s = (int)(blockIdx.x % S), qi = (int)(blockIdx.x / S), h = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = (int64_t)qi * dm.Hq + h, prow = row * S + s;
-  const int64_t held = (int64_t)c.max_pages << c.page_log2;
-  const int max_len = held < dm.max_seqlen ? (int)held : dm.max_seqlen;
-  int r, len, p;
-  if (!tail_position(cu_q, c.lens, dm.batch, max_len, qi, r, p, len, status)) return;
-  const int g = h / (dm.Hq / dm.Hkv), own = p / dm.B;
-  int lo = 0, hi = 0;
-  const int e = idx[row * dm.topk + s / spb];
-  if (e >= 0 && e <= own) {
-    lo = e * dm.B + (s % spb) * split_keys(dm);
-    hi = min(min(lo + split_keys(dm), (e + 1) * dm.B), p + 1);
-  }
+  int r, len, p, lo = 0, hi = 0;
+  const bool valid = tail_position(a.cu_q, c.lens, dm.batch, a.max_len, qi, r, p, len, nullptr);
+  tc::grid_wait();  // the chosen blocks
+  if (!valid) return;
+  split_range(a, row, s, p, lo, hi);
   if (lo >= hi) {
-    if (tid == 0) part_lse[prow] = -INFINITY;
-  } else {
-    const int p0 = lo >> c.page_log2, np = ((hi - 1) >> c.page_log2) - p0 + 1;
-    for (int i = tid; i < np; i += kThreads) {
-      page_row[i] = cache_page_row(c, dm.Hkv, c.table[(int64_t)r * c.max_pages + p0 + i], g);
-      if (page_row[i] < 0) set_status(status, kStBadIndices);
+    if (tid == 0) a.part_lse[prow] = -INFINITY;
+    return;
+  }
+  const int g = h / (dm.Hq / dm.Hkv), p0 = lo >> c.page_log2;
+  load_pages<kThreads>(a, r, g, lo, hi, page_row);
+  const int grp_id = warp * GPW + lane / LPK, sub = lane % LPK;
+  const float sl2 = kLog2e * rsqrtf((float)D);
+  float qv[16];
+#pragma unroll
+  for (int x = 0; x < 16; ++x) qv[x] = q[row * D + sub * 16 + x] * sl2;
+  float m = -INFINITY, l = 0.f, o[16];
+#pragma unroll
+  for (int x = 0; x < 16; ++x) o[x] = 0.f;
+  const int mask = (1 << c.page_log2) - 1;
+  __syncthreads();
+  for (int base = lo; base < hi; base += U * G) {
+    uint4 kr[U], vr[U];
+    float ks[U], vs[U];
+    bool on[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = base + grp_id + u * G;
+      const int jj = j < hi ? j : lo;
+      const int pr = page_row[(jj >> c.page_log2) - p0];
+      on[u] = j < hi && pr >= 0;
+      const int64_t at = pr < 0 ? 0 : pr + (jj & mask);
+      kr[u] = __ldg(reinterpret_cast<const uint4*>(c.k + at * D + sub * 16));
+      vr[u] = __ldg(reinterpret_cast<const uint4*>(c.v + at * D + sub * 16));
+      ks[u] = e8m0_value(__ldg(c.ks + at));
+      vs[u] = e8m0_value(__ldg(c.vs + at));
     }
-    const int grp_id = warp * GPW + lane / LPK, sub = lane % LPK;
-    const float sl2 = kLog2e * rsqrtf((float)D);
-    float qv[16];
+    float d[U], mn = m;
 #pragma unroll
-    for (int x = 0; x < 16; ++x) qv[x] = to_f32(q[row * D + sub * 16 + x]) * sl2;
-    float m = -INFINITY, l = 0.f, o[16];
-#pragma unroll
-    for (int x = 0; x < 16; ++x) o[x] = 0.f;
-    const int mask = (1 << c.page_log2) - 1;
-    __syncthreads();
-    for (int base = lo; base < hi; base += U * G) {
-      uint4 kr[U], vr[U];
-      float ks[U], vs[U];
-      bool on[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = base + grp_id + u * G;
-        const int jj = j < hi ? j : lo;
-        const int64_t pr = page_row[(jj >> c.page_log2) - p0];
-        on[u] = j < hi && pr >= 0;
-        const int64_t at = pr < 0 ? 0 : pr + (jj & mask);
-        kr[u] = __ldg(reinterpret_cast<const uint4*>(c.k + at * D + sub * 16));
-        vr[u] = __ldg(reinterpret_cast<const uint4*>(c.v + at * D + sub * 16));
-        ks[u] = e8m0_value(__ldg(c.ks + at));
-        vs[u] = e8m0_value(__ldg(c.vs + at));
-      }
-      float d[U], mn = m;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float x[16];
-        decode16(kr[u], x);
-        float acc = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc = fmaf(qv[i], x[i], acc);
-#pragma unroll
-        for (int off = LPK / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-        d[u] = on[u] ? acc * ks[u] : -INFINITY;
-        mn = fmaxf(mn, d[u]);
-      }
-      if (mn == -INFINITY) {
-        // nothing to weigh in this step, but a NaN logit must not be lost
-        float bad = 0.f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) bad += on[u] && d[u] != d[u] ? d[u] : 0.f;
-        l += bad;
-        continue;
-      }
-      const float corr = exp2f(m - mn);
-      l *= corr;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] *= corr;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float w = on[u] ? exp2f(d[u] - mn) : 0.f;
-        l += w;
-        const float wv = on[u] ? w * vs[u] : 0.f;
-        float x[16];
-        decode16(vr[u], x);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = fmaf(wv, x[i], o[i]);
-      }
-      m = mn;
-    }
-    // merge the lane groups of the warp, then the warps
-#pragma unroll
-    for (int off = LPK; off < 32; off <<= 1) {
-      const float mo = __shfl_xor_sync(0xffffffffu, m, off);
-      const float lo2 = __shfl_xor_sync(0xffffffffu, l, off);
-      const float mn = fmaxf(m, mo);
-      const float a = m == -INFINITY ? 1.f : exp2f(m - mn);
-      const float b = mo == -INFINITY ? 1.f : exp2f(mo - mn);
-      l = l * a + lo2 * b;
-#pragma unroll
-      for (int x = 0; x < 16; ++x) o[x] = o[x] * a + __shfl_xor_sync(0xffffffffu, o[x], off) * b;
-      m = mn;
-    }
-    if (lane < LPK) {
-#pragma unroll
-      for (int x = 0; x < 16; ++x) wo[warp][sub * 16 + x] = o[x];
-      if (lane == 0) {
-        wm[warp] = m;
-        wl[warp] = l;
-      }
-    }
-    __syncthreads();
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w]);
-    float L = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) L += wl[w] * (wm[w] == -INFINITY ? 1.f : exp2f(wm[w] - M));
-    // a split all of whose keys weigh nothing (bad pages) leaves no partial;
-    // one with a NaN logit leaves NaN
-    const bool none = M == -INFINITY && L == 0.f;
-    for (int x = tid; x < D && !none; x += kThreads) {
+    for (int u = 0; u < U; ++u) {
+      float x[16];
+      decode16(kr[u], x);
       float acc = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        acc = fmaf(wo[w][x], wm[w] == -INFINITY ? 1.f : exp2f(wm[w] - M), acc);
-      part_o[prow * D + x] = acc / L;
-    }
-    if (tid == 0)
-      part_lse[prow] = none ? -INFINITY : L != L ? L : (M + log2f(L)) * 0.6931471805599453f;
-  }
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) last = atomicAdd(&arrivals[row], 1) == S - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  // the row's partials by eq. (7)-(8): w_s = exp(lse_s - max), in split order
-  const float* ls = part_lse + row * S;
-  float M = -INFINITY;
-  for (int s2 = tid; s2 < S; s2 += kThreads) M = fmaxf(M, __ldcg(ls + s2));
+      for (int i = 0; i < 16; ++i) acc = fmaf(qv[i], x[i], acc);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if (lane == 0) wm[warp] = M;
+      for (int off = LPK / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+      d[u] = on[u] ? acc * ks[u] : -INFINITY;
+      mn = fmaxf(mn, d[u]);
+    }
+    if (mn == -INFINITY) {
+      // nothing to weigh in this step, but a NaN logit must not be lost
+#pragma unroll
+      for (int u = 0; u < U; ++u) l += on[u] && d[u] != d[u] ? d[u] : 0.f;
+      continue;
+    }
+    const float corr = exp2f(m - mn);
+    l *= corr;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] *= corr;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = on[u] ? exp2f(d[u] - mn) : 0.f;
+      l += w;
+      const float wv = on[u] ? w * vs[u] : 0.f;
+      float x[16];
+      decode16(vr[u], x);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = on[u] ? fmaf(wv, x[i], o[i]) : o[i];
+    }
+    m = mn;
+  }
+  // merge the lane groups of the warp, then the warps
+#pragma unroll
+  for (int off = LPK; off < 32; off <<= 1) {
+    const float mo = __shfl_xor_sync(0xffffffffu, m, off);
+    const float lo2 = __shfl_xor_sync(0xffffffffu, l, off);
+    const float mn = fmaxf(m, mo);
+    const float fa = m == -INFINITY ? 1.f : exp2f(m - mn);
+    const float fb = mo == -INFINITY ? 1.f : exp2f(mo - mn);
+    l = l * fa + lo2 * fb;
+#pragma unroll
+    for (int x = 0; x < 16; ++x) o[x] = o[x] * fa + __shfl_xor_sync(0xffffffffu, o[x], off) * fb;
+    m = mn;
+  }
+  if (lane < LPK) {
+#pragma unroll
+    for (int x = 0; x < 16; ++x) wo[warp][sub * 16 + x] = o[x];
+    if (lane == 0) {
+      wm[warp] = m;
+      wl[warp] = l;
+    }
+  }
   __syncthreads();
+  float M = -INFINITY;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w]);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float Lw = 0.f;
-  const bool cols = lane * 4 < D;
-#pragma unroll 4
-  for (int s2 = warp; s2 < S; s2 += kWarps) {
-    const float lv = __ldcg(ls + s2);
-    const bool on = lv != -INFINITY;  // NaN counts: it has to show
-    const float w = on ? expf(lv - M) : 0.f;
-    Lw += w;
-    if (cols) {
-      const float4 ov = __ldcg(reinterpret_cast<const float4*>(part_o + (row * S + s2) * D) + lane);
-      acc.x += on ? w * ov.x : 0.f;
-      acc.y += on ? w * ov.y : 0.f;
-      acc.z += on ? w * ov.z : 0.f;
-      acc.w += on ? w * ov.w : 0.f;
-    }
-  }
-  __syncthreads();
-  if (cols) *reinterpret_cast<float4*>(&wo[warp][lane * 4]) = acc;
-  if (lane == 0) wl[warp] = Lw;
-  __syncthreads();
-  for (int x = tid; x < D; x += kThreads) {
-    float O = 0.f, L = 0.f;
+  float L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kWarps; ++w) L += wl[w] * (wm[w] == -INFINITY ? 1.f : exp2f(wm[w] - M));
+  // a split all of whose keys weigh nothing (bad pages) leaves no partial;
+  // one with a NaN logit leaves NaN
+  const bool none = M == -INFINITY && L == 0.f;
+  for (int x = tid; x < D && !none; x += kThreads) {
+    float acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      acc = fmaf(wo[w][x], wm[w] == -INFINITY ? 1.f : exp2f(wm[w] - M), acc);
+    a.part_o[prow * D + x] = acc / L;
+  }
+  if (tid == 0) a.part_lse[prow] = none ? -INFINITY : L != L ? L : M + log2f(L);
+}
+
+// ---- a row's partials --------------------------------------------------------
+// Eq. (7)-(8) written with lse: w_s = 2^(lse_s - max), o = sum w_s o_s / sum w_s,
+// in a fixed order. One CTA per row; warp w takes splits w, w + 4, ...
+constexpr int kMergeWarps = 4;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+cache_merge_kernel(const Step a, T* __restrict__ out, float* __restrict__ lse_out) {
+  __shared__ float wl[kMergeWarps];
+  __shared__ __align__(16) float wo[kMergeWarps][D];
+  constexpr int E = D / 32;
+  const int64_t row = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = a.sp.per_row;
+  int r, len, p;
+  const bool valid = tail_position(a.cu_q, a.c.lens, a.dm.batch, a.max_len,
+                                   (int)(row / a.dm.Hq), r, p, len, nullptr);
+  tc::grid_wait();  // the partials
+  if (!valid) return;
+  const float* ls = a.part_lse + row * S;
+  float M = -INFINITY;
+  for (int s = lane; s < S; s += 32) M = fmaxf(M, ls[s]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float acc[E], L = 0.f;
+#pragma unroll
+  for (int x = 0; x < E; ++x) acc[x] = 0.f;
+#pragma unroll 4
+  for (int s = warp; s < S; s += kMergeWarps) {
+    const float lv = ls[s];
+    if (lv == -INFINITY) continue;  // its partial was never written; NaN counts: it has to show
+    const float w = exp2f(lv - M);
+    L += w;
+    const float* src = a.part_o + (row * S + s) * D + lane * E;
+#pragma unroll
+    for (int x = 0; x < E; ++x) acc[x] = fmaf(w, src[x], acc[x]);
+  }
+#pragma unroll
+  for (int x = 0; x < E; ++x) wo[warp][lane * E + x] = acc[x];
+  if (lane == 0) wl[warp] = L;
+  __syncthreads();
+  for (int x = threadIdx.x; x < D; x += kMergeWarps * 32) {
+    float O = 0.f, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
       O += wo[w][x];
-      L += wl[w];
+      sum += wl[w];
     }
-    // L == 0: every page of the row was bad; zeros and -inf, not 0 / 0
-    out[row * D + x] = from_f32<T>(L == 0.f ? 0.f : O / L);
-    if (x == 0 && lse_out) lse_out[row] = L == 0.f ? -INFINITY : M + logf(L);
+    // sum == 0: every page of the row was bad; zeros and -inf, not 0 / 0
+    out[row * D + x] = from_f32<T>(sum == 0.f ? 0.f : O / sum);
+    if (x == 0 && lse_out)
+      lse_out[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
   }
 }
 
+// A launch that may begin beside the one before it in the stream.
+template <typename... P, typename... A>
+cudaError_t launch_beside(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                          cudaStream_t st, A... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <typename T, int D>
-cudaError_t run(const Dims& dm, const Cache& c, const void* q, const int32_t* cu_q,
-                const int32_t* idx, float* part_o, float* part_lse, int* arrivals, void* out,
-                float* lse, int* status, cudaStream_t st) {
-  const int64_t x = (int64_t)dm.topk * splits_per_block(dm) * dm.T;
-  if (x > INT32_MAX) return cudaErrorInvalidValue;
-  cache_attn_kernel<T, D><<<dim3((unsigned)x, (unsigned)dm.Hq), kThreads, 0, st>>>(
-      dm, c, static_cast<const T*>(q), cu_q, idx, part_o, part_lse, arrivals,
-      static_cast<T*>(out), lse, status);
-  return cudaGetLastError();
+cudaError_t run_gate(const Step& a, const void* q, const float* kbar, int32_t* idx,
+                     cudaStream_t st) {
+  const Dims& dm = a.dm;
+  const int grp = dm.Hq / dm.Hkv, rows = dm.shared ? 1 : grp < kGateRows ? grp : kGateRows;
+  const int chunks = dm.shared ? 1 : (grp + kGateRows - 1) / kGateRows;
+  // CTAs a cluster: about 32 blocks, four a warp, each
+  const int cs = dm.nb > 128 ? 8 : dm.nb > 64 ? 4 : dm.nb > 32 ? 2 : 1;
+  const int64_t grid = (int64_t)dm.T * dm.Hkv * chunks * cs;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  const size_t smem = sizeof(float) * rows * (size_t)dm.nb;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(cache_gate_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)(sizeof(float) * kGateRows * kGateBlocks))))
+    return e;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)cs;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kGateThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_gate_kernel<T, D>, a, static_cast<const T*>(q), kbar, idx,
+                            cs);
+}
+
+template <typename T, int D>
+cudaError_t run(const Step& a, const void* q, const float* kbar, int32_t* idx, void* out,
+                float* lse, cudaStream_t st) {
+  const Dims& dm = a.dm;
+  cudaError_t e;
+  if (dm.nb <= kGateBlocks)
+    e = run_gate<T, D>(a, q, kbar, idx, st);
+  else  // lists in registers instead of all scores in shared memory
+    e = launch_cache_gate(dm, q, kbar, a.c.lens, a.cu_q, idx, a.max_len, a.status, st);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)dm.T * dm.Hq;
+  if constexpr (sizeof(T) == 2) {
+    CUtensorMap mk, mv;
+    const int64_t cache_rows = ((int64_t)a.c.pages * dm.Hkv) << a.c.page_log2;
+    if ((e = tc::make_rows_map(&mk, a.c.k, cache_rows, D, 16))) return e;
+    if ((e = tc::make_rows_map(&mv, a.c.v, cache_rows, D, 16))) return e;
+    if ((e = cudaFuncSetAttribute(cache_attn_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  Ring<D>::kBytes)))
+      return e;
+    const int hc = (dm.Hq / dm.Hkv + kHeads - 1) / kHeads;
+    const int64_t per = dm.shared ? (int64_t)dm.Hkv * hc * a.sp.per_row
+                                  : (int64_t)dm.Hkv * hc * a.sp.spb +
+                                        (int64_t)dm.Hq * (dm.topk - 1) * a.sp.spb;
+    if (per * dm.T > INT32_MAX || rows > INT32_MAX) return cudaErrorInvalidValue;
+    e = launch_beside(cache_attn_tc<D>, dim3((unsigned)(per * dm.T)), kW * 32, Ring<D>::kBytes, st,
+                      mk, mv, a, static_cast<const __nv_bfloat16*>(q));
+  } else {
+    const int64_t x = (int64_t)a.sp.per_row * dm.T;
+    if (x > INT32_MAX || rows > INT32_MAX) return cudaErrorInvalidValue;
+    e = launch_beside(cache_attn_kernel<D>, dim3((unsigned)x, (unsigned)dm.Hq), kThreads, 0, st, a,
+                      static_cast<const float*>(q));
+  }
+  if (e != cudaSuccess) return e;
+  return launch_beside(cache_merge_kernel<T, D>, dim3((unsigned)rows), kMergeWarps * 32, 0, st, a,
+                       static_cast<T*>(out), lse);
 }
 
 }  // namespace
 
 size_t decode_cache_partial_rows(const Dims& dm) {
-  return (size_t)dm.T * dm.Hq * dm.topk * splits_per_block(dm);
+  return (size_t)dm.T * dm.Hq * split_of(dm).per_row;
 }
 
-cudaError_t launch_cache_attn(const Dims& dm, const Cache& c, const void* q, const int32_t* cu_q,
-                              const int32_t* idx, float* part_o, float* part_lse, int* arrivals,
-                              void* out, float* lse, int* status, cudaStream_t st) {
+cudaError_t launch_decode_cache(const Dims& dm, const Cache& c, const void* q, const float* kbar,
+                                const int32_t* cu_q, int32_t* idx, float* part_o, float* part_lse,
+                                void* out, float* lse, int* status, cudaStream_t st) {
+  const int64_t held = (int64_t)c.max_pages << c.page_log2;
+  const Step a{dm,     c,
+               split_of(dm), cu_q,
+               idx,    part_o,
+               part_lse, held < dm.max_seqlen ? (int)held : dm.max_seqlen,
+               status};
   if (dm.dtype == kBF16)
-    return dm.d == 128 ? run<__nv_bfloat16, 128>(dm, c, q, cu_q, idx, part_o, part_lse, arrivals,
-                                                 out, lse, status, st)
-                       : run<__nv_bfloat16, 64>(dm, c, q, cu_q, idx, part_o, part_lse, arrivals,
-                                                out, lse, status, st);
-  return dm.d == 128
-             ? run<float, 128>(dm, c, q, cu_q, idx, part_o, part_lse, arrivals, out, lse, status, st)
-             : run<float, 64>(dm, c, q, cu_q, idx, part_o, part_lse, arrivals, out, lse, status, st);
+    return dm.d == 128 ? run<__nv_bfloat16, 128>(a, q, kbar, idx, out, lse, st)
+                       : run<__nv_bfloat16, 64>(a, q, kbar, idx, out, lse, st);
+  return dm.d == 128 ? run<float, 128>(a, q, kbar, idx, out, lse, st)
+                     : run<float, 64>(a, q, kbar, idx, out, lse, st);
 }
 
 }  // namespace moba

@@ -14,7 +14,7 @@
 //
 // This file: the row statistics both passes read, and the passes for fp32
 // inputs in fp32 FMA. bf16 inputs take dense_bwd_tc.cu.
-#include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace moba {
 namespace {
@@ -38,6 +38,9 @@ dense_bwd_stat_kernel(Dims dm, const T* __restrict__ out, const T* __restrict__ 
                       T* __restrict__ dv) {
   constexpr int VEC = Vec16<T>::N, LPR = D / VEC, RPS = kThreads / LPR;  // rows per step
   __shared__ float ds[32];
+  // the tensor-core passes may begin: they wait for this launch where they
+  // read the statistics
+  tc::grid_let_next();
   const int h = blockIdx.y, t0 = blockIdx.x * 32;
   const int sub = threadIdx.x % LPR, rr = threadIdx.x / LPR;
   for (int r = rr; r < 32; r += RPS) {

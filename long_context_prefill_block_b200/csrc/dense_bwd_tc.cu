@@ -29,8 +29,6 @@
 //
 // Every wait is bounded (tc::mbar_wait); on expiry the CTA records kStTimeout,
 // drains the copies and products it issued, frees its TMEM and exits.
-#include <mutex>
-
 #include "tc_ptx.cuh"
 
 namespace moba {
@@ -42,9 +40,6 @@ constexpr int TT = 128;  // keys and queries per tile
 constexpr int kWarpsE = 16;                   // element-wise warps, four threads a TMEM lane
 constexpr int kThreads = 128 + kWarpsE * 32;
 constexpr int CW = TT * 4 / kWarpsE;          // columns of a tile per element-wise thread
-// Columns whose P the q pass forms before dP arrives; it forms the others
-// with dS, where the exponential unit would idle.
-constexpr int kAhead = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kHalf = 128 * 128;  // bytes of one 64-column half of a tile
 constexpr uint32_t kTmemCols = 512;
@@ -68,6 +63,10 @@ struct Args {
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
   int* status;
+};
+
+struct Maps {
+  const CUtensorMap *q, *k, *v, *o;
 };
 
 // Static shared memory, padded so that the dynamic part starts on a
@@ -200,30 +199,21 @@ __device__ __forceinline__ void store_cols(__nv_bfloat16* dst, uint32_t taddr, f
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
-                const Args a) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ Shared sh;
+__device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int cta,
+                                        const Maps& m, const Args& a) {
   constexpr uint32_t kTile = Cfg<D>::kTile;
   const Dims& dm = a.dm;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // heads outermost: the CTAs that run together read the same Q and dO, and
   // within a head the tiles with the most queries come first
   const int nt = (dm.max_seqlen + TT - 1) / TT;
-  const int kt = blockIdx.x % nt, g = blockIdx.x / nt % dm.Hkv, b = blockIdx.x / nt / dm.Hkv;
+  const int kt = cta % nt, g = cta / nt % dm.Hkv, b = cta / nt / dm.Hkv;
   int64_t start;
   int len;
   if (!seq_bounds(dm, a.cu, b, start, len, a.status) || !MOBA_CHECK(start + len <= dm.T, a.status))
     return;
   const int k0 = kt * TT;
   if (k0 >= len) return;
-  const uint32_t sb = smem_u32(smem);
-  if (sb & 1023u) {  // the layout above did not hold: nothing can be right
-    if (threadIdx.x == 0) set_status(a.status, kStCheck);
-    return;
-  }
   const uint32_t sK = sb, sV = sb + kTile, sQ = sb + 2 * kTile, sO = sQ + NA * kTile;
   const int grp = dm.Hq / dm.Hkv, per = (len - k0 + TT - 1) / TT, n_items = grp * per;
   const int last_rows = len - (k0 + (per - 1) * TT);  // queries of each head's last tile
@@ -235,8 +225,8 @@ dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__
   if (warp == 0) {
     if (lane == 0) {
       mbar_expect_tx(&sh.fixed_full, 2 * kTile);
-      load_tile<D>(sK, &tmk, &sh.fixed_full, g, (int)start + k0);
-      load_tile<D>(sV, &tmv, &sh.fixed_full, g, (int)start + k0);
+      load_tile<D>(sK, m.k, &sh.fixed_full, g, (int)start + k0);
+      load_tile<D>(sV, m.v, &sh.fixed_full, g, (int)start + k0);
       int na = 0, nb = 0;
       bool ok = true;
       for (int it = 0, h = g * grp, i = 0; it < n_items; ++it) {
@@ -244,12 +234,12 @@ dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__
         if (it >= NA && !(ok = mbar_wait(&sh.a_empty[it % NA], (it / NA - 1) & 1, abort, status)))
           break;
         mbar_expect_tx(&sh.a_full[it % NA], kTile);
-        load_tile<D>(sQ + it % NA * kTile, &tmq, &sh.a_full[it % NA], h, z);
+        load_tile<D>(sQ + it % NA * kTile, m.q, &sh.a_full[it % NA], h, z);
         ++na;
         if (it >= NB && !(ok = mbar_wait(&sh.b_empty[it % NB], (it / NB - 1) & 1, abort, status)))
           break;
         mbar_expect_tx(&sh.b_full[it % NB], kTile);
-        load_tile<D>(sO + it % NB * kTile, &tmo, &sh.b_full[it % NB], h, z);
+        load_tile<D>(sO + it % NB * kTile, m.o, &sh.b_full[it % NB], h, z);
         ++nb;
         if (++i == per) {
           i = 0;
@@ -321,6 +311,7 @@ dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__
     // it, so this warp is at most one partial tile ahead of the issuer
     const float* st = a.stat + start + k0;
     int cleared = 0;
+    grid_wait();  // the statistics are the launch before this one
     for (int it = 0, h = g * grp, i = 0; it < n_items; ++it) {
       const int s = it & 1, n = i == per - 1 ? last_rows : TT;
       bool ok = it < 2 || mbar_wait(&sh.stat_empty[s], (it / 2 - 1) & 1, abort, status);
@@ -441,19 +432,15 @@ dense_bwd_kv_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-               const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
-               const Args a) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ Shared sh;
+__device__ __forceinline__ void q_pass(Shared& sh, const uint32_t sb, const int cta, const Maps& m,
+                                       const Args& a) {
   constexpr uint32_t kTile = Cfg<D>::kTile;
   const Dims& dm = a.dm;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // the heads of a group outermost but one: CTAs that run together read the
   // same K and V; the longest tiles of a head come first
   const int nt = (dm.max_seqlen + TT - 1) / TT;
-  const int qt = nt - 1 - blockIdx.x % nt, h = blockIdx.x / nt % dm.Hq, b = blockIdx.x / nt / dm.Hq;
+  const int qt = nt - 1 - cta % nt, h = cta / nt % dm.Hq, b = cta / nt / dm.Hq;
   int64_t start;
   int len;
   if (!seq_bounds(dm, a.cu, b, start, len, a.status) || !MOBA_CHECK(start + len <= dm.T, a.status))
@@ -462,11 +449,6 @@ dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   if (q0 >= len) return;
   const int g = h / (dm.Hq / dm.Hkv), n_items = qt + 1;
   const int last_keys = min(len - q0, TT);  // keys of the diagonal tile
-  const uint32_t sb = smem_u32(smem);
-  if (sb & 1023u) {  // the layout above did not hold: nothing can be right
-    if (threadIdx.x == 0) set_status(a.status, kStCheck);
-    return;
-  }
   const uint32_t sQ = sb, sO = sb + kTile, sK = sb + 2 * kTile, sV = sK + NA * kTile;
   if (!init_shared(sh, a.status)) return;
   constexpr uint32_t tP = 256, tQ = 384;  // TMEM columns; S at 0 and 128
@@ -477,20 +459,20 @@ dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     bool ok = true;
     if (lane == 0) {
       mbar_expect_tx(&sh.fixed_full, 2 * kTile);
-      load_tile<D>(sQ, &tmq, &sh.fixed_full, h, (int)start + q0);
-      load_tile<D>(sO, &tmo, &sh.fixed_full, h, (int)start + q0);
+      load_tile<D>(sQ, m.q, &sh.fixed_full, h, (int)start + q0);
+      load_tile<D>(sO, m.o, &sh.fixed_full, h, (int)start + q0);
       int na = 0, nb = 0;
       for (int j = 0; j < n_items; ++j) {
         const int z = (int)start + j * TT;
         if (j >= NA && !(ok = mbar_wait(&sh.a_empty[j % NA], (j / NA - 1) & 1, abort, status)))
           break;
         mbar_expect_tx(&sh.a_full[j % NA], kTile);
-        load_tile<D>(sK + j % NA * kTile, &tmk, &sh.a_full[j % NA], g, z);
+        load_tile<D>(sK + j % NA * kTile, m.k, &sh.a_full[j % NA], g, z);
         ++na;
         if (j >= NB && !(ok = mbar_wait(&sh.b_empty[j % NB], (j / NB - 1) & 1, abort, status)))
           break;
         mbar_expect_tx(&sh.b_full[j % NB], kTile);
-        load_tile<D>(sV + j % NB * kTile, &tmv, &sh.b_full[j % NB], g, z);
+        load_tile<D>(sV + j % NB * kTile, m.v, &sh.b_full[j % NB], g, z);
         ++nb;
       }
       if (!ok || *abort) {
@@ -551,6 +533,7 @@ dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     const float sl2 = rsqrtf((float)D) * kLog2e;
     const bool on = q0 + r < len;
     float l2 = 0.f, dd = 0.f;
+    grid_wait();  // the statistics are the launch before this one
     if (on) {
       const float* st = a.stat + (int64_t)h * dm.T + start + q0 + r;
       l2 = __ldg(st);
@@ -562,17 +545,20 @@ dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       ok = mbar_wait(&sh.s_full[j & 1], j / 2 & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after_sync();
-      uint32_t sv[CW], v[CW], w[CW / 2];
-      float p[kAhead];
-      tmem_ld32(tS, sv);
-      tmem_wait_ld();
+      float p[CW];
+      {
+        uint32_t v[CW];
+        tmem_ld32(tS, v);
+        tmem_wait_ld();
 #pragma unroll
-      for (int x = 0; x < kAhead; ++x) p[x] = ex2(fmaf(__uint_as_float(sv[x]), sl2, -l2));
+        for (int x = 0; x < CW; ++x) p[x] = ex2(fmaf(__uint_as_float(v[x]), sl2, -l2));
+      }
       ok = mbar_wait(&sh.dp_full, j & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after_sync();
       const bool masked = j == n_items - 1;  // the diagonal: keys up to the query
       const int hi = min(r + 1, last_keys) - c0;
+      uint32_t v[CW], w[CW / 2];
       tmem_ld32(tP + at, v);
       tmem_wait_ld();
 #pragma unroll
@@ -580,9 +566,7 @@ dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         float ds[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float pu = x + u < kAhead ? p[(x + u) % kAhead]
-                                          : ex2(fmaf(__uint_as_float(sv[x + u]), sl2, -l2));
-          ds[u] = pu * (__uint_as_float(v[x + u]) - dd);
+          ds[u] = p[x + u] * (__uint_as_float(v[x + u]) - dd);
           if (masked) ds[u] = x + u < hi ? ds[u] : 0.f;
         }
         w[x / 2] = pack_bf16x2(ds[0], ds[1]);
@@ -602,6 +586,30 @@ dense_bwd_q_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   finish(sh);
 }
 
+// Both passes in one launch: the first n_kv CTAs own keys, the others queries,
+// so that the second pass fills the SMs that the first one's end leaves idle.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+dense_bwd_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+             const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
+             const Args a, const int n_kv) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Shared sh;
+  const uint32_t sb = smem_u32(smem);
+  if (sb & 1023u) {  // the layout above did not hold: nothing can be right
+    if (threadIdx.x == 0) set_status(a.status, kStCheck);
+    return;
+  }
+  if (threadIdx.x < 4)
+    prefetch_map(threadIdx.x == 0 ? &tmq : threadIdx.x == 1 ? &tmk : threadIdx.x == 2 ? &tmv : &tmo);
+  const Maps m{&tmq, &tmk, &tmv, &tmo};
+  if ((int)blockIdx.x < n_kv)
+    kv_pass<D>(sh, sb, (int)blockIdx.x, m, a);
+  else
+    q_pass<D>(sh, sb, (int)blockIdx.x - n_kv, m, a);
+  grid_wait();  // a CTA without work too: what follows this launch follows the last one
+}
+
 template <int D>
 cudaError_t run(const Args& a, const void* q, const void* k, const void* v, const void* dout,
                 cudaStream_t st) {
@@ -613,18 +621,24 @@ cudaError_t run(const Args& a, const void* q, const void* k, const void* v, cons
   if ((e = make_head_map(&mv, v, dm.T, dm.Hkv, TT, D))) return e;
   if ((e = make_head_map(&mo, dout, dm.T, dm.Hq, TT, D))) return e;
   constexpr int smem = (int)Cfg<D>::kSmem;
-  if ((e = cudaFuncSetAttribute(dense_bwd_kv_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem)))
-    return e;
-  if ((e = cudaFuncSetAttribute(dense_bwd_q_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if ((e = cudaFuncSetAttribute(dense_bwd_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 smem)))
     return e;
   const int64_t nt = (int64_t)((dm.max_seqlen + TT - 1) / TT) * dm.batch;
-  if (nt * dm.Hq > INT32_MAX) return cudaErrorInvalidValue;
-  dense_bwd_kv_tc<D><<<(unsigned)(nt * dm.Hkv), kThreads, smem, st>>>(mq, mk, mv, mo, a);
-  if ((e = cudaGetLastError())) return e;
-  dense_bwd_q_tc<D><<<(unsigned)(nt * dm.Hq), kThreads, smem, st>>>(mq, mk, mv, mo, a);
-  return cudaGetLastError();
+  if (nt * (dm.Hq + dm.Hkv) > INT32_MAX) return cudaErrorInvalidValue;
+  // begins beside the statistics' launch: loads and the first products do
+  // not read them
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(nt * (dm.Hq + dm.Hkv)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dense_bwd_tc<D>, mq, mk, mv, mo, a, (int)(nt * dm.Hkv));
 }
 
 }  // namespace

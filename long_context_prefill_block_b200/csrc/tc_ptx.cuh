@@ -17,6 +17,11 @@ namespace tc {
 // y = head, z = token), 128-byte swizzle, box 64 x 1 x rows: one 64-column
 // half of `rows` consecutive tokens of one head.
 cudaError_t make_head_map(CUtensorMap* map, const void* base, int T, int H, int rows, int d = 128);
+// TMA descriptor of `rows` rows of 128 or 64 bytes, box = box_rows whole rows,
+// 16-byte pieces swizzled (128-byte rows: piece ^ row % 8; 64-byte rows:
+// piece ^ row / 2 % 4).
+cudaError_t make_rows_map(CUtensorMap* map, const void* base, int64_t rows, int row_bytes,
+                          int box_rows);
 int sm_count();
 constexpr int kMaxDevices = 64;  // host-side per-device caches
 
@@ -89,6 +94,36 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// Brings a tensor map (a __grid_constant__ parameter) close to the copy engine.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+// Waits until the launches this one was allowed to overlap (programmatic
+// stream serialization) have finished and their writes are visible; and lets
+// the next launch of the stream begin its part that does not wait.
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_let_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+// Untiled copy: both addresses and the size multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
 // 16-byte global -> shared copy, zero-filled when src_bytes == 0.

@@ -223,8 +223,10 @@ def test_decode_matches_the_definition(lens, nq, Hq, Hkv, d, page, B, topk, dtyp
     mine = torch.full_like(qp, 9.0)
     got = moba.moba_decode_cache(qp, pool.cache, pool.table, i32(lens), offsets(nq), kbar, B, topk,
                                  shared_routing=shared, out=mine)
-    assert got is mine and torch.equal(mine[:n], out) and (mine[n:] == 9).all()
-    assert moba.moba_device_status() == 0
+    assert got is mine and (mine[n:] == 9).all() and moba.moba_device_status() == 0
+    # a row's keys are split by the number of rows in the call, so the sums' order differs: both
+    # are within the tolerance of the definition, and of each other within twice that
+    assert ref.off(mine[:n], out.double().cpu()) <= 2 * TOL[dtype]
 
 
 @pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.bfloat16, 64),
