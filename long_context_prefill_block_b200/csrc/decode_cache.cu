@@ -16,6 +16,7 @@
 
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "tc_ptx.cuh"
 
@@ -232,7 +233,7 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const float* __restrict
 // of up to 8 heads of a kv head for the own block, which they share, and for
 // every block with shared routing. A warp owns steps of 32 keys, w, w + 4, ...;
 // codes come by TMA in tiles of 16 rows (never across a page: pages are 16 or
-// more, tiles are aligned to 16 positions) into the warp's ring of three
+// more, tiles are aligned to 16 positions) into the warp's ring of two
 // steps, so the bytes in flight do not cost registers.
 //
 // The products run on m16n8k16 f16 instructions: e4m3 widens to f16 exactly in
@@ -244,11 +245,12 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const float* __restrict
 //   O^T = V^T P^T A: 16 dims; pairs of keys interleaved by byte permutes; P
 //                 reaches the B layout by two 8 x 8 transposes
 // q is scaled to [1, 2) by a power of two a head, since f16 has a narrower
-// range than bf16: what drops out is 2^-24 of the largest entry. Weights are
-// rounded to f16 (half a step of 2^-11) relative to the largest weight times
-// value scale of the warp's keys so far; sums of weights stay fp32.
+// range than bf16: what drops out is 2^-24 of the largest entry. Weights times
+// value scales are rounded to f16 (half a step of 2^-11) relative to a
+// reference that the warp raises, with its sums, when one passes it by 2^8;
+// sums of weights stay fp32.
 constexpr int kW = 4;        // warps
-constexpr int kStages = 3;   // steps in a warp's ring
+constexpr int kStages = 2;   // steps in a warp's ring: three CTAs an SM, 192 KB in flight
 constexpr int kStep = 32;    // keys a step
 constexpr int kHeads = 8;    // columns
 
@@ -259,9 +261,12 @@ struct Ring {
   static constexpr int kBytes = kW * kStages * kStage;
 };
 
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return (uint32_t)h.x | (uint32_t)h.y << 16;
+// Four e4m3 values as two pairs of f16 (exact).
+__device__ __forceinline__ void widen4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -281,11 +286,6 @@ __device__ __forceinline__ float max_over_keys(float x) {  // over the 8 lanes o
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
 }
-// 2^(x - ref), ref being the largest x or -inf where there is none yet.
-__device__ __forceinline__ float weight(float x, float ref) {
-  return tc::ex2(x - (ref == -INFINITY ? 0.f : ref));
-}
-
 template <int D>
 __global__ void __launch_bounds__(kW * 32)
 cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -379,56 +379,47 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     const int pr = page_row[(pos >> cc.page_log2) - p0];
     return pr < 0 ? -1 : pr + (pos & mask);
   };
-  auto request = [&](int i, int st) {  // lane 0: the loads of step i
-    int at[2];
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      at[t] = tile_row(t0 + i * kStep + t * 16);
-      if (at[t] >= 0) bytes += 2 * R::kTile + 32;
-    }
+  // the loads of step i, one lane a copy: tile lane / 4, then K, V and their scales
+  auto request = [&](int i, int st) {
+    const int t = lane >> 2 & 1, what = lane & 3;
+    const int at = tile_row(t0 + i * kStep + t * 16);
     uint64_t* bar = &full[warp][st];
-    tc::mbar_expect_tx(bar, bytes);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if (at[t] < 0) continue;
-      const uint32_t dst = base + st * R::kStage + t * R::kTile;
-      tc::tma_load_2d(dst, &tmk, bar, 0, at[t]);
-      tc::tma_load_2d(dst + 2 * R::kTile, &tmv, bar, 0, at[t]);
-      tc::bulk_load(tc::smem_u32(&scales[warp][st][0][t * 16]), cc.ks + at[t], 16, bar);
-      tc::bulk_load(tc::smem_u32(&scales[warp][st][1][t * 16]), cc.vs + at[t], 16, bar);
+    const uint32_t there = __ballot_sync(0xffffffffu, at >= 0);
+    if (lane == 0)
+      tc::mbar_expect_tx(bar, ((there & 1) + (there >> 4 & 1)) * (2 * R::kTile + 32));
+    __syncwarp();
+    if (lane < 8 && at >= 0) {
+      if (what < 2)
+        tc::tma_load_2d(base + st * R::kStage + (what * 2 + t) * R::kTile, what ? &tmv : &tmk, bar,
+                        0, at);
+      else
+        tc::bulk_load(tc::smem_u32(&scales[warp][st][what - 2][t * 16]),
+                      (what == 2 ? cc.ks : cc.vs) + at, 16, bar);
     }
   };
-  if (lane == 0)
-    for (int x = 0; x < kStages && warp + x * kW < n_steps; ++x) request(warp + x * kW, x);
+  for (int x = 0; x < kStages && warp + x * kW < n_steps; ++x) request(warp + x * kW, x);
   volatile int* abort = &abort_flag;
-  float m0 = -INFINITY, m1 = -INFINITY, o0 = -INFINITY, o1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  // columns 2 c4 and 2 c4 + 1: references of the logits and of logit plus
+  // value exponent, and the sum of weights
+  float mr[2] = {-INFINITY, -INFINITY}, mo[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  const float qc[2] = {qe0, qe1};
   float acc[D / 16][4];
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
     for (int x = 0; x < 4; ++x) acc[i][x] = 0.f;
-  int n = 0;  // steps of this warp so far
-  bool ok = true;
-  for (int i = warp; i < n_steps; i += kW, ++n) {
-    const int st = n % kStages;
-    ok = tc::mbar_wait(&full[warp][st], n / kStages & 1, abort, a.status);
-    if (!__all_sync(0xffffffffu, ok)) {
-      ok = false;
-      break;
-    }
+
+  // One step of 32 keys whose codes are in stage st. `one`: only column 0 of
+  // lane column 0 is a head, so the second column is left out. `whole`: every
+  // key counts.
+  auto step = [&](auto one_t, auto whole_t, int i, int st) {
+    constexpr int NCOL = decltype(one_t)::value ? 1 : 2;
+    constexpr bool whole = decltype(whole_t)::value;
     const uint32_t sK = base + st * R::kStage, sV = sK + 2 * R::kTile;
-    const uint8_t* ksb = scales[warp][st][0];
-    const uint8_t* vsb = scales[warp][st][1];
-    // ---- logits, base 2: keys r8 and r8 + 8 of two tiles, columns 2 c4 and 2 c4 + 1
-    float x[2][2][2], ev[2][2];
+    float x[2][2][NCOL], ev[2][2];
     bool on[2][2];
-    bool whole = true;  // every key of the step counts (uniform over the warp)
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int pos = t0 + i * kStep + t * 16;
-      const bool there = tile_row(pos) >= 0;
-      whole = whole && there && pos >= lo && pos + 16 <= hi;
       float sc[4] = {0.f, 0.f, 0.f, 0.f};
       uint4 k0[NC], k1[NC];
 #pragma unroll
@@ -449,67 +440,83 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         const uint32_t w1[4] = {k1[m].x, k1[m].y, k1[m].z, k1[m].w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint32_t fa[4] = {e4m3x2_to_f16x2(w0[w] & 0xffff), e4m3x2_to_f16x2(w1[w] & 0xffff),
-                                  e4m3x2_to_f16x2(w0[w] >> 16), e4m3x2_to_f16x2(w1[w] >> 16)};
+          uint32_t fa[4];
+          widen4(w0[w], fa[0], fa[2]);
+          widen4(w1[w], fa[1], fa[3]);
           mma16816(sc, fa, qf[m * 8 + w * 2], qf[m * 8 + w * 2 + 1]);
         }
       }
+      const int pos = t0 + i * kStep + t * 16;
+      const bool there = whole || tile_row(pos) >= 0;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int kp = pos + r8 + 8 * y;
-        on[t][y] = there && kp >= lo && kp < hi;
-        const float ks = e8m0_value(ksb[t * 16 + r8 + 8 * y]);
-        const uint32_t vb = vsb[t * 16 + r8 + 8 * y];
+        on[t][y] = whole || (there && kp >= lo && kp < hi);
+        const float ks = e8m0_value(scales[warp][st][0][t * 16 + r8 + 8 * y]);
+        const uint32_t vb = scales[warp][st][1][t * 16 + r8 + 8 * y];
         ev[t][y] = vb == 255 ? NAN : (float)((int)vb - 127);
-        x[t][y][0] = on[t][y] ? sc[2 * y] * qe0 * ks : -INFINITY;
-        x[t][y][1] = on[t][y] ? sc[2 * y + 1] * qe1 * ks : -INFINITY;
+#pragma unroll
+        for (int z = 0; z < NCOL; ++z)
+          x[t][y][z] = on[t][y] ? sc[2 * y + z] * qc[z] * ks : -INFINITY;
       }
     }
-    // ---- running maxima: of the logits, and of logit + value exponent
-    float n0 = -INFINITY, n1 = -INFINITY, y0 = -INFINITY, y1 = -INFINITY;
+    // ---- references: raised when a value passes one by 2^8 (the first always does)
+    bool up = false;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        n0 = fmaxf(n0, x[t][y][0]);
-        n1 = fmaxf(n1, x[t][y][1]);
-        if (on[t][y]) {
-          y0 = fmaxf(y0, x[t][y][0] + ev[t][y]);
-          y1 = fmaxf(y1, x[t][y][1] + ev[t][y]);
-        }
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int z = 0; z < NCOL; ++z)
+          up = up || x[t][y][z] > mr[z] + 8.f || (on[t][y] && x[t][y][z] + ev[t][y] > mo[z] + 8.f);
+    if (__any_sync(0xffffffffu, up)) {
+      float f[2] = {1.f, 1.f};
+#pragma unroll
+      for (int z = 0; z < NCOL; ++z) {
+        float a0 = mr[z], a1 = mo[z];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            a0 = fmaxf(a0, x[t][y][z]);
+            if (on[t][y]) a1 = fmaxf(a1, x[t][y][z] + ev[t][y]);
+          }
+        a0 = max_over_keys(a0);
+        a1 = max_over_keys(a1);
+        if (mr[z] != -INFINITY) l[z] *= tc::ex2(mr[z] - a0);
+        if (mo[z] != -INFINITY) f[z] = tc::ex2(mo[z] - a1);
+        mr[z] = a0;
+        mo[z] = a1;
       }
-    n0 = fmaxf(m0, max_over_keys(n0));
-    n1 = fmaxf(m1, max_over_keys(n1));
-    y0 = fmaxf(o0, max_over_keys(y0));
-    y1 = fmaxf(o1, max_over_keys(y1));
-    if (m0 != -INFINITY) l0 *= tc::ex2(m0 - n0);
-    if (m1 != -INFINITY) l1 *= tc::ex2(m1 - n1);
-    if (__any_sync(0xffffffffu, (y0 != o0 && o0 != -INFINITY) || (y1 != o1 && o1 != -INFINITY))) {
-      const float f0 = o0 == -INFINITY ? 1.f : tc::ex2(o0 - y0);
-      const float f1 = o1 == -INFINITY ? 1.f : tc::ex2(o1 - y1);
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
-        acc[d][0] *= f0;
-        acc[d][1] *= f1;
-        acc[d][2] *= f0;
-        acc[d][3] *= f1;
+        acc[d][0] *= f[0];
+        acc[d][2] *= f[0];
+        acc[d][1] *= f[1];
+        acc[d][3] *= f[1];
       }
     }
-    m0 = n0;
-    m1 = n1;
-    o0 = y0;
-    o1 = y1;
     // ---- weights, and their products with the values
+    float rm[2], ro[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      rm[z] = mr[z] == -INFINITY ? 0.f : mr[z];
+      ro[z] = mo[z] == -INFINITY ? 0.f : mo[z];
+    }
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       uint32_t b[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        l0 += on[t][y] ? weight(x[t][y][0], m0) : 0.f;
-        l1 += on[t][y] ? weight(x[t][y][1], m1) : 0.f;
-        const float p0f = on[t][y] ? weight(x[t][y][0] + ev[t][y], o0) : 0.f;
-        const float p1f = on[t][y] ? weight(x[t][y][1] + ev[t][y], o1) : 0.f;
-        const __half2 h = __floats2half2_rn(p0f, p1f);
+        float po[2] = {0.f, 0.f};
+#pragma unroll
+        for (int z = 0; z < NCOL; ++z) {
+          const float pw = tc::ex2(x[t][y][z] - rm[z]);
+          const float ow = tc::ex2(x[t][y][z] + ev[t][y] - ro[z]);
+          l[z] += on[t][y] ? pw : 0.f;
+          po[z] = on[t][y] ? ow : 0.f;
+        }
+        const __half2 h = __floats2half2_rn(po[0], po[1]);
         b[y] = transpose8(*reinterpret_cast<const uint32_t*>(&h));
       }
       // keys 2 c4, 2 c4 + 1 and 8 further; dims r8 * D / 8 ..
@@ -538,17 +545,36 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const uint32_t pick = z ? 0x7362u : 0x5140u;
-          const uint32_t ab = __byte_perm(v[0][w], v[1][w], pick);
-          const uint32_t cd = __byte_perm(v[2][w], v[3][w], pick);
-          const uint32_t fa[4] = {e4m3x2_to_f16x2(ab & 0xffff), e4m3x2_to_f16x2(ab >> 16),
-                                  e4m3x2_to_f16x2(cd & 0xffff), e4m3x2_to_f16x2(cd >> 16)};
+          uint32_t fa[4];
+          widen4(__byte_perm(v[0][w], v[1][w], pick), fa[0], fa[1]);
+          widen4(__byte_perm(v[2][w], v[3][w], pick), fa[2], fa[3]);
           mma16816(acc[w * 2 + z], fa, b[0], b[1]);
         }
       }
     }
+  };
+  int n = 0;  // steps of this warp so far
+  bool ok = true;
+  for (int i = warp; i < n_steps; i += kW, ++n) {
+    const int st = n % kStages;
+    ok = tc::mbar_wait(&full[warp][st], n / kStages & 1, abort, a.status);
+    if (!__all_sync(0xffffffffu, ok)) {
+      ok = false;
+      break;
+    }
+    const int pos = t0 + i * kStep;
+    const bool whole =
+        pos >= lo && pos + kStep <= hi && tile_row(pos) >= 0 && tile_row(pos + 16) >= 0;
+    if (whole) {
+      if (nh == 1)
+        step(std::true_type{}, std::true_type{}, i, st);
+      else
+        step(std::false_type{}, std::true_type{}, i, st);
+    } else {
+      step(std::false_type{}, std::false_type{}, i, st);
+    }
     __syncwarp();  // the step's buffers are free
-    const int next = i + kStages * kW;
-    if (lane == 0 && next < n_steps) request(next, st);
+    if (i + kStages * kW < n_steps) request(i + kStages * kW, st);
   }
   if (!ok) {  // let the copies already issued land before the CTA exits
     for (int x = 0; x < kStages; ++x)
@@ -556,12 +582,11 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         tc::mbar_drain(&full[warp][(n + x) % kStages], (n + x) / kStages & 1);
   }
   // ---- the warps' results, in their own rings
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 4);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 4);
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 8);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 8);
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 16);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 16);
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
+    l[1] += __shfl_xor_sync(0xffffffffu, l[1], off);
+  }
   float* res = reinterpret_cast<float*>(ring + warp * kStages * R::kStage);  // [head][D]
 #pragma unroll
   for (int d = 0; d < D / 16; ++d) {
@@ -572,12 +597,12 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       *reinterpret_cast<float2*>(res + (2 * c4 + 1) * D + dim) = make_float2(acc[d][1], acc[d][3]);
   }
   if (r8 == 0) {
-    wm[warp][2 * c4] = m0;
-    wm[warp][2 * c4 + 1] = m1;
-    wo[warp][2 * c4] = o0;
-    wo[warp][2 * c4 + 1] = o1;
-    wl[warp][2 * c4] = l0;
-    wl[warp][2 * c4 + 1] = l1;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      wm[warp][2 * c4 + z] = mr[z];
+      wo[warp][2 * c4 + z] = mo[z];
+      wl[warp][2 * c4 + z] = l[z];
+    }
   }
   __syncthreads();
   if (*abort) return;
