@@ -14,42 +14,65 @@
 // NaN (byte 255): it reads back as NaN rather than as numbers.
 #include <cuda_fp8.h>
 
-#include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace moba {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;  // write and read: four warps that share nothing
+constexpr int kMeanThreads = 256;
+constexpr int kMaxCluster = 8;
 
-// The largest e4m3 code value for scale 2^e, and 2^-e in two exact factors.
-__device__ __forceinline__ int row_exponent(float top) {
-  if (top == 0.f) return -127;
-  const uint32_t u = __float_as_uint(top);
-  int ex = (int)(u >> 23);
-  uint32_t man = u & 0x7fffffu;
-  if (ex == 0) {  // a number below 2^-126: 448 * 2^-127 holds it
-    return -127;
-  }
-  // top = 1.man * 2^(ex - 127); 448 = 1.75 * 2^8
-  const int e = ex - 127 - 8 + (man > 0x600000u ? 1 : 0);
-  return e < -127 ? -127 : e;
+// Exponent of a row whose largest magnitude has the fp32 bits `top` (finite).
+__device__ __forceinline__ int row_exponent(uint32_t top) {
+  // top = 1.man * 2^(ex - 127), 448 = 1.75 * 2^8; below 2^-126, 2^-127 holds it
+  const int e = (int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return top < 0x00800000u || e < -127 ? -127 : e;
 }
 
-// Values x[0 .. N) of a row as N e4m3 bytes.
+// 16 bytes of a row: as they are, their largest magnitude as fp32 bits, and
+// as fp32 values.
+__device__ __forceinline__ uint32_t top_of(const uint4& r, __nv_bfloat16) {
+  const uint32_t a = __vmaxu2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu);
+  const uint32_t b = __vmaxu2(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu);
+  const uint32_t c = __vmaxu2(a, b);
+  return max(c << 16, c & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t top_of(const uint4& r, float) {
+  return max(max(r.x & 0x7fffffffu, r.y & 0x7fffffffu), max(r.z & 0x7fffffffu, r.w & 0x7fffffffu));
+}
+__device__ __forceinline__ void widen(const uint4& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void widen(const uint4& r, float (&x)[4]) {
+  x[0] = __uint_as_float(r.x);
+  x[1] = __uint_as_float(r.y);
+  x[2] = __uint_as_float(r.z);
+  x[3] = __uint_as_float(r.w);
+}
+
+// Values x[0 .. N) of a row as N e4m3 bytes: e in [-127, 120], so 2^-e is a
+// normal number, and |x| * 2^-e <= 448.
 template <int N>
-__device__ __forceinline__ void encode(const float (&x)[N], int e, uint32_t (&w)[N / 4]) {
-  // 2^-e = 2^h * 2^(-e-h): each a normal number for e in [-127, 120]
-  const int h = (-e) >> 1;
-  const float f0 = __uint_as_float((uint32_t)(h + 127) << 23);
-  const float f1 = __uint_as_float((uint32_t)(-e - h + 127) << 23);
-  const float lim = e >= 120 ? 240.f : 448.f;
+__device__ __forceinline__ void encode(float (&x)[N], int e, uint32_t (&w)[N / 4]) {
+  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] *= f;
+  if (e >= 120) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = fminf(fmaxf(x[i], -240.f), 240.f);
+  }
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
-    float y[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) y[u] = fminf(fmaxf(x[i + u] * f0 * f1, -lim), lim);
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[i], x[i + 1]), __NV_SATFINITE,
+                                                 __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[i + 2], x[i + 3]), __NV_SATFINITE,
+                                                 __NV_E4M3);
     w[i / 4] = lo | hi << 16;
   }
 }
@@ -88,123 +111,187 @@ __device__ __forceinline__ int max_positions(const Dims& dm, const Cache& c) {
   return held < dm.max_seqlen ? (int)held : dm.max_seqlen;
 }
 
-// Quantise and store. Row i = token * Hkv + head of the packed new rows; a
-// row is held by LPR lanes of 16 bytes, which share its maximum by shuffles;
-// blockIdx.y: K or V. Bound by HBM: d * sizeof(T) bytes in, d + 1 out.
+// Warp of a write or read: head and tokens it takes. blockIdx.y: K or V.
+// A warp takes `tpw` consecutive tokens of one head, so that their rows are
+// neighbours in a page; lane t looks token t's row up (-1: none) while the
+// rows are on their way.
+struct WarpPlace {
+  int g, t0, n;  // head, first token, tokens
+  int row;       // lane t: cache row of token t0 + t
+};
+__device__ __forceinline__ WarpPlace warp_place(const Dims& dm, int tpw) {
+  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  WarpPlace p;
+  p.g = (int)(w % dm.Hkv);
+  const int64_t t0 = w / dm.Hkv * tpw;
+  p.t0 = (int)(t0 < dm.T ? t0 : dm.T);
+  p.n = min(tpw, dm.T - p.t0);
+  p.row = -1;
+  return p;
+}
+__device__ __forceinline__ int token_row(const Dims& dm, const Cache& c,
+                                         const int32_t* __restrict__ cu, const WarpPlace& p,
+                                         int* status) {
+  const int lane = threadIdx.x & 31;
+  int r, pos, len;
+  if (lane >= p.n ||
+      !tail_position(cu, c.lens, dm.batch, max_positions(dm, c), p.t0 + lane, r, pos, len, status))
+    return -1;
+  return (int)cache_row(c, dm.Hkv, r, pos, p.g, status);
+}
+
+// Quantise and store: a row is held by LPR lanes of 16 bytes, which share its
+// maximum (as integers: an infinity or NaN is above every number). U rows' loads
+// a lane are in flight. Bound by HBM: d * sizeof(T) bytes in, d + 1 out.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 cache_write_kernel(Dims dm, Cache c, const T* __restrict__ k, const T* __restrict__ v,
-                   const int32_t* __restrict__ cu_new, int* status) {
-  constexpr int VEC = Vec16<T>::N, LPR = D / VEC, G = kThreads / LPR, U = 4;
-  const int sub = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+                   const int32_t* __restrict__ cu_new, int tpw, int* status) {
+  constexpr int VEC = Vec16<T>::N, LPR = D / VEC, RPS = 32 / LPR, U = 8;  // rows a step
+  tc::grid_let_next();
+  const int lane = threadIdx.x & 31, sub = lane % LPR, sel = lane / LPR;
   const T* __restrict__ src = blockIdx.y ? v : k;
   uint8_t* __restrict__ codes = blockIdx.y ? c.v : c.k;
   uint8_t* __restrict__ scales = blockIdx.y ? c.vs : c.ks;
-  const int64_t rows = (int64_t)dm.T * dm.Hkv, i0 = (int64_t)blockIdx.x * (G * U) + grp;
-  const int max_len = max_positions(dm, c);
-  float x[U][VEC];
+  WarpPlace p = warp_place(dm, tpw);
+  if (p.n <= 0) return;
+  const T* base = src + ((int64_t)p.t0 * dm.Hkv + p.g) * D + sub * VEC;
+  uint32_t mine = 255;  // lane t: scale byte of token t
+  for (int s0 = 0; s0 < p.n; s0 += RPS * U) {
+    uint4 x[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t i = i0 + u * G;
-    if (i < rows) Vec16<T>::load(src + i * D + sub * VEC, x[u]);
-  }
+    for (int u = 0; u < U; ++u) {
+      const int t = s0 + u * RPS + sel;
+      x[u] = t < p.n ? __ldg(reinterpret_cast<const uint4*>(base + (int64_t)t * dm.Hkv * D))
+                     : make_uint4(0, 0, 0, 0);
+    }
+    if (s0 == 0) p.row = token_row(dm, c, cu_new, p, status);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t i = i0 + u * G;
-    float top = 0.f;
-    bool fine = true;
-    if (i < rows) {
+    for (int u = 0; u < U; ++u) {
+      const int t = s0 + u * RPS + sel;
+      uint32_t top = top_of(x[u], T{});
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        top = fmaxf(top, fabsf(x[u][e]));
-        fine = fine && fabsf(x[u][e]) <= 3.4028234663852886e38f;
+      for (int off = LPR / 2; off > 0; off >>= 1)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+      const bool fine = top < 0x7f800000u;
+      const int e = fine ? row_exponent(top) : -127;
+      float y[VEC];
+      widen(x[u], y);
+      if (!fine) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) y[i] = 0.f;
+      }
+      uint32_t w[VEC / 4];
+      encode<VEC>(y, e, w);
+      const int row = __shfl_sync(0xffffffffu, p.row, t & 31);
+      if (t < p.n && row >= 0) {
+        uint8_t* dst = codes + (int64_t)row * D + sub * VEC;
+        if constexpr (VEC == 8)
+          *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        else
+          *reinterpret_cast<uint32_t*>(dst) = w[0];
+      }
+      const uint32_t byte = fine ? (uint32_t)(e + 127) : 255u;
+#pragma unroll
+      for (int q = 0; q < RPS; ++q) {
+        const uint32_t b = __shfl_sync(0xffffffffu, byte, q * LPR);
+        if (lane == s0 + u * RPS + q) mine = b;
       }
     }
-#pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1) {
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      fine = __shfl_xor_sync(0xffffffffu, (int)fine, off) && fine;
-    }
-    if (i >= rows) continue;
-    int r, pos, len;
-    if (!tail_position(cu_new, c.lens, dm.batch, max_len, (int)(i / dm.Hkv), r, pos, len, status))
-      continue;
-    const int64_t row = cache_row(c, dm.Hkv, r, pos, (int)(i % dm.Hkv), status);
-    if (row < 0) continue;
-    uint32_t w[VEC / 4];
-    const int e = row_exponent(fine ? top : 0.f);
-    if (!fine) {
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) x[u][q] = 0.f;
-    }
-    encode<VEC>(x[u], e, w);
-    uint8_t* dst = codes + row * D + sub * VEC;
-    if constexpr (VEC == 8)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-    else
-      *reinterpret_cast<uint32_t*>(dst) = w[0];
-    if (sub == 0) scales[row] = (uint8_t)(fine ? e + 127 : 255);
   }
+  if (lane < p.n && p.row >= 0) scales[p.row] = (uint8_t)mine;
 }
 
 // Mean of each block that the new rows complete, over the rows as the cache
 // holds them. Slot j of the grid: request r's completed blocks have slots
-// from cu_new[r] / B + r on (n / B + 1 of them at most). One CTA per (slot,
-// kv head): LPR lanes of 16 bytes a row, fp32 sums of every G-th row, then
-// the groups' sums in order.
+// from cu_new[r] / B + r on (n / B + 1 of them at most). One cluster per
+// (slot, kv head), its CTAs taking equal parts of the block: LPR lanes of 16
+// bytes a row, fp32 sums of every G-th row, then the lane groups' sums and the
+// CTAs' sums in order. Bound by the codes' bytes for long prompts, by latency
+// for one block (a 4096-key block: four CTAs).
+constexpr int kMeanPages = 2048 / 16 + 1;  // pages looked up at a time
+
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kMeanThreads, 4)
 cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
-                   float* __restrict__ kbar, int* status) {
-  constexpr int LPR = D / 16, G = kThreads / LPR, U = 4;
+                   float* __restrict__ kbar, int cs, int* status) {
+  constexpr int LPR = D / 16, G = kMeanThreads / LPR, U = 8;
   __shared__ float sum[G][D + 4];
-  const int g = blockIdx.y, B = dm.B;
-  int lo = 0, hi = dm.batch;  // largest r with cu_new[r] / B + r <= slot
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu_new[mid] / B + mid <= (int)blockIdx.x) lo = mid;
-    else hi = mid - 1;
+  __shared__ float part[kMaxCluster][D];
+  __shared__ int page_row[kMeanPages];
+  const int g = blockIdx.y, B = dm.B, slot = blockIdx.x / cs, rank = blockIdx.x % cs;
+  int r = 0;  // the largest with cu_new[r] / B + r <= slot, 32 requests a round
+  for (int n = dm.batch + 1; n > 1;) {
+    const int lane = threadIdx.x & 31, step = (n + 31) / 32, at = r + lane * step;
+    const uint32_t le =
+        __ballot_sync(0xffffffffu, lane * step < n && cu_new[at] / B + at <= slot);
+    const int k = le ? 31 - __clz(le) : 0;
+    n = min(step, n - k * step);
+    r += k * step;
   }
-  const int r = lo;
-  if (r >= dm.batch) return;
-  const int n = cu_new[r + 1] - cu_new[r], len = c.lens[r];
-  if (n <= 0 || len < n || len > max_positions(dm, c)) return;
-  const int blk = (len - n) / B + (int)blockIdx.x - (cu_new[r] / B + r);
-  if (blk < 0 || blk >= len / B || blk >= dm.nb) return;
-  const int sub = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+  // every early return below is the whole cluster's
+  int blk = -1;
+  if (r < dm.batch) {
+    const int n = cu_new[r + 1] - cu_new[r], len = c.lens[r];
+    if (n > 0 && len >= n && len <= max_positions(dm, c)) {
+      blk = (len - n) / B + slot - (cu_new[r] / B + r);
+      if (blk >= len / B || blk >= dm.nb) blk = -1;
+    }
+  }
+  tc::grid_wait();  // the rows
+  if (blk < 0) return;
+  const int per = (B + cs - 1) / cs, first = blk * B + rank * per;
+  const int last = min(first + per, (blk + 1) * B);
+  const int sub = threadIdx.x % LPR, grp = threadIdx.x / LPR, mask = (1 << c.page_log2) - 1;
   float acc[16];
 #pragma unroll
   for (int x = 0; x < 16; ++x) acc[x] = 0.f;
-  for (int j0 = grp; j0 < B; j0 += G * U) {
-    uint4 w[U];
-    float s[U];
+  for (int c0 = first; c0 < last; c0 += 2048) {
+    const int c1 = min(c0 + 2048, last), p0 = c0 >> c.page_log2;
+    __syncthreads();
+    for (int i = threadIdx.x; i <= ((c1 - 1) >> c.page_log2) - p0; i += kMeanThreads) {
+      const int64_t row = cache_page_row(c, dm.Hkv, c.table[(int64_t)r * c.max_pages + p0 + i], g);
+      page_row[i] = (int)row;
+      if (row < 0) set_status(status, kStBadIndices);
+    }
+    __syncthreads();
+    for (int j0 = c0 + grp; j0 < c1; j0 += G * U) {
+      uint4 w[U];
+      float s[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * G;
-      w[u] = make_uint4(0, 0, 0, 0);
-      s[u] = 0.f;
-      if (j < B) {
-        const int64_t row = cache_row(c, dm.Hkv, r, blk * B + j, g, status);
-        if (row >= 0) {
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * G;
+        const int pr = j < c1 ? page_row[(j >> c.page_log2) - p0] : -1;
+        w[u] = make_uint4(0, 0, 0, 0);
+        s[u] = 0.f;
+        if (pr >= 0) {
+          const int64_t row = pr + (j & mask);
           w[u] = *reinterpret_cast<const uint4*>(c.k + row * D + sub * 16);
           s[u] = e8m0_value(c.ks[row]);
         }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float x[16];
-      decode16(w[u], x);
+      for (int u = 0; u < U; ++u) {
+        float x[16];
+        decode16(w[u], x);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[e] = fmaf(x[e], s[u], acc[e]);
+        for (int e = 0; e < 16; ++e) acc[e] = fmaf(x[e], s[u], acc[e]);
+      }
     }
   }
 #pragma unroll
   for (int x = 0; x < 16; ++x) sum[grp][sub * 16 + x] = acc[x];
-  __syncthreads();
-  for (int x = threadIdx.x; x < D; x += kThreads) {
+  tc::cluster_sync();
+  for (int x = threadIdx.x; x < D; x += kMeanThreads) {
     float t = 0.f;
     for (int i = 0; i < G; ++i) t += sum[i][x];
+    tc::store_first(&part[rank][x], t);
+  }
+  tc::cluster_sync();
+  if (rank != 0) return;
+  for (int x = threadIdx.x; x < D; x += kMeanThreads) {
+    float t = 0.f;
+    for (int i = 0; i < cs; ++i) t += part[i][x];
     kbar[(((int64_t)r * dm.nb + blk) * dm.Hkv + g) * D + x] = t / (float)B;
   }
 }
@@ -230,60 +317,66 @@ __device__ __forceinline__ void store16(__nv_bfloat16* dst, const float (&x)[16]
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 cache_read_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_rows, T* __restrict__ k,
-                  T* __restrict__ v, int* status) {
-  constexpr int LPR = D / 16, G = kThreads / LPR, U = 4;
-  const int sub = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+                  T* __restrict__ v, int tpw, int* status) {
+  constexpr int LPR = D / 16, RPS = 32 / LPR, U = 8;
+  const int lane = threadIdx.x & 31, sub = lane % LPR, sel = lane / LPR;
   T* __restrict__ dst = blockIdx.y ? v : k;
   const uint8_t* __restrict__ codes = blockIdx.y ? c.v : c.k;
   const uint8_t* __restrict__ scales = blockIdx.y ? c.vs : c.ks;
-  const int64_t rows = (int64_t)dm.T * dm.Hkv, i0 = (int64_t)blockIdx.x * (G * U) + grp;
-  const int max_len = max_positions(dm, c);
-  uint4 w[U];
-  float s[U];
-  bool on[U];
+  WarpPlace p = warp_place(dm, tpw);
+  if (p.n <= 0) return;
+  p.row = token_row(dm, c, cu_rows, p, status);
+  const float scale = p.row >= 0 ? e8m0_value(scales[p.row]) : 0.f;
+  T* base = dst + ((int64_t)p.t0 * dm.Hkv + p.g) * D + sub * 16;
+  for (int s0 = 0; s0 < p.n; s0 += RPS * U) {
+    uint4 w[U];
+    int row[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t i = i0 + u * G;
-    int r, pos, len;
-    on[u] = false;
-    if (i < rows &&
-        tail_position(cu_rows, c.lens, dm.batch, max_len, (int)(i / dm.Hkv), r, pos, len, status)) {
-      const int64_t row = cache_row(c, dm.Hkv, r, pos, (int)(i % dm.Hkv), status);
-      if (row >= 0) {
-        on[u] = true;
-        w[u] = *reinterpret_cast<const uint4*>(codes + row * D + sub * 16);
-        s[u] = e8m0_value(scales[row]);
-      }
+    for (int u = 0; u < U; ++u) {
+      const int t = s0 + u * RPS + sel;
+      row[u] = __shfl_sync(0xffffffffu, p.row, t & 31);
+      if (t >= p.n) row[u] = -1;
+      if (row[u] >= 0)
+        w[u] = *reinterpret_cast<const uint4*>(codes + (int64_t)row[u] * D + sub * 16);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = s0 + u * RPS + sel;
+      const float f = __shfl_sync(0xffffffffu, scale, t & 31);
+      if (row[u] < 0) continue;
+      float x[16];
+      decode16(w[u], x);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] *= f;
+      store16(base + (int64_t)t * dm.Hkv * D, x);
     }
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (!on[u]) continue;
-    float x[16];
-    decode16(w[u], x);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] *= s[u];
-    store16(dst + (i0 + u * G) * D + sub * 16, x);
-  }
+}
+
+// Tokens a warp takes: 32, or 8 where that leaves SMs without work.
+int tokens_per_warp(const Dims& dm) {
+  return (int64_t)dm.T * dm.Hkv < (int64_t)32 * 16 * tc::sm_count() ? 8 : 32;
+}
+dim3 warp_grid(const Dims& dm, int tpw) {
+  const int64_t warps = (int64_t)((dm.T + tpw - 1) / tpw) * dm.Hkv;
+  return dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)), 2);
 }
 
 template <typename T, int D>
 cudaError_t run_write(const Dims& dm, const Cache& c, const void* k, const void* v,
                       const int32_t* cu_new, int* status, cudaStream_t st) {
-  constexpr int per = kThreads / (D / Vec16<T>::N) * 4;
-  const int64_t rows = (int64_t)dm.T * dm.Hkv;
-  cache_write_kernel<T, D><<<dim3((unsigned)((rows + per - 1) / per), 2), kThreads, 0, st>>>(
-      dm, c, static_cast<const T*>(k), static_cast<const T*>(v), cu_new, status);
+  const int tpw = tokens_per_warp(dm);
+  cache_write_kernel<T, D><<<warp_grid(dm, tpw), kThreads, 0, st>>>(
+      dm, c, static_cast<const T*>(k), static_cast<const T*>(v), cu_new, tpw, status);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t run_read(const Dims& dm, const Cache& c, const int32_t* cu_rows, void* k, void* v,
                      int* status, cudaStream_t st) {
-  constexpr int per = kThreads / (D / 16) * 4;
-  const int64_t rows = (int64_t)dm.T * dm.Hkv;
-  cache_read_kernel<T, D><<<dim3((unsigned)((rows + per - 1) / per), 2), kThreads, 0, st>>>(
-      dm, c, cu_rows, static_cast<T*>(k), static_cast<T*>(v), status);
+  const int tpw = tokens_per_warp(dm);
+  cache_read_kernel<T, D><<<warp_grid(dm, tpw), kThreads, 0, st>>>(
+      dm, c, cu_rows, static_cast<T*>(k), static_cast<T*>(v), tpw, status);
   return cudaGetLastError();
 }
 
@@ -300,12 +393,12 @@ cudaError_t launch_cache_write(const Dims& dm, const Cache& c, const void* k, co
 
 cudaError_t launch_cache_means(const Dims& dm, const Cache& c, const int32_t* cu_new, float* kbar,
                                int* status, cudaStream_t st) {
-  const dim3 grid((unsigned)(dm.T / dm.B + dm.batch), (unsigned)dm.Hkv);
-  if (dm.d == 128)
-    cache_means_kernel<128><<<grid, kThreads, 0, st>>>(dm, c, cu_new, kbar, status);
-  else
-    cache_means_kernel<64><<<grid, kThreads, 0, st>>>(dm, c, cu_new, kbar, status);
-  return cudaGetLastError();
+  const int64_t slots = (int64_t)dm.T / dm.B + dm.batch;
+  const int cs = dm.B >= 1024 && slots * dm.Hkv < 2 * tc::sm_count() ? 4 : 1;
+  if (slots * cs > INT32_MAX) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)(slots * cs), (unsigned)dm.Hkv);
+  const auto kernel = dm.d == 128 ? cache_means_kernel<128> : cache_means_kernel<64>;
+  return tc::launch_beside(kernel, grid, kMeanThreads, 0, st, cs, dm, c, cu_new, kbar, cs, status);
 }
 
 cudaError_t launch_cache_read(const Dims& dm, const Cache& c, const int32_t* cu_rows, void* k,

@@ -148,15 +148,31 @@ __device__ __forceinline__ int find_request(const int32_t* __restrict__ cu, int 
   return lo;
 }
 
+// The same for one i by a whole warp: 32 offsets a round instead of one, two
+// rounds of dependent loads for up to 1023 requests.
+__device__ __forceinline__ int find_request_warp(const int32_t* __restrict__ cu, int batch, int i) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = batch + 1;  // the answer is in [lo, lo + n), cu[lo] <= i (or nothing is)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && cu[at] <= i);
+    const int k = le ? 31 - __clz(le) : 0;
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
 // Request r and cache position of row i of a call on a paged cache: request
 // r's rows cu[r] .. cu[r+1]-1 stand at the last positions of its seqlens[r].
 // False for a row that no request owns (a padded batch), and, with a status
 // code, for a request whose length does not hold its rows or passes max_len.
+// whole_warp: every lane of the warp asks for the same i.
 __device__ __forceinline__ bool tail_position(const int32_t* __restrict__ cu,
                                               const int32_t* __restrict__ seqlens, int batch,
                                               int max_len, int i, int& r, int& pos, int& len,
-                                              int* status) {
-  r = find_request(cu, batch, i);
+                                              int* status, bool whole_warp = false) {
+  r = whole_warp ? find_request_warp(cu, batch, i) : find_request(cu, batch, i);
   if (r >= batch || i < cu[r]) return false;
   const int n = cu[r + 1] - cu[r];
   len = seqlens[r];

@@ -104,22 +104,6 @@ constexpr int kGateThreads = 256;
 constexpr int kGateRows = 16;      // q rows of a group at a time
 constexpr int kGateBlocks = 1024;  // blocks whose scores fit: 64 KB
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-// A float into the shared memory of CTA 0 of the cluster, at this CTA's address.
-__device__ __forceinline__ void store_first(float* p, float x) {
-  uint32_t at;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(tc::smem_u32(p)));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kGateThreads)
 cache_gate_kernel(const Step a, const T* __restrict__ q, const float* __restrict__ kbar,
@@ -130,13 +114,14 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const float* __restrict
   tc::grid_let_next();
   const Dims& dm = a.dm;
   const int grp = dm.Hq / dm.Hkv, chunks = dm.shared ? 1 : (grp + kGateRows - 1) / kGateRows;
-  const int rank = (int)cluster_rank(), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % cs, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int unit = blockIdx.x / cs;
   const int h_first = unit % chunks * kGateRows;
   unit /= chunks;
   const int g = unit % dm.Hkv, qi = unit / dm.Hkv;
   int r, len, p;
-  if (!tail_position(a.cu_q, a.c.lens, dm.batch, a.max_len, qi, r, p, len, a.status)) return;
+  if (!tail_position(a.cu_q, a.c.lens, dm.batch, a.max_len, qi, r, p, len, a.status, true))
+    return;
   const int h0 = g * grp + h_first;
   const int rows = dm.shared ? 1 : min(kGateRows, grp - h_first);
   const int c = p / dm.B, need = min(dm.topk - 1, c);
@@ -148,7 +133,7 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const float* __restrict
         for (int j = 1; j < grp; ++j) s += to_f32(src[j * D]);
       qs[e / D][e % D] = s;
     }
-    cluster_sync();  // also: CTA 0 runs, so its shared memory can be written
+    tc::cluster_sync();  // also: CTA 0 runs, so its shared memory can be written
     constexpr int LPB = D / 4, BPW = 32 / LPB, U = 4;  // lanes a mean, means a warp, steps in flight
     const int sub = lane % LPB, per = (c + cs - 1) / cs;
     const int first = rank * per, end = min(c, first + per), stride = kGateThreads / 32 * BPW;
@@ -169,12 +154,12 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const float* __restrict
           float acc = fmaf(kv[u].w, qv.w, fmaf(kv[u].z, qv.z, fmaf(kv[u].y, qv.y, kv[u].x * qv.x)));
 #pragma unroll
           for (int off = LPB / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-          if (sub == 0 && i0 + u * stride < end) store_first(&score[j * c + i0 + u * stride], acc);
+          if (sub == 0 && i0 + u * stride < end) tc::store_first(&score[j * c + i0 + u * stride], acc);
         }
       }
     }
   }
-  cluster_sync();
+  tc::cluster_sync();
   if (rank != 0) return;
   for (int j = warp; j < rows; j += kGateThreads / 32) {
     const int words = (c + 31) / 32;
@@ -325,7 +310,7 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   const int64_t row0 = (int64_t)qi * dm.Hq + h0;
   int r, len, p;
   const bool valid =
-      tail_position(a.cu_q, cc.lens, dm.batch, a.max_len, qi, r, p, len, nullptr);
+      tail_position(a.cu_q, cc.lens, dm.batch, a.max_len, qi, r, p, len, nullptr, true);
   // ---- q of head r8: this lane's pieces, f16, scaled into [1, 2)
   uint32_t qf[NC * 8];
   float qe = 0.f;  // what head r8's logits are multiplied by
@@ -668,7 +653,7 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = (int64_t)qi * dm.Hq + h, prow = row * S + s;
   int r, len, p, lo = 0, hi = 0;
-  const bool valid = tail_position(a.cu_q, c.lens, dm.batch, a.max_len, qi, r, p, len, nullptr);
+  const bool valid = tail_position(a.cu_q, c.lens, dm.batch, a.max_len, qi, r, p, len, nullptr, true);
   tc::grid_wait();  // the chosen blocks
   if (!valid) return;
   split_range(a, row, s, p, lo, hi);
@@ -795,7 +780,7 @@ cache_merge_kernel(const Step a, T* __restrict__ out, float* __restrict__ lse_ou
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = a.sp.per_row;
   int r, len, p;
   const bool valid = tail_position(a.cu_q, a.c.lens, a.dm.batch, a.max_len,
-                                   (int)(row / a.dm.Hq), r, p, len, nullptr);
+                                   (int)(row / a.dm.Hq), r, p, len, nullptr, true);
   tc::grid_wait();  // the partials
   if (!valid) return;
   const float* ls = a.part_lse + row * S;
@@ -834,23 +819,6 @@ cache_merge_kernel(const Step a, T* __restrict__ out, float* __restrict__ lse_ou
   }
 }
 
-// A launch that may begin beside the one before it in the stream.
-template <typename... P, typename... A>
-cudaError_t launch_beside(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
-                          cudaStream_t st, A... args) {
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename T, int D>
 cudaError_t run_gate(const Step& a, const void* q, const float* kbar, int32_t* idx,
                      cudaStream_t st) {
@@ -866,19 +834,8 @@ cudaError_t run_gate(const Step& a, const void* q, const float* kbar, int32_t* i
   if ((e = cudaFuncSetAttribute(cache_gate_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)(sizeof(float) * kGateRows * kGateBlocks))))
     return e;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = (unsigned)cs;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kGateThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_gate_kernel<T, D>, a, static_cast<const T*>(q), kbar, idx,
-                            cs);
+  return tc::launch_cluster(cache_gate_kernel<T, D>, dim3((unsigned)grid), kGateThreads, smem, st, cs,
+                            a, static_cast<const T*>(q), kbar, idx, cs);
 }
 
 template <typename T, int D>
@@ -905,16 +862,16 @@ cudaError_t run(const Step& a, const void* q, const float* kbar, int32_t* idx, v
                                   : (int64_t)dm.Hkv * hc * a.sp.spb +
                                         (int64_t)dm.Hq * (dm.topk - 1) * a.sp.spb;
     if (per * dm.T > INT32_MAX || rows > INT32_MAX) return cudaErrorInvalidValue;
-    e = launch_beside(cache_attn_tc<D>, dim3((unsigned)(per * dm.T)), kW * 32, Ring<D>::kBytes, st,
-                      mk, mv, a, static_cast<const __nv_bfloat16*>(q));
+    e = tc::launch_beside(cache_attn_tc<D>, dim3((unsigned)(per * dm.T)), kW * 32,
+                          Ring<D>::kBytes, st, 1, mk, mv, a, static_cast<const __nv_bfloat16*>(q));
   } else {
     const int64_t x = (int64_t)a.sp.per_row * dm.T;
     if (x > INT32_MAX || rows > INT32_MAX) return cudaErrorInvalidValue;
-    e = launch_beside(cache_attn_kernel<D>, dim3((unsigned)x, (unsigned)dm.Hq), kThreads, 0, st, a,
+    e = tc::launch_beside(cache_attn_kernel<D>, dim3((unsigned)x, (unsigned)dm.Hq), kThreads, 0, st, 1, a,
                       static_cast<const float*>(q));
   }
   if (e != cudaSuccess) return e;
-  return launch_beside(cache_merge_kernel<T, D>, dim3((unsigned)rows), kMergeWarps * 32, 0, st, a,
+  return tc::launch_beside(cache_merge_kernel<T, D>, dim3((unsigned)rows), kMergeWarps * 32, 0, st, 1, a,
                        static_cast<T*>(out), lse);
 }
 

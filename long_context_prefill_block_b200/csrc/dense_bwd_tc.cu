@@ -628,17 +628,8 @@ cudaError_t run(const Args& a, const void* q, const void* k, const void* v, cons
   if (nt * (dm.Hq + dm.Hkv) > INT32_MAX) return cudaErrorInvalidValue;
   // begins beside the statistics' launch: loads and the first products do
   // not read them
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(nt * (dm.Hq + dm.Hkv)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dense_bwd_tc<D>, mq, mk, mv, mo, a, (int)(nt * dm.Hkv));
+  return launch_beside(dense_bwd_tc<D>, dim3((unsigned)(nt * (dm.Hq + dm.Hkv))), kThreads, smem, st,
+                       1, mq, mk, mv, mo, a, (int)(nt * dm.Hkv));
 }
 
 }  // namespace

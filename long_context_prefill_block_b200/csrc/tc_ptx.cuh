@@ -25,6 +25,37 @@ cudaError_t make_rows_map(CUtensorMap* map, const void* base, int64_t rows, int 
 int sm_count();
 constexpr int kMaxDevices = 64;  // host-side per-device caches
 
+// A launch in clusters of cs CTAs; launch_beside's may also begin before the
+// launch ahead of it in the stream has ended (see grid_wait).
+template <typename... P, typename... A>
+cudaError_t launch_with(bool beside, void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                        cudaStream_t st, int cs, A... args) {
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = beside ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                           cudaStream_t st, int cs, A... args) {
+  return launch_with(false, kernel, grid, threads, smem, st, cs, args...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_beside(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                          cudaStream_t st, int cs, A... args) {
+  return launch_with(true, kernel, grid, threads, smem, st, cs, args...);
+}
+
 // A bounded wait gives up after this many SM clock cycles (about one second
 // at 2 GHz; clock64 is read, which is cheap, unlike %globaltimer) and
 // reports kStTimeout through the device status word.
@@ -32,6 +63,19 @@ constexpr long long kWaitLimitCycles = 2000ll * 1000ll * 1000ll;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// ---- clusters (along x) ------------------------------------------------------
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// A float into the shared memory of the cluster's first CTA, at this CTA's
+// address of p (after a cluster_sync: that CTA must have begun).
+__device__ __forceinline__ void store_first(float* p, float x) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(p)));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
 }
 
 // ---- mbarrier --------------------------------------------------------------
