@@ -190,9 +190,9 @@ def _check_inputs(*ts):
     for t in ts:
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError("tensors must be contiguous CUDA tensors")
-    devs = {t.device for t in ts}
-    if len(devs) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+    first = ts[0].get_device() if ts else 0
+    if any(t.get_device() != first for t in ts):
+        raise ValueError(f"tensors on different devices: {sorted({str(t.device) for t in ts})}")
 
 
 def _check_qkv(q, k, v=None, out=None):

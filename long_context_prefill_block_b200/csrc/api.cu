@@ -2,6 +2,7 @@
 // workspace layout and the launch sequence of the MoBA prefill forward pass
 // (PaperTrace "2.1.3 MoBA", section 3.1): mean-pool -> gate/top-k ->
 // regroup by key block -> history attention + own-block attention -> merge.
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -18,6 +19,7 @@
 namespace moba {
 // Per-device status word; kernels get its address, never the symbol.
 __device__ int g_status;
+constexpr int kMaxStatusDevices = 64;
 
 cudaError_t launch_history_tc(const Dims& dm, const Chunk& ch, const void* q, const void* k,
                               const void* v, const int32_t* cu, const Regroup& rg,
@@ -65,8 +67,16 @@ moba_status validate(const moba_params* p, Dims& dm) {
 }
 
 int* status_word() {
+  // looked up once a device: the address does not change
+  static std::atomic<int*> cache[kMaxStatusDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  const bool known = dev >= 0 && dev < kMaxStatusDevices;
+  if (known)
+    if (int* p = cache[dev].load()) return p;
   void* ptr = nullptr;
   if (cudaGetSymbolAddress(&ptr, g_status) != cudaSuccess) return nullptr;
+  if (known) cache[dev].store(static_cast<int*>(ptr));
   return static_cast<int*>(ptr);
 }
 

@@ -831,8 +831,9 @@ cudaError_t run_gate(const Step& a, const void* q, const float* kbar, int32_t* i
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   const size_t smem = sizeof(float) * rows * (size_t)dm.nb;
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(cache_gate_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)(sizeof(float) * kGateRows * kGateBlocks))))
+  static std::atomic<bool> ready[tc::kMaxDevices];
+  if ((e = tc::allow_smem(cache_gate_kernel<T, D>, (int)sizeof(float) * kGateRows * kGateBlocks,
+                          ready)))
     return e;
   return tc::launch_cluster(cache_gate_kernel<T, D>, dim3((unsigned)grid), kGateThreads, smem, st, cs,
                             a, static_cast<const T*>(q), kbar, idx, cs);
@@ -854,9 +855,8 @@ cudaError_t run(const Step& a, const void* q, const float* kbar, int32_t* idx, v
     const int64_t cache_rows = ((int64_t)a.c.pages * dm.Hkv) << a.c.page_log2;
     if ((e = tc::make_rows_map(&mk, a.c.k, cache_rows, D, 16))) return e;
     if ((e = tc::make_rows_map(&mv, a.c.v, cache_rows, D, 16))) return e;
-    if ((e = cudaFuncSetAttribute(cache_attn_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  Ring<D>::kBytes)))
-      return e;
+    static std::atomic<bool> ready[tc::kMaxDevices];
+    if ((e = tc::allow_smem(cache_attn_tc<D>, Ring<D>::kBytes, ready))) return e;
     const int hc = (dm.Hq / dm.Hkv + kHeads - 1) / kHeads;
     const int64_t per = dm.shared ? (int64_t)dm.Hkv * hc * a.sp.per_row
                                   : (int64_t)dm.Hkv * hc * a.sp.spb +

@@ -91,16 +91,19 @@ struct Args {
   float* dk;
   float* dv;
   int* status;
+  int cs;  // CTAs a cluster
 };
 
-// CTA x of a grid of tiles x batch x heads, tile-major: the tiles with the
-// most work come first when the tile index grows with falling work.
+// Cluster x of a grid of tiles x batch x heads, tile-major: the tiles with the
+// most work come first when the tile index grows with falling work. With few
+// tiles the other side's tiles are dealt to the cs CTAs of a cluster, which
+// sum their results in the order of the ranks.
 struct Place {
-  int tile, b, h;
+  int tile, b, h, rank;
 };
-__device__ __forceinline__ Place place(int batch, int heads) {
-  const int x = blockIdx.x;
-  return {x / (batch * heads), x / heads % batch, x % heads};
+__device__ __forceinline__ Place place(int batch, int heads, int cs) {
+  const int x = blockIdx.x / cs;
+  return {x / (batch * heads), x / heads % batch, x % heads, (int)blockIdx.x % cs};
 }
 
 // 64 rows of one head (row stride in elements) into shared memory, rows at
@@ -202,15 +205,58 @@ __device__ __forceinline__ void load_queries(const Args& a, Smem<D>& sm, int64_t
   }
 }
 
+// Writes accumulators acc[i][4 w + u] (row ty * 4 + i, column tx * 4 + 64 w + u)
+// times f to rows of `out` (n of them, row stride in elements). In a cluster
+// they are left in `tile` first, and each CTA sums and writes 1/cs of the rows.
+template <int D>
+__device__ __forceinline__ void store_rows(const float (&acc)[4][D / 16], float (*tile)[D + 4],
+                                           int rank, int cs, float f, float* out, int64_t stride,
+                                           int n) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  if (cs == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (ty * 4 + i >= n) continue;
+#pragma unroll
+      for (int w = 0; w < D / 64; ++w)
+        store4(out + (ty * 4 + i) * stride + tx * 4 + 64 * w, acc[i][4 * w] * f,
+               acc[i][4 * w + 1] * f, acc[i][4 * w + 2] * f, acc[i][4 * w + 3] * f);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int w = 0; w < D / 64; ++w)
+      store4(&tile[ty * 4 + i][tx * 4 + 64 * w], acc[i][4 * w], acc[i][4 * w + 1],
+             acc[i][4 * w + 2], acc[i][4 * w + 3]);
+  tc::cluster_sync();
+  const int rows = 64 / cs;
+  for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
+    const int row = rank * rows + e / (D / 4), c = e % (D / 4) * 4;
+    if (row >= n) continue;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < cs; ++k) {
+      const float4 v = tc::load_rank(tc::smem_u32(&tile[row][c]), k);
+      t.x += v.x;
+      t.y += v.y;
+      t.z += v.z;
+      t.w += v.w;
+    }
+    store4(out + row * stride + c, t.x * f, t.y * f, t.z * f, t.w * f);
+  }
+  tc::cluster_sync();  // the others' reads of this tile
+}
+
 // dk, dv of 64 keys of one kv head: every later query tile of every q head
 // of the group. Bound by the fp32 FMA rate (shared-memory reads are 6 of
 // every 8 issue slots' wavefronts).
 template <int D>
-__global__ void __launch_bounds__(kThreads) dense_bwd_kv_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) dense_bwd_kv_kernel(const Args a) {
   extern __shared__ __align__(16) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   const Dims& dm = a.dm;
-  const Place pl = place(dm.batch, dm.Hkv);
+  const Place pl = place(dm.batch, dm.Hkv, a.cs);
   const int g = pl.h, b = pl.b;
   int64_t start;
   int len;
@@ -224,14 +270,16 @@ __global__ void __launch_bounds__(kThreads) dense_bwd_kv_kernel(const Args a) {
   load_tile<D>(sm.V, a.v + krow * D, (int64_t)dm.Hkv * D, nk);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // keys ty * 4 .., dims tx * 4 + 64 w
   constexpr int NW = D / 64;
-  float dk[4][4 * NW], dv[4][4 * NW];
+  float dk[4][D / 16], dv[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int x = 0; x < 4 * NW; ++x) dk[i][x] = dv[i][x] = 0.f;
   const int grp = dm.Hq / dm.Hkv;
+  int item = 0;
   for (int h = g * grp; h < (g + 1) * grp; ++h) {
     for (int q0 = k0; q0 < len; q0 += BR) {
+      if (item++ % a.cs != pl.rank) continue;
       __syncthreads();
       load_queries<D>(a, sm, start, q0, len, h);
       __syncthreads();
@@ -261,30 +309,20 @@ __global__ void __launch_bounds__(kThreads) dense_bwd_kv_kernel(const Args a) {
       }
     }
   }
-  const float scale = rsqrtf((float)D);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int kj = ty * 4 + i;
-    if (kj >= nk) continue;
-    const int64_t at = (krow + (int64_t)kj * dm.Hkv) * D + tx * 4;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      store4(a.dk + at + 64 * w, dk[i][4 * w] * scale, dk[i][4 * w + 1] * scale,
-             dk[i][4 * w + 2] * scale, dk[i][4 * w + 3] * scale);
-      store4(a.dv + at + 64 * w, dv[i][4 * w], dv[i][4 * w + 1], dv[i][4 * w + 2],
-             dv[i][4 * w + 3]);
-    }
-  }
+  __syncthreads();
+  const int64_t stride = (int64_t)dm.Hkv * D;
+  store_rows<D>(dk, sm.Q, pl.rank, a.cs, rsqrtf((float)D), a.dk + krow * D, stride, nk);
+  store_rows<D>(dv, sm.O, pl.rank, a.cs, 1.f, a.dv + krow * D, stride, nk);
 }
 
 // dq of 64 queries of one head: every key tile up to the diagonal. Blocks
 // are numbered last tile first, the longest work.
 template <int D>
-__global__ void __launch_bounds__(kThreads) dense_bwd_q_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) dense_bwd_q_kernel(const Args a) {
   extern __shared__ __align__(16) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   const Dims& dm = a.dm;
-  const Place pl = place(dm.batch, dm.Hq);
+  const Place pl = place(dm.batch, dm.Hq, a.cs);
   const int h = pl.h, b = pl.b, g = h / (dm.Hq / dm.Hkv);
   int64_t start;
   int len;
@@ -295,12 +333,12 @@ __global__ void __launch_bounds__(kThreads) dense_bwd_q_kernel(const Args a) {
   load_queries<D>(a, sm, start, q0, len, h);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // queries ty * 4 .., dims tx * 4 + 64 w
   constexpr int NW = D / 64;
-  float dq[4][4 * NW];
+  float dq[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int x = 0; x < 4 * NW; ++x) dq[i][x] = 0.f;
-  for (int k0 = 0; k0 <= q0; k0 += BK) {
+  for (int k0 = pl.rank * BK; k0 <= q0; k0 += a.cs * BK) {
     const int64_t krow = (start + k0) * dm.Hkv + g;
     __syncthreads();
     load_tile<D>(sm.K, a.k + krow * D, (int64_t)dm.Hkv * D, min(BK, len - k0));
@@ -325,17 +363,9 @@ __global__ void __launch_bounds__(kThreads) dense_bwd_q_kernel(const Args a) {
       }
     }
   }
-  const float scale = rsqrtf((float)D);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int qi = ty * 4 + i;
-    if (q0 + qi >= len) continue;
-    const int64_t at = ((start + q0 + qi) * dm.Hq + h) * D + tx * 4;
-#pragma unroll
-    for (int w = 0; w < NW; ++w)
-      store4(a.dq + at + 64 * w, dq[i][4 * w] * scale, dq[i][4 * w + 1] * scale,
-             dq[i][4 * w + 2] * scale, dq[i][4 * w + 3] * scale);
-  }
+  __syncthreads();
+  store_rows<D>(dq, sm.K, pl.rank, a.cs, rsqrtf((float)D), a.dq + ((start + q0) * dm.Hq + h) * D,
+                (int64_t)dm.Hq * D, min(BR, len - q0));
 }
 
 template <typename T, int D>
@@ -354,18 +384,27 @@ cudaError_t run_simt(const Args& a, cudaStream_t st) {
   const Dims& dm = a.dm;
   cudaError_t e;
   constexpr int smem = (int)sizeof(Smem<D>);
-  if ((e = cudaFuncSetAttribute(dense_bwd_kv_kernel<D>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+  static std::atomic<bool> ready[2][tc::kMaxDevices];
+  if ((e = tc::allow_smem(dense_bwd_kv_kernel<D>, smem, ready[0]))) return e;
+  if ((e = tc::allow_smem(dense_bwd_q_kernel<D>, smem, ready[1]))) return e;
+  const int64_t tiles = (dm.max_seqlen + BK - 1) / BK, nt = tiles * dm.batch;
+  // CTAs a tile: while one tile's work is more than an SM's share of a pass
+  // (with T tokens in sequences of the longest length)
+  const int64_t share = (int64_t)(dm.T / BK + 1) * dm.Hq * (tiles + 1) / 2 / tc::sm_count();
+  auto split = [&](int64_t longest) {
+    int cs = 1;
+    while (cs < 4 && longest > cs * 2 && longest > cs * share) cs *= 2;
+    return cs;
+  };
+  Args b = a;
+  b.cs = split(tiles * (dm.Hq / dm.Hkv));
+  if (nt * dm.Hq * 4 > INT32_MAX) return cudaErrorInvalidValue;
+  if ((e = tc::launch_cluster(dense_bwd_kv_kernel<D>, dim3((unsigned)(nt * dm.Hkv * b.cs)),
+                              kThreads, smem, st, b.cs, b)))
     return e;
-  if ((e = cudaFuncSetAttribute(dense_bwd_q_kernel<D>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
-    return e;
-  const int64_t nt = (int64_t)((dm.max_seqlen + BK - 1) / BK) * dm.batch;
-  if (nt * dm.Hq > INT32_MAX) return cudaErrorInvalidValue;
-  dense_bwd_kv_kernel<D><<<(unsigned)(nt * dm.Hkv), kThreads, smem, st>>>(a);
-  if ((e = cudaGetLastError())) return e;
-  dense_bwd_q_kernel<D><<<(unsigned)(nt * dm.Hq), kThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  b.cs = split(tiles);
+  return tc::launch_cluster(dense_bwd_q_kernel<D>, dim3((unsigned)(nt * dm.Hq * b.cs)), kThreads,
+                            smem, st, b.cs, b);
 }
 
 }  // namespace
@@ -395,7 +434,8 @@ cudaError_t launch_dense_bwd_simt(const Dims& dm, const void* q, const void* k, 
                static_cast<float*>(dq),
                static_cast<float*>(dk),
                static_cast<float*>(dv),
-               status};
+               status,
+               1};
   return dm.d == 128 ? run_simt<128>(a, st) : run_simt<64>(a, st);
 }
 

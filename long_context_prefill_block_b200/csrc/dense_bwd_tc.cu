@@ -198,9 +198,53 @@ __device__ __forceinline__ void store_cols(__nv_bfloat16* dst, uint32_t taddr, f
   }
 }
 
+// ---- sums over a cluster
+// With few tiles the items of one tile are dealt to the cs CTAs of a cluster
+// (item x to CTA x % cs); each leaves its accumulators in its shared memory, as
+// fp32 rows whose 16-byte pieces are permuted by the row, and sums and writes
+// 1/cs of the rows of all of them, in the order of the ranks.
 template <int D>
-__device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int cta,
-                                        const Maps& m, const Args& a) {
+__device__ __forceinline__ uint32_t sum_at(uint32_t mat, int row, int piece) {
+  return mat + (uint32_t)row * D * 4 + (((uint32_t)(piece ^ row) & (D / 4 - 1)) << 4);
+}
+// 32 columns from c of an accumulator row (zeros: a CTA without items).
+template <int D>
+__device__ __forceinline__ void leave_cols(uint32_t mat, int row, int c, uint32_t taddr, bool some) {
+  uint32_t r[32];
+  tmem_ld32(taddr, r);
+  tmem_wait_ld();
+#pragma unroll
+  for (int x = 0; x < 32; x += 4)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sum_at<D>(mat, row, (c + x) / 4)),
+                 "r"(some ? r[x] : 0u), "r"(some ? r[x + 1] : 0u), "r"(some ? r[x + 2] : 0u),
+                 "r"(some ? r[x + 3] : 0u)
+                 : "memory");
+}
+// Sums rows of this CTA's share of a matrix, times f, to rows of `out` (row
+// stride in elements), n of them.
+template <int D>
+__device__ __forceinline__ void sum_rows(uint32_t mat, int rank, int cs, float f,
+                                         __nv_bfloat16* out, int64_t stride, int n) {
+  const int rows = TT / cs;
+  for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
+    const int row = rank * rows + e / (D / 4), piece = e % (D / 4);
+    if (row >= n) continue;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < cs; ++k) {
+      const float4 v = load_rank(sum_at<D>(mat, row, piece), k);
+      t.x += v.x;
+      t.y += v.y;
+      t.z += v.z;
+      t.w += v.w;
+    }
+    *reinterpret_cast<uint2*>(out + row * stride + piece * 4) =
+        make_uint2(pack_bf16x2(t.x * f, t.y * f), pack_bf16x2(t.z * f, t.w * f));
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int cta, const int rank,
+                                        const int cs, const Maps& m, const Args& a) {
   constexpr uint32_t kTile = Cfg<D>::kTile;
   const Dims& dm = a.dm;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -215,9 +259,18 @@ __device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int
   const int k0 = kt * TT;
   if (k0 >= len) return;
   const uint32_t sK = sb, sV = sb + kTile, sQ = sb + 2 * kTile, sO = sQ + NA * kTile;
-  const int grp = dm.Hq / dm.Hkv, per = (len - k0 + TT - 1) / TT, n_items = grp * per;
+  const int grp = dm.Hq / dm.Hkv, per = (len - k0 + TT - 1) / TT;
+  const int n_items = (grp * per - rank + cs - 1) / cs;  // of this CTA; 0 is possible
+  // item it: q head h, query tile kt + i; the next item's by advance()
+  const int h_first = g * grp + rank / per, i_first = rank % per;
+  auto advance = [&](int& h, int& i) {
+    for (i += cs; i >= per; i -= per) ++h;
+  };
   const int last_rows = len - (k0 + (per - 1) * TT);  // queries of each head's last tile
-  if (!init_shared(sh, a.status)) return;
+  if (!init_shared(sh, a.status)) {
+    if (cs > 1) cluster_sync(), cluster_sync();
+    return;
+  }
   constexpr uint32_t tS = 0, tP = 128, tV = 256, tK = 256 + D;  // TMEM columns
   volatile int* abort = &sh.abort;
   int* status = a.status;
@@ -229,7 +282,7 @@ __device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int
       load_tile<D>(sV, m.v, &sh.fixed_full, g, (int)start + k0);
       int na = 0, nb = 0;
       bool ok = true;
-      for (int it = 0, h = g * grp, i = 0; it < n_items; ++it) {
+      for (int it = 0, h = h_first, i = i_first; it < n_items; ++it, advance(h, i)) {
         const int z = (int)start + k0 + i * TT;
         if (it >= NA && !(ok = mbar_wait(&sh.a_empty[it % NA], (it / NA - 1) & 1, abort, status)))
           break;
@@ -241,10 +294,6 @@ __device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int
         mbar_expect_tx(&sh.b_full[it % NB], kTile);
         load_tile<D>(sO + it % NB * kTile, m.o, &sh.b_full[it % NB], h, z);
         ++nb;
-        if (++i == per) {
-          i = 0;
-          ++h;
-        }
       }
       if (!ok || *abort) {  // let the copies already issued land before the CTA exits
         mbar_drain(&sh.fixed_full, 0);
@@ -254,7 +303,7 @@ __device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int
     }
   } else if (warp == 1) {
     const uint32_t on = elect_one();
-    int cleared = 0;
+    int cleared = 0, hn = h_first, in = i_first;  // of the next item to land
     // a wait of the whole warp; false in every lane if one gave up
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status)) != 0;
@@ -263,19 +312,20 @@ __device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int
     // Q and dO of an item are in shared memory, and cleared where partial
     auto landed = [&](int it) {
       bool w = wait(&sh.a_full[it % NA], it / NA & 1);
-      if (w && last_rows < TT && it % per == per - 1) {
+      if (w && last_rows < TT && in == per - 1) {
         w = wait(&sh.clear_full[cleared & 1], cleared / 2 & 1);
         ++cleared;
       }
+      advance(hn, in);
       return w;
     };
-    if (ok) ok = landed(0);
-    if (ok) {
+    if (ok && n_items > 0) ok = landed(0);
+    if (ok && n_items > 0) {
       mma_nn<D>(on, tS, sK, sQ);
       commit_on(on, &sh.s_full[0]);
       ok = wait(&sh.b_full[0], 0);
     }
-    if (ok) {
+    if (ok && n_items > 0) {
       mma_nn<D>(on, tP, sV, sO);
       commit_on(on, &sh.dp_full);
     }
@@ -312,7 +362,7 @@ __device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int
     const float* st = a.stat + start + k0;
     int cleared = 0;
     grid_wait();  // the statistics are the launch before this one
-    for (int it = 0, h = g * grp, i = 0; it < n_items; ++it) {
+    for (int it = 0, h = h_first, i = i_first; it < n_items; ++it, advance(h, i)) {
       const int s = it & 1, n = i == per - 1 ? last_rows : TT;
       bool ok = it < 2 || mbar_wait(&sh.stat_empty[s], (it / 2 - 1) & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -332,24 +382,19 @@ __device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int
         fence_proxy_async_smem();
         warp_arrive(&sh.clear_full[cleared++ & 1]);
       }
-      if (++i == per) {
-        i = 0;
-        ++h;
-      }
     }
   } else if (warp >= 4) {
     const int c0 = ((warp - 4) >> 2) * CW, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, at = lanes + c0;
     const float sl2 = rsqrtf((float)D) * kLog2e;
     bool ok = true;
-    for (int it = 0, i = 0; it < n_items; ++it) {
+    for (int it = 0, h = h_first, i = i_first; it < n_items; ++it, advance(h, i)) {
       const int s = it & 1;
       // keys after a query and queries behind the sequence: only in each
       // head's first and last tile. Column x is visible in [lo, hi).
       const bool masked = i == 0 || (i == per - 1 && last_rows < TT);
       const int lo = (i == 0 ? r : 0) - c0;
       const int hi = (i == per - 1 ? last_rows : TT) - c0;
-      if (++i == per) i = 0;
       ok = mbar_wait(&sh.stat_full[s], it / 2 & 1, abort, status) &&
            mbar_wait(&sh.s_full[0], it & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -416,7 +461,13 @@ __device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int
     }
     // dK (the first half of the warps) and dV of key r, 32 columns at a time
     if (ok) ok = mbar_wait(&sh.acc_full, 0, abort, status);
-    if (__all_sync(0xffffffffu, ok)) {
+    if (__all_sync(0xffffffffu, ok) && cs > 1) {
+      fence_after_sync();
+#pragma unroll 1
+      for (int c = c0; c < 2 * D; c += TT)
+        leave_cols<D>(sb + c / D * TT * D * 4, r, c % D, tK + lanes - (c < D ? 0 : 2 * D) + c,
+                      n_items > 0);
+    } else if (__all_sync(0xffffffffu, ok)) {
       fence_after_sync();
       const bool on = k0 + r < len;
       const int64_t row = ((start + k0 + (on ? r : 0)) * dm.Hkv + g) * D;
@@ -428,12 +479,20 @@ __device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int
       }
     }
   }
+  if (cs > 1) {
+    __syncwarp();
+    cluster_sync();
+    const int64_t row = ((start + k0) * dm.Hkv + g) * D, stride = (int64_t)dm.Hkv * D;
+    sum_rows<D>(sb, rank, cs, rsqrtf((float)D), a.dk + row, stride, min(TT, len - k0));
+    sum_rows<D>(sb + TT * D * 4, rank, cs, 1.f, a.dv + row, stride, min(TT, len - k0));
+    cluster_sync();
+  }
   finish(sh);
 }
 
 template <int D>
-__device__ __forceinline__ void q_pass(Shared& sh, const uint32_t sb, const int cta, const Maps& m,
-                                       const Args& a) {
+__device__ __forceinline__ void q_pass(Shared& sh, const uint32_t sb, const int cta, const int rank,
+                                       const int cs, const Maps& m, const Args& a) {
   constexpr uint32_t kTile = Cfg<D>::kTile;
   const Dims& dm = a.dm;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -447,10 +506,15 @@ __device__ __forceinline__ void q_pass(Shared& sh, const uint32_t sb, const int 
     return;
   const int q0 = qt * TT;
   if (q0 >= len) return;
-  const int g = h / (dm.Hq / dm.Hkv), n_items = qt + 1;
+  const int g = h / (dm.Hq / dm.Hkv);
+  const int n_items = (qt + 1 - rank + cs - 1) / cs;  // key tiles rank, rank + cs, ..; 0 is possible
+  const bool diagonal = rank == qt % cs;              // the last of them is the diagonal
   const int last_keys = min(len - q0, TT);  // keys of the diagonal tile
   const uint32_t sQ = sb, sO = sb + kTile, sK = sb + 2 * kTile, sV = sK + NA * kTile;
-  if (!init_shared(sh, a.status)) return;
+  if (!init_shared(sh, a.status)) {
+    if (cs > 1) cluster_sync(), cluster_sync();
+    return;
+  }
   constexpr uint32_t tP = 256, tQ = 384;  // TMEM columns; S at 0 and 128
   volatile int* abort = &sh.abort;
   int* status = a.status;
@@ -463,7 +527,7 @@ __device__ __forceinline__ void q_pass(Shared& sh, const uint32_t sb, const int 
       load_tile<D>(sO, m.o, &sh.fixed_full, h, (int)start + q0);
       int na = 0, nb = 0;
       for (int j = 0; j < n_items; ++j) {
-        const int z = (int)start + j * TT;
+        const int z = (int)start + (rank + j * cs) * TT;
         if (j >= NA && !(ok = mbar_wait(&sh.a_empty[j % NA], (j / NA - 1) & 1, abort, status)))
           break;
         mbar_expect_tx(&sh.a_full[j % NA], kTile);
@@ -481,7 +545,7 @@ __device__ __forceinline__ void q_pass(Shared& sh, const uint32_t sb, const int 
         for (int x = nb > NB ? nb - NB : 0; x < nb; ++x) mbar_drain(&sh.b_full[x % NB], x / NB & 1);
       }
     }
-    if (last_keys < TT) {  // the diagonal tile's keys behind the sequence
+    if (diagonal && last_keys < TT) {  // the diagonal tile's keys behind the sequence
       const int j = n_items - 1;
       if (lane == 0 && ok) ok = mbar_wait(&sh.a_full[j % NA], j / NA & 1, abort, status);
       if (__all_sync(0xffffffffu, ok)) {
@@ -498,7 +562,7 @@ __device__ __forceinline__ void q_pass(Shared& sh, const uint32_t sb, const int 
     bool ok = wait(&sh.fixed_full, 0);
     auto s_product = [&](int j) {
       if (!wait(&sh.a_full[j % NA], j / NA & 1)) return false;
-      if (j == n_items - 1 && last_keys < TT && !wait(&sh.clear_full[0], 0)) return false;
+      if (diagonal && j == n_items - 1 && last_keys < TT && !wait(&sh.clear_full[0], 0)) return false;
       mma_nn<D>(on, (j & 1) * 128, sQ, sK + j % NA * kTile);
       commit_on(on, &sh.s_full[j & 1]);
       return true;
@@ -510,7 +574,7 @@ __device__ __forceinline__ void q_pass(Shared& sh, const uint32_t sb, const int 
       commit_on(on, &sh.b_empty[j % NB]);
       return true;
     };
-    ok = ok && s_product(0) && dp_product(0);
+    ok = ok && (n_items == 0 || (s_product(0) && dp_product(0)));
     for (int j = 0; ok && j < n_items; ++j) {
       // S of the next keys goes into the other buffer, whose dS the last
       // dQ product has been issued for
@@ -556,7 +620,7 @@ __device__ __forceinline__ void q_pass(Shared& sh, const uint32_t sb, const int 
       ok = mbar_wait(&sh.dp_full, j & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after_sync();
-      const bool masked = j == n_items - 1;  // the diagonal: keys up to the query
+      const bool masked = diagonal && j == n_items - 1;  // the diagonal: keys up to the query
       const int hi = min(r + 1, last_keys) - c0;
       uint32_t v[CW], w[CW / 2];
       tmem_ld32(tP + at, v);
@@ -577,22 +641,33 @@ __device__ __forceinline__ void q_pass(Shared& sh, const uint32_t sb, const int 
       warp_arrive(&sh.ds_ready);
     }
     if (ok) ok = mbar_wait(&sh.acc_full, 0, abort, status);
-    if (__all_sync(0xffffffffu, ok)) {
+    if (__all_sync(0xffffffffu, ok) && cs > 1) {
+      fence_after_sync();
+      if (c0 < D) leave_cols<D>(sb, r, c0, tQ + lanes + c0, n_items > 0);
+    } else if (__all_sync(0xffffffffu, ok)) {
       fence_after_sync();
       const int64_t row = ((start + q0 + (on ? r : 0)) * dm.Hq + h) * D;
       if (c0 < D) store_cols(a.dq + row + c0, tQ + lanes + c0, rsqrtf((float)D), on);
     }
   }
+  if (cs > 1) {
+    __syncwarp();
+    cluster_sync();
+    sum_rows<D>(sb, rank, cs, rsqrtf((float)D), a.dq + ((start + q0) * dm.Hq + h) * D,
+                (int64_t)dm.Hq * D, min(TT, len - q0));
+    cluster_sync();
+  }
   finish(sh);
 }
 
-// Both passes in one launch: the first n_kv CTAs own keys, the others queries,
-// so that the second pass fills the SMs that the first one's end leaves idle.
+// Both passes in one launch: the first n_kv clusters own keys, the others
+// queries, so that the second pass fills the SMs that the first one's end
+// leaves idle.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 dense_bwd_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
              const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
-             const Args a, const int n_kv) {
+             const Args a, const int n_kv, const int cs) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Shared sh;
   const uint32_t sb = smem_u32(smem);
@@ -603,10 +678,11 @@ dense_bwd_tc(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   if (threadIdx.x < 4)
     prefetch_map(threadIdx.x == 0 ? &tmq : threadIdx.x == 1 ? &tmk : threadIdx.x == 2 ? &tmv : &tmo);
   const Maps m{&tmq, &tmk, &tmv, &tmo};
-  if ((int)blockIdx.x < n_kv)
-    kv_pass<D>(sh, sb, (int)blockIdx.x, m, a);
+  const int cta = (int)blockIdx.x / cs, rank = (int)blockIdx.x % cs;
+  if (cta < n_kv)
+    kv_pass<D>(sh, sb, cta, rank, cs, m, a);
   else
-    q_pass<D>(sh, sb, (int)blockIdx.x - n_kv, m, a);
+    q_pass<D>(sh, sb, cta - n_kv, rank, cs, m, a);
   grid_wait();  // a CTA without work too: what follows this launch follows the last one
 }
 
@@ -621,15 +697,18 @@ cudaError_t run(const Args& a, const void* q, const void* k, const void* v, cons
   if ((e = make_head_map(&mv, v, dm.T, dm.Hkv, TT, D))) return e;
   if ((e = make_head_map(&mo, dout, dm.T, dm.Hq, TT, D))) return e;
   constexpr int smem = (int)Cfg<D>::kSmem;
-  if ((e = cudaFuncSetAttribute(dense_bwd_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem)))
-    return e;
-  const int64_t nt = (int64_t)((dm.max_seqlen + TT - 1) / TT) * dm.batch;
-  if (nt * (dm.Hq + dm.Hkv) > INT32_MAX) return cudaErrorInvalidValue;
-  // begins beside the statistics' launch: loads and the first products do
-  // not read them
-  return launch_beside(dense_bwd_tc<D>, dim3((unsigned)(nt * (dm.Hq + dm.Hkv))), kThreads, smem, st,
-                       1, mq, mk, mv, mo, a, (int)(nt * dm.Hkv));
+  static std::atomic<bool> ready[kMaxDevices];
+  if ((e = allow_smem(dense_bwd_tc<D>, smem, ready))) return e;
+  const int64_t tiles = (dm.max_seqlen + TT - 1) / TT, nt = tiles * dm.batch;
+  // CTAs a tile: while one tile's items are more than twice an SM's share of
+  // all (with T tokens in sequences of the longest length), and worth a sum
+  const int64_t longest = tiles * (dm.Hq / dm.Hkv);
+  const int64_t share = (int64_t)(dm.T / TT + 1) * dm.Hq * (tiles + 1) / sm_count();
+  int cs = 1;
+  while (cs < 4 && longest > cs * 2 && longest > cs * 2 * share) cs *= 2;
+  if (nt * (dm.Hq + dm.Hkv) * cs > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_beside(dense_bwd_tc<D>, dim3((unsigned)(nt * (dm.Hq + dm.Hkv) * cs)), kThreads, smem,
+                       st, cs, mq, mk, mv, mo, a, (int)(nt * dm.Hkv), cs);
 }
 
 }  // namespace

@@ -7,6 +7,8 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace moba {
@@ -56,6 +58,20 @@ cudaError_t launch_beside(void (*kernel)(P...), dim3 grid, int threads, size_t s
   return launch_with(true, kernel, grid, threads, smem, st, cs, args...);
 }
 
+// Allows `kernel` that much dynamic shared memory, once a device; `done`: a
+// static array of the caller's, one per kernel.
+template <typename K>
+cudaError_t allow_smem(K* kernel, int bytes, std::atomic<bool> (&done)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < kMaxDevices;
+  if (known && done[dev].load()) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done[dev].store(true);
+  return e;
+}
+
 // A bounded wait gives up after this many SM clock cycles (about one second
 // at 2 GHz; clock64 is read, which is cheap, unlike %globaltimer) and
 // reports kStTimeout through the device status word.
@@ -76,6 +92,19 @@ __device__ __forceinline__ void store_first(float* p, float x) {
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(p)));
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+}
+
+// 16 bytes of the shared memory of CTA `rank` of the cluster, at this CTA's
+// address of p (between two cluster_syncs).
+__device__ __forceinline__ float4 load_rank(uint32_t p, uint32_t rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(p), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
 }
 
 // ---- mbarrier --------------------------------------------------------------

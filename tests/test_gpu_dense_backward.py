@@ -158,7 +158,10 @@ def test_a_longer_sequence_than_max_seqlen_is_reported():
     got = moba.dense_causal_backward(*a[:3], cu.to(DEV), out, lse, a[3], max_seqlen=200)
     torch.cuda.synchronize()
     assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG
-    assert all(torch.equal(x[:150], y[:150]) for x, y in zip(got, want))
+    # the tiles' sums are dealt out by max_seqlen: both calls are within the tolerance of the
+    # formulas, so within twice that of each other
+    for x, y in zip(got, want):
+        assert ref.off(x[:150], y[:150].double().cpu()) <= 2 * TOL[torch.bfloat16]
 
 
 def test_two_layers_trained_together():
