@@ -23,28 +23,44 @@
 namespace moba {
 namespace {
 
-constexpr int kMaxSplit = 2048;  // keys per split at most
-constexpr int kMaxPages = kMaxSplit / 16 + 1;
+constexpr int kMaxKeys = 2048;  // keys of a split at most
+constexpr int kMaxSlots = 16;   // blocks of a split at most
+constexpr int kMaxPages = kMaxKeys / 16 + 2 * kMaxSlots;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Keys per split: small enough for two splits an SM, large enough that a
-// CTA's start (about 3 us) is small beside its keys.
-int split_keys(const Dims& dm) {
-  int k = 128;
-  while (k < kMaxSplit && k < dm.B &&
-         (int64_t)dm.T * dm.Hq * dm.topk * ((dm.B + 2 * k - 1) / (2 * k)) >= 4 * tc::sm_count())
-    k *= 2;
-  return k < dm.B ? k : dm.B;
-}
-
-// How a row's keys are divided: slot j (a chosen earlier block, or the own
-// block in the last slot) in spb splits of sk keys.
+// How a row's keys are divided. Its slots are the topk - 1 places for chosen
+// earlier blocks and, last, the own block, which with shared routing is one
+// slot among them and else is read apart, once for all heads of a group. Split
+// x: of group x / parts of `slots` slots, part x % parts of each block (parts
+// > 1 only where a group is one slot).
 struct Split {
-  int sk, spb, per_row;
+  int keys;    // of a part
+  int parts;   // of a block
+  int slots;   // of a group
+  int groups;  // before the own block's
+  int per_row;
 };
+
+// Splits long enough that a CTA's start (about 5 us, most of it dependent
+// loads) is small beside its keys, while two CTAs an SM are left: large blocks
+// in parts of up to 2048 keys, small ones together. 48 x 32768 tokens, three
+// shared blocks of 512: 54 us with a block a CTA, SPLIT_US with all three.
 Split split_of(const Dims& dm) {
-  const int sk = split_keys(dm), spb = (dm.B + sk - 1) / sk;
-  return {sk, spb, dm.topk * spb};
+  const int64_t units = (int64_t)dm.T * (dm.shared ? dm.Hkv : dm.Hq), least = 2 * tc::sm_count();
+  const int listed = dm.shared ? dm.topk : dm.topk - 1;
+  Split s{128, 1, 1, 0, 0};
+  while (s.keys < kMaxKeys && s.keys < dm.B &&
+         units * dm.topk * ((dm.B + 2 * s.keys - 1) / (2 * s.keys)) >= 2 * least)
+    s.keys *= 2;
+  if (s.keys > dm.B) s.keys = dm.B;
+  s.parts = (dm.B + s.keys - 1) / s.keys;
+  if (s.parts == 1)
+    while (s.slots < kMaxSlots && s.slots < listed && (s.slots + 1) * (int64_t)dm.B <= kMaxKeys &&
+           units * ((listed + s.slots) / (s.slots + 1)) >= least)
+      ++s.slots;
+  s.groups = listed > 0 ? (listed + s.slots - 1) / s.slots : 0;
+  s.per_row = (s.groups + (dm.shared ? 0 : 1)) * s.parts;
+  return s;
 }
 
 // A call's fixed facts, and where a query's row stands.
@@ -60,16 +76,24 @@ struct Step {
   int* status;
 };
 
-// Keys [lo, hi) of split s of a row at position p (empty: lo >= hi). Slots
-// before the last hold the chosen earlier blocks, the last one the own block.
-__device__ __forceinline__ void split_range(const Step& a, int64_t row, int s, int p, int& lo,
-                                            int& hi) {
-  const int B = a.dm.B, own = p / B, slot = s / a.sp.spb;
+// Slots [first, last) of split x.
+__device__ __forceinline__ void split_slots(const Step& a, int x, int& first, int& last) {
+  const int group = x / a.sp.parts, listed = a.dm.shared ? a.dm.topk : a.dm.topk - 1;
+  first = group < a.sp.groups ? group * a.sp.slots : a.dm.topk - 1;
+  last = group < a.sp.groups ? min(first + a.sp.slots, listed) : a.dm.topk;
+}
+
+// Keys [lo, hi) of one slot of split x, for a row at position p (empty: lo >= hi).
+// An index row lists the chosen earlier blocks, then the own block; the last
+// slot stands for the own block wherever it is listed.
+__device__ __forceinline__ void slot_range(const Step& a, int64_t row, int x, int slot, int p,
+                                           int& lo, int& hi) {
+  const int B = a.dm.B, own = p / B;
   const int e = slot == a.dm.topk - 1 ? own : a.idx[row * a.dm.topk + slot];
   lo = hi = 0;
   if (slot == a.dm.topk - 1 || (e >= 0 && e < own)) {
-    lo = e * B + (s % a.sp.spb) * a.sp.sk;
-    hi = min(min(lo + a.sp.sk, (e + 1) * B), p + 1);
+    lo = e * B + x % a.sp.parts * a.sp.keys;
+    hi = min(min(lo + a.sp.keys, (e + 1) * B), p + 1);
   }
 }
 
@@ -79,7 +103,7 @@ template <int kThreads>
 __device__ __forceinline__ void load_pages(const Step& a, int r, int g, int lo, int hi,
                                            int* page_row) {
   const Cache& c = a.c;
-  const int p0 = lo >> c.page_log2, np = ((hi - 1) >> c.page_log2) - p0 + 1;
+  const int p0 = lo >> c.page_log2, np = lo < hi ? ((hi - 1) >> c.page_log2) - p0 + 1 : 0;
   for (int i = threadIdx.x; i < np; i += kThreads) {
     const int64_t row =
         cache_page_row(c, a.dm.Hkv, c.table[(int64_t)r * c.max_pages + p0 + i], g);
@@ -119,21 +143,27 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const float* __restrict
   const int h_first = unit % chunks * kGateRows;
   unit /= chunks;
   const int g = unit % dm.Hkv, qi = unit / dm.Hkv;
+  const int h0 = g * grp + h_first;
+  const int rows = dm.shared ? 1 : min(kGateRows, grp - h_first);
+  for (int e = tid; e < rows * D; e += kGateThreads) {
+    const T* src = q + ((int64_t)qi * dm.Hq + h0 + e / D) * D + e % D;
+    float s = to_f32(*src);
+    if (dm.shared)
+      for (int j = 1; j < grp; ++j) s += to_f32(src[j * D]);
+    qs[e / D][e % D] = s;
+  }
   int r, len, p;
   if (!tail_position(a.cu_q, a.c.lens, dm.batch, a.max_len, qi, r, p, len, a.status, true))
     return;
-  const int h0 = g * grp + h_first;
-  const int rows = dm.shared ? 1 : min(kGateRows, grp - h_first);
   const int c = p / dm.B, need = min(dm.topk - 1, c);
+  auto sync = [&] {
+    if (cs == 1)
+      __syncthreads();
+    else
+      tc::cluster_sync();
+  };
   if (need > 0) {
-    for (int e = tid; e < rows * D; e += kGateThreads) {
-      const T* src = q + ((int64_t)qi * dm.Hq + h0 + e / D) * D + e % D;
-      float s = to_f32(*src);
-      if (dm.shared)
-        for (int j = 1; j < grp; ++j) s += to_f32(src[j * D]);
-      qs[e / D][e % D] = s;
-    }
-    tc::cluster_sync();  // also: CTA 0 runs, so its shared memory can be written
+    sync();  // also: CTA 0 runs, so its shared memory can be written
     constexpr int LPB = D / 4, BPW = 32 / LPB, U = 4;  // lanes a mean, means a warp, steps in flight
     const int sub = lane % LPB, per = (c + cs - 1) / cs;
     const int first = rank * per, end = min(c, first + per), stride = kGateThreads / 32 * BPW;
@@ -154,12 +184,18 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const float* __restrict
           float acc = fmaf(kv[u].w, qv.w, fmaf(kv[u].z, qv.z, fmaf(kv[u].y, qv.y, kv[u].x * qv.x)));
 #pragma unroll
           for (int off = LPB / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-          if (sub == 0 && i0 + u * stride < end) tc::store_first(&score[j * c + i0 + u * stride], acc);
+          if (sub == 0 && i0 + u * stride < end) {
+            float* at = &score[j * c + i0 + u * stride];
+            if (cs == 1)
+              *at = acc;
+            else
+              tc::store_first(at, acc);
+          }
         }
       }
     }
   }
-  tc::cluster_sync();
+  sync();
   if (rank != 0) return;
   for (int j = warp; j < rows; j += kGateThreads / 32) {
     const int words = (c + 31) / 32;
@@ -272,13 +308,14 @@ __device__ __forceinline__ float max_over_keys(float x) {  // over the 8 lanes o
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
 }
 template <int D>
-__global__ void __launch_bounds__(kW * 32)
+__global__ void __launch_bounds__(kW * 32, 3)
 cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-              const Step a, const __nv_bfloat16* __restrict__ q) {
+              const Step a, const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ out,
+              float* __restrict__ lse_out) {
   extern __shared__ __align__(1024) uint8_t ring[];
   __shared__ uint64_t full[kW][kStages];
   __shared__ __align__(16) uint8_t scales[kW][kStages][2][kStep];
-  __shared__ int page_row[kMaxPages + 1];
+  __shared__ int page_row[kMaxPages];
   __shared__ float wm[kW][kHeads], wo[kW][kHeads], wl[kW][kHeads];
   __shared__ int abort_flag;
   constexpr int NC = D / 64;  // 16-byte pieces of a row a lane holds
@@ -290,27 +327,24 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   if (warp == 0 && lane < 2) tc::prefetch_map(lane ? &tmv : &tmk);
   // ---- which split, of which heads
   const int grp = dm.Hq / dm.Hkv, hc = (grp + kHeads - 1) / kHeads;
-  const int n_hist = dm.shared ? 0 : dm.Hq * (dm.topk - 1) * a.sp.spb;
-  const int n_group = dm.Hkv * hc * (dm.shared ? a.sp.per_row : a.sp.spb);
+  const int n_hist = dm.shared ? 0 : dm.Hq * a.sp.groups * a.sp.parts;
+  const int per = dm.shared ? a.sp.per_row : a.sp.parts;  // splits that a group's heads share
+  const int n_group = dm.Hkv * hc * per;
   const int qi = blockIdx.x / (n_hist + n_group);
   int u = blockIdx.x % (n_hist + n_group), h0, nh, s;
   if (u < n_group) {
-    const int per = dm.shared ? a.sp.per_row : a.sp.spb;
     s = u % per + (a.sp.per_row - per);
     u /= per;
     h0 = u / hc * grp + u % hc * kHeads;
     nh = min(kHeads, grp - u % hc * kHeads);
   } else {
     u -= n_group;
-    s = u % ((dm.topk - 1) * a.sp.spb);
-    h0 = u / ((dm.topk - 1) * a.sp.spb);
+    s = u % (a.sp.groups * a.sp.parts);
+    h0 = u / (a.sp.groups * a.sp.parts);
     nh = 1;
   }
   const int g = h0 / grp;
   const int64_t row0 = (int64_t)qi * dm.Hq + h0;
-  int r, len, p;
-  const bool valid =
-      tail_position(a.cu_q, cc.lens, dm.batch, a.max_len, qi, r, p, len, nullptr, true);
   // ---- q of head r8: this lane's pieces, f16, scaled into [1, 2)
   uint32_t qf[NC * 8];
   float qe = 0.f;  // what head r8's logits are multiplied by
@@ -345,29 +379,74 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[warp][i], 1);
   if (tid == 0) abort_flag = 0;
   tc::mbar_fence_init();
+  int r, len, p;
+  const bool valid =
+      tail_position(a.cu_q, cc.lens, dm.batch, a.max_len, qi, r, p, len, nullptr, true);
   tc::grid_wait();  // the chosen blocks
-  int lo = 0, hi = 0;
-  if (valid) split_range(a, row0, s, p, lo, hi);
-  if (lo >= hi) {  // no keys (uniform over the CTA)
-    if (valid && tid < nh) a.part_lse[(row0 + tid) * a.sp.per_row + s] = -INFINITY;
+  if (!valid) return;
+  const int page = 1 << cc.page_log2;
+  // lane x of every warp: slot x of the split, its keys, steps and page entries
+  int my_lo = 0, my_hi = 0, my_step, my_page;  // step: one past the slot's last; page: its first
+  {
+    int first, last;
+    split_slots(a, s, first, last);
+    if (first + lane < last) slot_range(a, row0, s, first + lane, p, my_lo, my_hi);
+    const int t0 = my_lo & ~15, np = my_lo < my_hi ? ((my_hi - 1) / page - t0 / page) + 1 : 0;
+    my_step = my_lo < my_hi ? (my_hi - t0 + kStep - 1) / kStep : 0;
+    my_page = np;
+#pragma unroll
+    for (int off = 1; off < kMaxSlots; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, my_step, off);
+      const int y = __shfl_up_sync(0xffffffffu, my_page, off);
+      if (lane >= off) {
+        my_step += x;
+        my_page += y;
+      }
+    }
+    my_page -= np;
+  }
+  const int n_steps = __shfl_sync(0xffffffffu, my_step, kMaxSlots - 1);
+  if (n_steps == 0) {  // no keys (uniform over the CTA; never the only split of a row)
+    if (tid < nh) a.part_lse[(row0 + tid) * a.sp.per_row + s] = -INFINITY;
     return;
   }
-  const int t0 = lo & ~15;
-  load_pages<kW * 32>(a, r, g, t0, hi, page_row);
+  // A walk over the steps: the slot of the current one.
+  struct Walk {
+    int slot, lo, hi, step, end, page;
+  };
+  auto enter = [&](Walk& w, int x) {
+    w.slot = x;
+    w.lo = __shfl_sync(0xffffffffu, my_lo, x);
+    w.hi = __shfl_sync(0xffffffffu, my_hi, x);
+    w.end = __shfl_sync(0xffffffffu, my_step, x);
+    w.step = x ? __shfl_sync(0xffffffffu, my_step, x ? x - 1 : 0) : 0;
+    w.page = __shfl_sync(0xffffffffu, my_page, x) - (w.lo >> cc.page_log2);
+  };
+  Walk wr, wc;  // of the requests, of the computation
+  enter(wr, 0);
+  for (int x = 0;; enter(wr, ++x)) {
+    load_pages<kW * 32>(a, r, g, wr.lo & ~15, wr.hi, page_row + wr.page + (wr.lo >> cc.page_log2));
+    if (wr.end == n_steps) break;
+  }
+  enter(wr, 0);
+  enter(wc, 0);
   __syncthreads();
   const uint32_t base = tc::smem_u32(ring) + warp * kStages * R::kStage;
-  const int n_steps = (hi - t0 + kStep - 1) / kStep, p0 = t0 >> cc.page_log2;
-  const int mask = (1 << cc.page_log2) - 1;
+  // moves a walk to step i (its slots rise); the step's first position
+  auto locate = [&](Walk& w, int i) {
+    while (i >= w.end) enter(w, w.slot + 1);
+    return (w.lo & ~15) + (i - w.step) * kStep;
+  };
   // the cache row that 16 keys from pos begin at, or -1: nothing to read
-  auto tile_row = [&](int pos) {
-    if (pos >= hi) return -1;
-    const int pr = page_row[(pos >> cc.page_log2) - p0];
-    return pr < 0 ? -1 : pr + (pos & mask);
+  auto tile_row = [&](const Walk& w, int pos) {
+    if (pos >= w.hi) return -1;
+    const int pr = page_row[w.page + (pos >> cc.page_log2)];
+    return pr < 0 ? -1 : pr + (pos & (page - 1));
   };
   // the loads of step i, one lane a copy: tile lane / 4, then K, V and their scales
   auto request = [&](int i, int st) {
     const int t = lane >> 2 & 1, what = lane & 3;
-    const int at = tile_row(t0 + i * kStep + t * 16);
+    const int pos = locate(wr, i), at = tile_row(wr, pos + t * 16);
     uint64_t* bar = &full[warp][st];
     const uint32_t there = __ballot_sync(0xffffffffu, at >= 0);
     if (lane == 0)
@@ -397,9 +476,10 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   // One step of 32 keys whose codes are in stage st. `one`: only column 0 of
   // lane column 0 is a head, so the second column is left out. `whole`: every
   // key counts.
-  auto step = [&](auto one_t, auto whole_t, int i, int st) {
+  auto step = [&](auto one_t, auto whole_t, int from, int st) {
     constexpr int NCOL = decltype(one_t)::value ? 1 : 2;
     constexpr bool whole = decltype(whole_t)::value;
+    const int lo = wc.lo, hi = wc.hi;
     const uint32_t sK = base + st * R::kStage, sV = sK + 2 * R::kTile;
     float x[2][2][NCOL], ev[2][2];
     bool on[2][2];
@@ -431,8 +511,8 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
           mma16816(sc, fa, qf[m * 8 + w * 2], qf[m * 8 + w * 2 + 1]);
         }
       }
-      const int pos = t0 + i * kStep + t * 16;
-      const bool there = whole || tile_row(pos) >= 0;
+      const int pos = from + t * 16;
+      const bool there = whole || tile_row(wc, pos) >= 0;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int kp = pos + r8 + 8 * y;
@@ -519,8 +599,8 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
                        : "=r"(v[y][0]), "=r"(v[y][1])
                        : "r"(at + (((r8 >> 1) ^ (key >> 1 & 3)) << 4) + (r8 & 1) * 8));
         if (!whole) {  // zero weights do not silence NaN codes behind a request
-          const int kp = t0 + i * kStep + t * 16 + key;
-          const bool in = kp >= lo && kp < hi && tile_row(t0 + i * kStep + t * 16) >= 0;
+          const int kp = from + t * 16 + key;
+          const bool in = kp >= lo && kp < hi && tile_row(wc, from + t * 16) >= 0;
 #pragma unroll
           for (int w = 0; w < NC * 2; ++w) v[y][w] = in ? v[y][w] : 0u;
         }
@@ -547,16 +627,16 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       ok = false;
       break;
     }
-    const int pos = t0 + i * kStep;
-    const bool whole =
-        pos >= lo && pos + kStep <= hi && tile_row(pos) >= 0 && tile_row(pos + 16) >= 0;
+    const int pos = locate(wc, i);
+    const bool whole = pos >= wc.lo && pos + kStep <= wc.hi && tile_row(wc, pos) >= 0 &&
+                       tile_row(wc, pos + 16) >= 0;
     if (whole) {
       if (nh == 1)
-        step(std::true_type{}, std::true_type{}, i, st);
+        step(std::true_type{}, std::true_type{}, pos, st);
       else
-        step(std::false_type{}, std::true_type{}, i, st);
+        step(std::false_type{}, std::true_type{}, pos, st);
     } else {
-      step(std::false_type{}, std::false_type{}, i, st);
+      step(std::false_type{}, std::false_type{}, pos, st);
     }
     __syncwarp();  // the step's buffers are free
     if (i + kStages * kW < n_steps) request(i + kStages * kW, st);
@@ -612,6 +692,15 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     const int64_t at = (row0 + h) * a.sp.per_row + s;
     const bool none = M == -INFINITY && L == 0.f;  // bad pages only
     const float inv = 1.f / L;
+    if (a.sp.per_row == 1) {  // the row's only split: this is the result
+      *reinterpret_cast<uint2*>(out + (row0 + h) * D + d4 * 4) =
+          none ? make_uint2(0, 0)
+               : make_uint2(tc::pack_bf16x2(o.x * inv, o.y * inv),
+                            tc::pack_bf16x2(o.z * inv, o.w * inv));
+      if (d4 == 0 && lse_out)
+        lse_out[row0 + h] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      continue;
+    }
     if (!none)
       reinterpret_cast<float4*>(a.part_o + at * D)[d4] =
           make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
@@ -644,7 +733,7 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
   constexpr int LPK = D / 16, GPW = 32 / LPK, G = GPW * kWarps, U = 4;
   __shared__ float wm[kWarps], wl[kWarps];
   __shared__ __align__(16) float wo[kWarps][D];
-  __shared__ int page_row[kMaxPages + 1];
+  __shared__ int page_row[kMaxPages];
   tc::grid_let_next();
   const Dims& dm = a.dm;
   const Cache& c = a.c;
@@ -652,17 +741,11 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
   const int s = (int)(blockIdx.x % S), qi = (int)(blockIdx.x / S), h = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = (int64_t)qi * dm.Hq + h, prow = row * S + s;
-  int r, len, p, lo = 0, hi = 0;
+  int r, len, p;
   const bool valid = tail_position(a.cu_q, c.lens, dm.batch, a.max_len, qi, r, p, len, nullptr, true);
   tc::grid_wait();  // the chosen blocks
   if (!valid) return;
-  split_range(a, row, s, p, lo, hi);
-  if (lo >= hi) {
-    if (tid == 0) a.part_lse[prow] = -INFINITY;
-    return;
-  }
-  const int g = h / (dm.Hq / dm.Hkv), p0 = lo >> c.page_log2;
-  load_pages<kThreads>(a, r, g, lo, hi, page_row);
+  const int g = h / (dm.Hq / dm.Hkv);
   const int grp_id = warp * GPW + lane / LPK, sub = lane % LPK;
   const float sl2 = kLog2e * rsqrtf((float)D);
   float qv[16];
@@ -672,6 +755,14 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
 #pragma unroll
   for (int x = 0; x < 16; ++x) o[x] = 0.f;
   const int mask = (1 << c.page_log2) - 1;
+  int first, last;
+  split_slots(a, s, first, last);
+  for (int slot = first; slot < last; ++slot) {
+  int lo, hi;
+  slot_range(a, row, s, slot, p, lo, hi);
+  const int p0 = lo >> c.page_log2;
+  __syncthreads();
+  load_pages<kThreads>(a, r, g, lo, hi, page_row);
   __syncthreads();
   for (int base = lo; base < hi; base += U * G) {
     uint4 kr[U], vr[U];
@@ -724,6 +815,7 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
     }
     m = mn;
   }
+  }
   // merge the lane groups of the warp, then the warps
 #pragma unroll
   for (int off = LPK; off < 32; off <<= 1) {
@@ -752,7 +844,7 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
   float L = 0.f;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) L += wl[w] * (wm[w] == -INFINITY ? 1.f : exp2f(wm[w] - M));
-  // a split all of whose keys weigh nothing (bad pages) leaves no partial;
+  // a split without keys, or with bad pages only, leaves no partial;
   // one with a NaN logit leaves NaN
   const bool none = M == -INFINITY && L == 0.f;
   for (int x = tid; x < D && !none; x += kThreads) {
@@ -825,8 +917,8 @@ cudaError_t run_gate(const Step& a, const void* q, const float* kbar, int32_t* i
   const Dims& dm = a.dm;
   const int grp = dm.Hq / dm.Hkv, rows = dm.shared ? 1 : grp < kGateRows ? grp : kGateRows;
   const int chunks = dm.shared ? 1 : (grp + kGateRows - 1) / kGateRows;
-  // CTAs a cluster: about 32 blocks, four a warp, each
-  const int cs = dm.nb > 128 ? 8 : dm.nb > 64 ? 4 : dm.nb > 32 ? 2 : 1;
+  // CTAs a cluster: 16 to 32 blocks each, up to four a warp; one CTA to 64 blocks
+  const int cs = dm.nb > 128 ? 8 : dm.nb > 64 ? 4 : 1;
   const int64_t grid = (int64_t)dm.T * dm.Hkv * chunks * cs;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   const size_t smem = sizeof(float) * rows * (size_t)dm.nb;
@@ -859,11 +951,13 @@ cudaError_t run(const Step& a, const void* q, const float* kbar, int32_t* idx, v
     if ((e = tc::allow_smem(cache_attn_tc<D>, Ring<D>::kBytes, ready))) return e;
     const int hc = (dm.Hq / dm.Hkv + kHeads - 1) / kHeads;
     const int64_t per = dm.shared ? (int64_t)dm.Hkv * hc * a.sp.per_row
-                                  : (int64_t)dm.Hkv * hc * a.sp.spb +
-                                        (int64_t)dm.Hq * (dm.topk - 1) * a.sp.spb;
+                                  : (int64_t)dm.Hkv * hc * a.sp.parts +
+                                        (int64_t)dm.Hq * a.sp.groups * a.sp.parts;
     if (per * dm.T > INT32_MAX || rows > INT32_MAX) return cudaErrorInvalidValue;
     e = tc::launch_beside(cache_attn_tc<D>, dim3((unsigned)(per * dm.T)), kW * 32,
-                          Ring<D>::kBytes, st, 1, mk, mv, a, static_cast<const __nv_bfloat16*>(q));
+                          Ring<D>::kBytes, st, 1, mk, mv, a, static_cast<const __nv_bfloat16*>(q),
+                          static_cast<__nv_bfloat16*>(out), lse);
+    if (e != cudaSuccess || a.sp.per_row == 1) return e;
   } else {
     const int64_t x = (int64_t)a.sp.per_row * dm.T;
     if (x > INT32_MAX || rows > INT32_MAX) return cudaErrorInvalidValue;
