@@ -50,10 +50,10 @@ Split split_of(const Dims& dm) {
   const int listed = dm.shared ? dm.topk : dm.topk - 1;
   Split s{128, 1, 1, 0, 0};
   while (s.keys < kMaxKeys && s.keys < dm.B &&
-         units * dm.topk * ((dm.B + 2 * s.keys - 1) / (2 * s.keys)) >= 2 * least)
+         units * dm.topk * (((int64_t)dm.B + 2 * s.keys - 1) / (2 * s.keys)) >= 2 * least)
     s.keys *= 2;
   if (s.keys > dm.B) s.keys = dm.B;
-  s.parts = (dm.B + s.keys - 1) / s.keys;
+  s.parts = (int)(((int64_t)dm.B + s.keys - 1) / s.keys);
   if (s.parts == 1)
     while (s.slots < kMaxSlots && s.slots < listed && (s.slots + 1) * (int64_t)dm.B <= kMaxKeys &&
            units * ((listed + s.slots) / (s.slots + 1)) >= least)
@@ -93,7 +93,7 @@ __device__ __forceinline__ void slot_range(const Step& a, int64_t row, int x, in
   lo = hi = 0;
   if (slot == a.dm.topk - 1 || (e >= 0 && e < own)) {
     lo = e * B + x % a.sp.parts * a.sp.keys;
-    hi = min(min(lo + a.sp.keys, (e + 1) * B), p + 1);
+    hi = min(lo + a.sp.keys, e < own ? (e + 1) * B : p + 1);
   }
 }
 

@@ -28,7 +28,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // stat[0][h][t] = lse * log2(e), stat[1][h][t] = D = dO . out, laid out head
 // by head so that a tile of one head's queries reads contiguous floats. Also
-// writes the gradients of rows that no sequence owns (t >= cu[batch]): zero.
+// writes the gradients of rows that no sequence owns (a padded batch) or that
+// stand in a sequence longer than max_seqlen, which is skipped: zeros.
 // One CTA: 32 tokens of one head; 16 bytes of a row per lane.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
@@ -38,6 +39,7 @@ dense_bwd_stat_kernel(Dims dm, const T* __restrict__ out, const T* __restrict__ 
                       T* __restrict__ dv) {
   constexpr int VEC = Vec16<T>::N, LPR = D / VEC, RPS = kThreads / LPR;  // rows per step
   __shared__ float ds[32];
+  __shared__ bool owned[32];
   // the tensor-core passes may begin: they wait for this launch where they
   // read the statistics
   tc::grid_let_next();
@@ -60,21 +62,25 @@ dense_bwd_stat_kernel(Dims dm, const T* __restrict__ out, const T* __restrict__ 
   }
   __syncthreads();
   const int t = t0 + threadIdx.x;
-  if (threadIdx.x < 32 && t < dm.T) {
-    stat[(int64_t)h * dm.T + t] = lse[(int64_t)t * dm.Hq + h] * kLog2e;
-    stat[((int64_t)dm.Hq + h) * dm.T + t] = ds[threadIdx.x];
+  if (threadIdx.x < 32) {
+    bool mine = false;
+    if (t < dm.T) {
+      stat[(int64_t)h * dm.T + t] = lse[(int64_t)t * dm.Hq + h] * kLog2e;
+      stat[((int64_t)dm.Hq + h) * dm.T + t] = ds[threadIdx.x];
+      const int b = find_request(cu, dm.batch, t);
+      mine = b < dm.batch && t >= cu[b] && cu[b + 1] - cu[b] <= dm.max_seqlen;
+    }
+    owned[threadIdx.x] = mine;
   }
-  const int end = min(max(cu[dm.batch], 0), dm.T);
-  if (t0 + 32 > end) {
-    const T zero = from_f32<T>(0.f);
-    for (int e = threadIdx.x; e < 32 * D; e += kThreads) {
-      const int64_t row = t0 + e / D;
-      if (row < end || row >= dm.T) continue;
-      dq[(row * dm.Hq + h) * D + e % D] = zero;
-      if (h < dm.Hkv) {
-        dk[(row * dm.Hkv + h) * D + e % D] = zero;
-        dv[(row * dm.Hkv + h) * D + e % D] = zero;
-      }
+  if (__syncthreads_and(threadIdx.x >= 32 || owned[threadIdx.x & 31])) return;
+  const T zero = from_f32<T>(0.f);
+  for (int e = threadIdx.x; e < 32 * D; e += kThreads) {
+    const int64_t row = t0 + e / D;
+    if (row >= dm.T || owned[e / D]) continue;
+    dq[(row * dm.Hq + h) * D + e % D] = zero;
+    if (h < dm.Hkv) {
+      dk[(row * dm.Hkv + h) * D + e % D] = zero;
+      dv[(row * dm.Hkv + h) * D + e % D] = zero;
     }
   }
 }

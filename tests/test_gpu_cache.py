@@ -206,7 +206,8 @@ def check_decode(q, pool, lens, nq, B, topk, shared, out, lse, idx):
     ([100, 0, 257], [1, 0, 3], 4, 2, 64, 32, 20, 4), ([1500, 700], [1, 1], 8, 2, 128, 16, 128, 3),
     ([3000], [4], 4, 4, 128, 64, 100, 12), ([2999, 1025], [2, 1], 10, 2, 128, 64, 1000, 2),
     ([1300], [1], 16, 1, 64, 128, 600, 3), ([700], [1], 3, 3, 128, 64, 4096, 8),
-    ([640, 513], [5, 1], 12, 4, 128, 64, 64, 32)])
+    ([640, 513], [5, 1], 12, 4, 128, 64, 64, 32), ([900, 33], [1, 1], 40, 1, 64, 1024, 64, 5),
+    ([2500], [1], 18, 2, 128, 32, 48, 20)])
 def test_decode_matches_the_definition(lens, nq, Hq, Hkv, d, page, B, topk, dtype, shared):
     pool, kbar = filled(lens, Hkv, d, page, B, seed=sum(lens))
     g = torch.Generator().manual_seed(1)
@@ -227,6 +228,47 @@ def test_decode_matches_the_definition(lens, nq, Hq, Hkv, d, page, B, topk, dtyp
     # a row's keys are split by the number of rows in the call, so the sums' order differs: both
     # are within the tolerance of the definition, and of each other within twice that
     assert ref.off(mine[:n], out.double().cpu()) <= 2 * TOL[dtype]
+
+
+@pytest.mark.parametrize("dtype,shared", [(torch.bfloat16, False), (torch.float32, True)])
+def test_more_blocks_than_fit_shared_memory(dtype, shared):
+    """1100 blocks of 16 keys: the gate that keeps lists instead of all scores."""
+    lens, nq, B, topk = [17600, 200], [1, 2], 16, 6
+    pool, kbar = filled(lens, 1, 64, 64, B, seed=31)
+    q = (torch.randn(3, 2, 64, generator=torch.Generator().manual_seed(4)) * 0.7).to(dtype).to(DEV)
+    got = moba.moba_decode_cache(q, pool.cache, pool.table, i32(lens), offsets(nq), kbar, B, topk,
+                                 shared_routing=shared, return_lse=True, return_idx=True)
+    assert moba.moba_device_status() == 0
+    check_decode(q, pool, lens, nq, B, topk, shared, *got)
+
+
+def test_many_requests_with_one_token_each():
+    """70 requests, some without a row, in one call, with padded rows behind: three rounds of the
+    search for a row's request."""
+    g = torch.Generator().manual_seed(6)
+    lens = torch.randint(1, 90, (70,), generator=g).tolist()
+    nq = [0 if r % 9 == 4 else 1 for r in range(70)]
+    n, B = sum(nq), 16
+    pool, kbar = filled(lens, 2, 64, 16, B, seed=32)
+    x = (torch.randn(n + 5, 2, 64, generator=g) * 0.7).to(DEV)
+    x[n:] = float("nan")
+    before = pool.bits()
+    moba.moba_cache_write(pool.cache, x, -x, pool.table, i32(lens), offsets(nq), kbar, B)
+    for w, y in enumerate((x[:n], -x[:n])):
+        codes, scales = expected(pool, before, y, pool.table.cpu(), nq, lens, w)
+        after = pool.bits()
+        assert torch.equal(after[w].view(torch.float8_e4m3fn).float(),
+                           codes.view(torch.float8_e4m3fn).float())
+        assert torch.equal(after[w + 2], scales)
+    q = (torch.randn(n, 4, 64, generator=g) * 0.7).to(DEV)
+    got = moba.moba_decode_cache(q, pool.cache, pool.table, i32(lens), offsets(nq), kbar, B, 3,
+                                 return_lse=True, return_idx=True)
+    assert moba.moba_device_status() == 0
+    check_decode(q, pool, lens, nq, B, 3, False, *got)
+    k, _ = moba.moba_cache_read(pool.cache, pool.table, i32(lens), offsets(nq), n,
+                                dtype=torch.float32)
+    c, e, _ = ref.quantise(x[:n].cpu())
+    assert torch.equal(k.cpu().double(), c * torch.exp2(e.double())[..., None])
 
 
 @pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.bfloat16, 64),

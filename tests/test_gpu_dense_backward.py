@@ -61,7 +61,8 @@ def room(q, k, v, cu, out, lse, do):
 @pytest.mark.parametrize("lens,Hq,Hkv,d", [
     ((1,), 1, 1, 128), ((2, 1, 3), 2, 1, 64), ((127,), 2, 2, 128), ((128,), 1, 1, 64),
     ((129, 0, 64), 2, 1, 128), ((255, 257), 4, 2, 64), ((65, 63, 1, 500), 3, 3, 128),
-    ((640,), 6, 2, 128), ((383, 31), 5, 1, 64)])
+    ((640,), 6, 2, 128), ((383, 31), 5, 1, 64), ((1,) * 40 + (129,), 1, 1, 128),
+    ((260, 7), 12, 1, 128)])
 def test_gradients_match_the_formulas(lens, Hq, Hkv, d, dtype):
     q, k, v, do, cu = case(lens, Hq, Hkv, d, dtype)
     check(q, k, v, do, cu, *run(q, k, v, do, cu))
@@ -162,6 +163,16 @@ def test_a_longer_sequence_than_max_seqlen_is_reported():
     # formulas, so within twice that of each other
     for x, y in zip(got, want):
         assert ref.off(x[:150], y[:150].double().cpu()) <= 2 * TOL[torch.bfloat16]
+        assert not x[150:].any()
+
+
+def test_many_tiles_and_a_generous_max_seqlen():
+    """Enough tiles that each has one CTA, and a bound of 16 times the longest sequence."""
+    q, k, v, do, cu = case((700, 650), 16, 16, 64, torch.bfloat16, seed=14)
+    out, lse, grads = run(q, k, v, do, cu)
+    check(q, k, v, do, cu, out, lse, grads)
+    grads = run(q, k, v, do, cu, max_seqlen=11200)[2]
+    check(q, k, v, do, cu, out, lse, grads)
 
 
 def test_two_layers_trained_together():
