@@ -4,7 +4,8 @@
 // its logit and a value's scale its weight, so codes are widened once and
 // never rescaled.
 //
-//   cache_gate_kernel  scores and top-k, a cluster of CTAs per (query, kv head)
+//   cache_gate_kernel  scores and top-k, a cluster of CTAs per (query, kv head),
+//                      where there are many blocks to choose from
 //   cache_attn_tc      bf16 queries: split over the chosen keys, codes by TMA
 //                      into each warp's own ring, products on the tensor core
 //   cache_attn_kernel  fp32 queries: the same split, fp32 FMA
@@ -69,7 +70,9 @@ struct Step {
   Cache c;
   Split sp;
   const int32_t* cu_q;
-  const int32_t* idx;
+  const float* kbar;
+  int32_t* idx;
+  bool gated;       // idx comes from a launch of its own; else each CTA chooses
   float* part_o;    // [row][split][d], normalised
   float* part_lse;  // [row][split], base 2
   int max_len;
@@ -86,10 +89,10 @@ __device__ __forceinline__ void split_slots(const Step& a, int x, int& first, in
 // Keys [lo, hi) of one slot of split x, for a row at position p (empty: lo >= hi).
 // An index row lists the chosen earlier blocks, then the own block; the last
 // slot stands for the own block wherever it is listed.
-__device__ __forceinline__ void slot_range(const Step& a, int64_t row, int x, int slot, int p,
-                                           int& lo, int& hi) {
+__device__ __forceinline__ void slot_range(const Step& a, const int32_t* list, int x, int slot,
+                                           int p, int& lo, int& hi) {
   const int B = a.dm.B, own = p / B;
-  const int e = slot == a.dm.topk - 1 ? own : a.idx[row * a.dm.topk + slot];
+  const int e = slot == a.dm.topk - 1 ? own : list[slot];
   lo = hi = 0;
   if (slot == a.dm.topk - 1 || (e >= 0 && e < own)) {
     lo = e * B + x % a.sp.parts * a.sp.keys;
@@ -122,16 +125,97 @@ __device__ __forceinline__ void load_pages(const Step& a, int r, int g, int lo, 
 // of the group (one row, their sum, with shared routing), and the scores meet
 // in the first CTA's shared memory, where a warp a row picks the best by rounds
 // of arg-max. A mean is read once for the group's rows, not once a row, and no
-// thread walks a list alone: 39 -> GATE_US us for four queries at the
-// million-token cache (1 MB of means: latency, not bandwidth).
+// thread walks a list alone: 39 -> 16 us for four queries at the million-token
+// cache (1 MB of means: latency, not bandwidth).
+//
+// With at most kOwnGate blocks there is no such launch: every split chooses for
+// its row itself (choose_blocks), which costs it less than the launch and the
+// wait for it would.
 constexpr int kGateThreads = 256;
 constexpr int kGateRows = 16;      // q rows of a group at a time
 constexpr int kGateBlocks = 1024;  // blocks whose scores fit: 64 KB
 
+constexpr int kOwnGate = 64;
+
+// The index row of heads h0 .. h0 + n - 1 taken together (n > 1: shared
+// routing), by a whole CTA into shared memory.
+struct OwnGate {
+  float score[kOwnGate];
+  int32_t list[32];
+};
+template <typename T, int D, int kThreads>
+__device__ __forceinline__ void choose_blocks(const Step& a, const T* __restrict__ q, int qi, int r,
+                                              int h0, int n, int p, float* qs, OwnGate& og) {
+  const Dims& dm = a.dm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = h0 / (dm.Hq / dm.Hkv), c = p / dm.B, need = min(dm.topk - 1, c);
+  for (int x = tid; x < D; x += kThreads) {
+    float s = 0.f;
+    for (int j = 0; j < n; ++j) s += to_f32(q[((int64_t)qi * dm.Hq + h0 + j) * D + x]);
+    qs[x] = s;
+  }
+  __syncthreads();
+  constexpr int LPB = D / 4, BPW = 32 / LPB, U = 4, stride = kThreads / 32 * BPW;
+  const int sub = lane % LPB, i_first = warp * BPW + lane / LPB;
+  const float4 qv = reinterpret_cast<const float4*>(qs)[sub];
+  for (int i0 = i_first; need > 0 && __any_sync(0xffffffffu, i0 < c); i0 += stride * U) {
+    float4 kv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * stride;
+      kv[u] = i < c ? __ldg(reinterpret_cast<const float4*>(
+                                a.kbar + (((int64_t)r * dm.nb + i) * dm.Hkv + g) * D) + sub)
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float acc = fmaf(kv[u].w, qv.w, fmaf(kv[u].z, qv.z, fmaf(kv[u].y, qv.y, kv[u].x * qv.x)));
+#pragma unroll
+      for (int off = LPB / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+      if (sub == 0 && i0 + u * stride < c) og.score[i0 + u * stride] = acc;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    float v[2] = {lane < c ? og.score[lane] : NAN, lane + 32 < c ? og.score[lane + 32] : NAN};
+    uint32_t f[2] = {0u, 0u};  // chosen among blocks 0 .. 31 and 32 .. 63
+    int taken = 0;
+    for (; taken < need; ++taken) {
+      float bs = -INFINITY;
+      int bi = INT_MAX;
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+        if (v[z] > bs || (v[z] == bs && lane + 32 * z < bi)) {
+          bs = v[z];
+          bi = lane + 32 * z;
+        }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        const float os = __shfl_xor_sync(0xffffffffu, bs, off);
+        const int oi = __shfl_xor_sync(0xffffffffu, bi, off);
+        if (os > bs || (os == bs && oi < bi)) {
+          bs = os;
+          bi = oi;
+        }
+      }
+      if (bi == INT_MAX) break;  // only NaN scores are left
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        if (bi == lane + 32 * z) v[z] = NAN;
+        if (bi / 32 == z) f[z] |= 1u << (bi & 31);
+      }
+    }
+    const uint32_t below = (1u << lane) - 1;
+    if (f[0] >> lane & 1) og.list[__popc(f[0] & below)] = lane;
+    if (f[1] >> lane & 1) og.list[__popc(f[0]) + __popc(f[1] & below)] = lane + 32;
+    if (taken + lane < dm.topk) og.list[taken + lane] = lane == 0 ? c : -1;
+  }
+  __syncthreads();
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kGateThreads)
-cache_gate_kernel(const Step a, const T* __restrict__ q, const float* __restrict__ kbar,
-                  int32_t* __restrict__ idx, const int cs) {
+cache_gate_kernel(const Step a, const T* __restrict__ q, const int cs) {
   extern __shared__ __align__(16) float score[];  // [rows][c]
   __shared__ __align__(16) float qs[kGateRows][D];
   __shared__ uint32_t chosen[kGateRows][kGateBlocks / 32];
@@ -174,7 +258,7 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const float* __restrict
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u * stride;
         kv[u] = i < end ? __ldg(reinterpret_cast<const float4*>(
-                                    kbar + (((int64_t)r * dm.nb + i) * dm.Hkv + g) * D) + sub)
+                                    a.kbar + (((int64_t)r * dm.nb + i) * dm.Hkv + g) * D) + sub)
                         : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       for (int j = 0; j < rows; ++j) {
@@ -241,7 +325,7 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const float* __restrict
     at -= __popc(f);
     const int copies = dm.shared ? grp : 1;
     for (int x = 0; x < copies; ++x) {
-      int32_t* row = idx + ((int64_t)qi * dm.Hq + h0 + (dm.shared ? x : j)) * dm.topk;
+      int32_t* row = a.idx + ((int64_t)qi * dm.Hq + h0 + (dm.shared ? x : j)) * dm.topk;
       int o = at;
       for (uint32_t m = f; m; m &= m - 1) row[o++] = lane * 32 + __ffs(m) - 1;
       if (n + lane < dm.topk) row[n + lane] = lane == 0 ? c : -1;
@@ -317,6 +401,8 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   __shared__ __align__(16) uint8_t scales[kW][kStages][2][kStep];
   __shared__ int page_row[kMaxPages];
   __shared__ float wm[kW][kHeads], wo[kW][kHeads], wl[kW][kHeads];
+  __shared__ __align__(16) float qs[D];
+  __shared__ OwnGate og;
   __shared__ int abort_flag;
   constexpr int NC = D / 64;  // 16-byte pieces of a row a lane holds
   using R = Ring<D>;
@@ -381,16 +467,26 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   tc::mbar_fence_init();
   int r, len, p;
   const bool valid =
-      tail_position(a.cu_q, cc.lens, dm.batch, a.max_len, qi, r, p, len, nullptr, true);
+      tail_position(a.cu_q, cc.lens, dm.batch, a.max_len, qi, r, p, len,
+                    a.gated ? nullptr : a.status, true);
   tc::grid_wait();  // the chosen blocks
   if (!valid) return;
+  const int32_t* list = a.idx + row0 * dm.topk;
+  if (!a.gated && a.sp.groups > 0 && s < a.sp.groups * a.sp.parts) {
+    choose_blocks<__nv_bfloat16, D, kW * 32>(a, q, qi, r, dm.shared ? g * grp : h0,
+                                             dm.shared ? grp : 1, p, qs, og);
+    list = og.list;
+  }
+  if (!a.gated && s == 0)
+    for (int e = tid; e < nh * dm.topk; e += kW * 32)
+      a.idx[row0 * dm.topk + e] = a.sp.groups > 0 ? og.list[e % dm.topk] : p / dm.B;
   const int page = 1 << cc.page_log2;
   // lane x of every warp: slot x of the split, its keys, steps and page entries
   int my_lo = 0, my_hi = 0, my_step, my_page;  // step: one past the slot's last; page: its first
   {
     int first, last;
     split_slots(a, s, first, last);
-    if (first + lane < last) slot_range(a, row0, s, first + lane, p, my_lo, my_hi);
+    if (first + lane < last) slot_range(a, list, s, first + lane, p, my_lo, my_hi);
     const int t0 = my_lo & ~15, np = my_lo < my_hi ? ((my_hi - 1) / page - t0 / page) + 1 : 0;
     my_step = my_lo < my_hi ? (my_hi - t0 + kStep - 1) / kStep : 0;
     my_page = np;
@@ -734,6 +830,7 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
   __shared__ float wm[kWarps], wl[kWarps];
   __shared__ __align__(16) float wo[kWarps][D];
   __shared__ int page_row[kMaxPages];
+  __shared__ OwnGate og;
   tc::grid_let_next();
   const Dims& dm = a.dm;
   const Cache& c = a.c;
@@ -742,10 +839,20 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = (int64_t)qi * dm.Hq + h, prow = row * S + s;
   int r, len, p;
-  const bool valid = tail_position(a.cu_q, c.lens, dm.batch, a.max_len, qi, r, p, len, nullptr, true);
+  const bool valid = tail_position(a.cu_q, c.lens, dm.batch, a.max_len, qi, r, p, len,
+                                   a.gated ? nullptr : a.status, true);
   tc::grid_wait();  // the chosen blocks
   if (!valid) return;
-  const int g = h / (dm.Hq / dm.Hkv);
+  const int grp = dm.Hq / dm.Hkv, g = h / grp;
+  const int32_t* list = a.idx + row * dm.topk;
+  if (!a.gated && a.sp.groups > 0 && s < a.sp.groups * a.sp.parts) {
+    choose_blocks<float, D, kThreads>(a, q, qi, r, dm.shared ? g * grp : h, dm.shared ? grp : 1, p,
+                                      &wo[0][0], og);
+    list = og.list;
+  }
+  if (!a.gated && s == 0)
+    for (int e = tid; e < dm.topk; e += kThreads)
+      a.idx[row * dm.topk + e] = a.sp.groups > 0 ? og.list[e] : p / dm.B;
   const int grp_id = warp * GPW + lane / LPK, sub = lane % LPK;
   const float sl2 = kLog2e * rsqrtf((float)D);
   float qv[16];
@@ -759,7 +866,7 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
   split_slots(a, s, first, last);
   for (int slot = first; slot < last; ++slot) {
   int lo, hi;
-  slot_range(a, row, s, slot, p, lo, hi);
+  slot_range(a, list, s, slot, p, lo, hi);
   const int p0 = lo >> c.page_log2;
   __syncthreads();
   load_pages<kThreads>(a, r, g, lo, hi, page_row);
@@ -912,8 +1019,7 @@ cache_merge_kernel(const Step a, T* __restrict__ out, float* __restrict__ lse_ou
 }
 
 template <typename T, int D>
-cudaError_t run_gate(const Step& a, const void* q, const float* kbar, int32_t* idx,
-                     cudaStream_t st) {
+cudaError_t run_gate(const Step& a, const void* q, cudaStream_t st) {
   const Dims& dm = a.dm;
   const int grp = dm.Hq / dm.Hkv, rows = dm.shared ? 1 : grp < kGateRows ? grp : kGateRows;
   const int chunks = dm.shared ? 1 : (grp + kGateRows - 1) / kGateRows;
@@ -928,18 +1034,17 @@ cudaError_t run_gate(const Step& a, const void* q, const float* kbar, int32_t* i
                           ready)))
     return e;
   return tc::launch_cluster(cache_gate_kernel<T, D>, dim3((unsigned)grid), kGateThreads, smem, st, cs,
-                            a, static_cast<const T*>(q), kbar, idx, cs);
+                            a, static_cast<const T*>(q), cs);
 }
 
 template <typename T, int D>
-cudaError_t run(const Step& a, const void* q, const float* kbar, int32_t* idx, void* out,
-                float* lse, cudaStream_t st) {
+cudaError_t run(const Step& a, const void* q, void* out, float* lse, cudaStream_t st) {
   const Dims& dm = a.dm;
-  cudaError_t e;
-  if (dm.nb <= kGateBlocks)
-    e = run_gate<T, D>(a, q, kbar, idx, st);
-  else  // lists in registers instead of all scores in shared memory
-    e = launch_cache_gate(dm, q, kbar, a.c.lens, a.cu_q, idx, a.max_len, a.status, st);
+  cudaError_t e = cudaSuccess;
+  if (a.gated && dm.nb <= kGateBlocks)
+    e = run_gate<T, D>(a, q, st);
+  else if (a.gated)  // lists in registers instead of all scores in shared memory
+    e = launch_cache_gate(dm, q, a.kbar, a.c.lens, a.cu_q, a.idx, a.max_len, a.status, st);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)dm.T * dm.Hq;
   if constexpr (sizeof(T) == 2) {
@@ -954,15 +1059,15 @@ cudaError_t run(const Step& a, const void* q, const float* kbar, int32_t* idx, v
                                   : (int64_t)dm.Hkv * hc * a.sp.parts +
                                         (int64_t)dm.Hq * a.sp.groups * a.sp.parts;
     if (per * dm.T > INT32_MAX || rows > INT32_MAX) return cudaErrorInvalidValue;
-    e = tc::launch_beside(cache_attn_tc<D>, dim3((unsigned)(per * dm.T)), kW * 32,
-                          Ring<D>::kBytes, st, 1, mk, mv, a, static_cast<const __nv_bfloat16*>(q),
+    e = tc::launch_with(a.gated, cache_attn_tc<D>, dim3((unsigned)(per * dm.T)), kW * 32,
+                        Ring<D>::kBytes, st, 1, mk, mv, a, static_cast<const __nv_bfloat16*>(q),
                           static_cast<__nv_bfloat16*>(out), lse);
     if (e != cudaSuccess || a.sp.per_row == 1) return e;
   } else {
     const int64_t x = (int64_t)a.sp.per_row * dm.T;
     if (x > INT32_MAX || rows > INT32_MAX) return cudaErrorInvalidValue;
-    e = tc::launch_beside(cache_attn_kernel<D>, dim3((unsigned)x, (unsigned)dm.Hq), kThreads, 0, st, 1, a,
-                      static_cast<const float*>(q));
+    e = tc::launch_with(a.gated, cache_attn_kernel<D>, dim3((unsigned)x, (unsigned)dm.Hq), kThreads,
+                        0, st, 1, a, static_cast<const float*>(q));
   }
   if (e != cudaSuccess) return e;
   return tc::launch_beside(cache_merge_kernel<T, D>, dim3((unsigned)rows), kMergeWarps * 32, 0, st, 1, a,
@@ -979,16 +1084,23 @@ cudaError_t launch_decode_cache(const Dims& dm, const Cache& c, const void* q, c
                                 const int32_t* cu_q, int32_t* idx, float* part_o, float* part_lse,
                                 void* out, float* lse, int* status, cudaStream_t st) {
   const int64_t held = (int64_t)c.max_pages << c.page_log2;
-  const Step a{dm,     c,
-               split_of(dm), cu_q,
-               idx,    part_o,
-               part_lse, held < dm.max_seqlen ? (int)held : dm.max_seqlen,
-               status};
+  Step a{};
+  a.dm = dm;
+  a.c = c;
+  a.sp = split_of(dm);
+  a.cu_q = cu_q;
+  a.kbar = kbar;
+  a.idx = idx;
+  a.gated = dm.nb > kOwnGate;
+  a.part_o = part_o;
+  a.part_lse = part_lse;
+  a.max_len = held < dm.max_seqlen ? (int)held : dm.max_seqlen;
+  a.status = status;
   if (dm.dtype == kBF16)
-    return dm.d == 128 ? run<__nv_bfloat16, 128>(a, q, kbar, idx, out, lse, st)
-                       : run<__nv_bfloat16, 64>(a, q, kbar, idx, out, lse, st);
-  return dm.d == 128 ? run<float, 128>(a, q, kbar, idx, out, lse, st)
-                     : run<float, 64>(a, q, kbar, idx, out, lse, st);
+    return dm.d == 128 ? run<__nv_bfloat16, 128>(a, q, out, lse, st)
+                       : run<__nv_bfloat16, 64>(a, q, out, lse, st);
+  return dm.d == 128 ? run<float, 128>(a, q, out, lse, st)
+                     : run<float, 64>(a, q, out, lse, st);
 }
 
 }  // namespace moba
