@@ -333,10 +333,13 @@ typedef struct {
  * cache. kbar, if not NULL (fp32 [batch][moba_num_blocks(p)][Hkv][d]): the
  * mean of every block that these rows complete, over the rows as the cache
  * holds them (what a decode query of a later position scores); other entries
- * are left alone. cu_new: device int32 [batch + 1]. */
+ * are left alone. cu_new: device int32 [batch + 1]. ws: with kbar,
+ * moba_cache_write_workspace_size(p) bytes (0 for a few rows), 32-byte aligned;
+ * else not used. */
+MOBA_API size_t moba_cache_write_workspace_size(const moba_params* p);
 MOBA_API moba_status moba_cache_write(const moba_params* p, const moba_cache* c, const void* k,
-                                      const void* v, const int32_t* cu_new, float* kbar,
-                                      void* stream);
+                                      const void* v, const int32_t* cu_new, float* kbar, void* ws,
+                                      size_t ws_bytes, void* stream);
 
 /* Reads each request's last cu_rows[r+1] - cu_rows[r] positions back into
  * k, v [total_tokens][Hkv][d] (p->dtype). cu_rows: device int32 [batch + 1]. */

@@ -141,11 +141,12 @@ class _CacheStruct(ctypes.Structure):
 _PARAMS, _CACHE, _V = ctypes.POINTER(MobaParams), ctypes.POINTER(_CacheStruct), ctypes.c_void_p
 _SIGNATURES = {
     "dense_causal_backward": [_PARAMS] + [_V] * 11 + [ctypes.c_size_t, _V],
-    "moba_cache_write": [_PARAMS, _CACHE] + [_V] * 5,
+    "moba_cache_write": [_PARAMS, _CACHE] + [_V] * 5 + [ctypes.c_size_t, _V],
     "moba_cache_read": [_PARAMS, _CACHE] + [_V] * 4,
     "moba_decode_cache": [_PARAMS, _V, _CACHE] + [_V] * 6 + [ctypes.c_size_t, _V],
     "dense_causal_backward_workspace_size": [_PARAMS],
     "moba_decode_cache_workspace_size": [_PARAMS],
+    "moba_cache_write_workspace_size": [_PARAMS],
 }
 _bound = {}  # entry points with their signatures set, by name
 
@@ -582,7 +583,8 @@ def _check_kbar(kbar, batch: int, heads: int, head_dim: int, block_size: int) ->
 
 
 def moba_cache_write(cache: MobaCache, k, v, page_table, seqlens, cu_new,
-                     kbar: Optional[torch.Tensor] = None, block_size: Optional[int] = None) -> None:
+                     kbar: Optional[torch.Tensor] = None, block_size: Optional[int] = None,
+                     ws: Optional[torch.Tensor] = None) -> None:
     """Quantise new rows k, v [n, Hkv, d] into the cache: request r's rows cu_new[r] ..
     cu_new[r+1]-1 go to its last positions (seqlens[r] counts them already) in the pages that
     page_table [batch, max_pages] names; rows behind cu_new[batch] are ignored. With kbar
@@ -590,7 +592,7 @@ def moba_cache_write(cache: MobaCache, k, v, page_table, seqlens, cu_new,
     are written too. page_table, seqlens, cu_new: int32 on the cache's device."""
     _check_qkv(k, k, v)
     n, hkv, d = k.shape
-    c = _check_cache(cache, hkv, d, page_table, seqlens, cu_new, k, v, kbar)
+    c = _check_cache(cache, hkv, d, page_table, seqlens, cu_new, k, v, kbar, ws)
     batch, longest, B = page_table.shape[0], 2**31 - 1, 1
     if kbar is not None:
         if block_size is None:
@@ -598,7 +600,11 @@ def moba_cache_write(cache: MobaCache, k, v, page_table, seqlens, cu_new,
         B = int(block_size)
         longest = _check_kbar(kbar, batch, hkv, d, B)
     p = _cache_params(batch, n, hkv, hkv, d, k.dtype, B, 1, longest)
-    _call("moba_cache_write", k.device, p, c, _at(k), _at(v), _at(cu_new), _at(kbar))
+    if kbar is not None and ws is None:
+        need = _entry("moba_cache_write_workspace_size")(p)
+        ws = torch.empty(need, dtype=torch.uint8, device=k.device) if need else None
+    _call("moba_cache_write", k.device, p, c, _at(k), _at(v), _at(cu_new), _at(kbar), _at(ws),
+          0 if ws is None else _nbytes(ws))
 
 
 def moba_cache_read(cache: MobaCache, page_table, seqlens, cu_rows, total_rows: int,

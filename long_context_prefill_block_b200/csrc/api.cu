@@ -611,8 +611,15 @@ moba_status dense_causal_backward(const moba_params* p, const void* q, const voi
   return cuda_status(launch(dm, q, k, v, dout, stat, cu_seqlens, dq, dk, dv, status, st));
 }
 
+size_t moba_cache_write_workspace_size(const moba_params* p) {
+  Dims dm;
+  if (validate(p, dm) != MOBA_OK) return 0;
+  return align256(sizeof(float) * cache_sums_floats(dm));
+}
+
 moba_status moba_cache_write(const moba_params* p, const moba_cache* c, const void* k,
-                             const void* v, const int32_t* cu_new, float* kbar, void* stream) {
+                             const void* v, const int32_t* cu_new, float* kbar, void* ws,
+                             size_t ws_bytes, void* stream) {
   Dims dm;
   Cache cv;
   moba_status s = validate(p, dm);
@@ -621,11 +628,16 @@ moba_status moba_cache_write(const moba_params* p, const moba_cache* c, const vo
   if ((s = check_cache(c, dm.Hkv, cv)) != MOBA_OK) return s;
   if (!k || !v || !cu_new || !aligned32(k) || !aligned32(v) || (kbar && !aligned32(kbar)))
     return MOBA_ERR_INVALID_ARG;
+  float* sums = nullptr;
+  if (const size_t need = kbar ? align256(sizeof(float) * cache_sums_floats(dm)) : 0) {
+    if (!ws || ws_bytes < need || !aligned32(ws)) return MOBA_ERR_WORKSPACE;
+    sums = static_cast<float*>(ws);
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int* status = status_word();
   if (!status) return MOBA_ERR_CUDA;
-  MOBA_TRY(launch_cache_write(dm, cv, k, v, cu_new, status, st));
-  if (kbar) MOBA_TRY(launch_cache_means(dm, cv, cu_new, kbar, status, st));
+  MOBA_TRY(launch_cache_write(dm, cv, k, v, cu_new, sums, status, st));
+  if (kbar) MOBA_TRY(launch_cache_means(dm, cv, cu_new, sums, kbar, status, st));
   return MOBA_OK;
 }
 

@@ -30,65 +30,74 @@ __device__ __forceinline__ int row_exponent(uint32_t top) {
   return top < 0x00800000u || e < -127 ? -127 : e;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+
 // 16 bytes of a row: as they are, their largest magnitude as fp32 bits, and
 // as fp32 values.
 __device__ __forceinline__ uint32_t top_of(const uint4& r, __nv_bfloat16) {
-  const uint32_t a = __vmaxu2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu);
-  const uint32_t b = __vmaxu2(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu);
-  const uint32_t c = __vmaxu2(a, b);
+  const uint32_t a = max_u16x2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu);
+  const uint32_t b = max_u16x2(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu);
+  const uint32_t c = max_u16x2(a, b);
   return max(c << 16, c & 0xffff0000u);
 }
 __device__ __forceinline__ uint32_t top_of(const uint4& r, float) {
   return max(max(r.x & 0x7fffffffu, r.y & 0x7fffffffu), max(r.z & 0x7fffffffu, r.w & 0x7fffffffu));
 }
-__device__ __forceinline__ void widen(const uint4& r, float (&x)[8]) {
+// 16 bytes of a row times 2^-e, e in [-127, 120] (so a normal number), as fp32.
+// For bf16 one multiply-add of mixed precision a value (exact), which spares
+// the integer pipe two unpacking instructions: it is the busier one here.
+__device__ __forceinline__ void scaled(const uint4& r, int e, float (&x)[8]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void widen(const uint4& r, float (&x)[4]) {
-  x[0] = __uint_as_float(r.x);
-  x[1] = __uint_as_float(r.y);
-  x[2] = __uint_as_float(r.z);
-  x[3] = __uint_as_float(r.w);
-}
-
-// Values x[0 .. N) of a row as N e4m3 bytes: e in [-127, 120], so 2^-e is a
-// normal number, and |x| * 2^-e <= 448.
-template <int N>
-__device__ __forceinline__ void encode(float (&x)[N], int e, uint32_t (&w)[N / 4]) {
-  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] *= f;
-  if (e >= 120) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = fminf(fmaxf(x[i], -240.f), 240.f);
-  }
-#pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[i], x[i + 1]), __NV_SATFINITE,
-                                                 __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[i + 2], x[i + 3]), __NV_SATFINITE,
-                                                 __NV_E4M3);
-    w[i / 4] = lo | hi << 16;
-  }
-}
-
-__device__ __forceinline__ void decode16(const uint4& r, float (&x)[16]) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  const uint16_t f = (uint16_t)((127 - e) << 7);  // bf16
 #pragma unroll
   for (int i = 0; i < 4; ++i)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "fma.rn.f32.bf16 %0, l, %3, %4;\n\tfma.rn.f32.bf16 %1, h, %3, %4;\n\t}"
+        : "=f"(x[2 * i]), "=f"(x[2 * i + 1])
+        : "r"(w[i]), "h"(f), "f"(0.f));
+}
+__device__ __forceinline__ void scaled(const uint4& r, int e, float (&x)[4]) {
+  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+  x[0] = __uint_as_float(r.x) * f;
+  x[1] = __uint_as_float(r.y) * f;
+  x[2] = __uint_as_float(r.z) * f;
+  x[3] = __uint_as_float(r.w) * f;
+}
+
+// Scaled values, |x| <= 448, as e4m3 bytes.
+template <int N>
+__device__ __forceinline__ void encode(const float (&x)[N], uint32_t (&w)[N / 4]) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] >> (16 * u)),
-                                                       __NV_E4M3);
-      const float2 f = __half22float2(__half2(h));
-      x[4 * i + 2 * u] = f.x;
-      x[4 * i + 2 * u + 1] = f.y;
-    }
+  for (int i = 0; i < N; i += 4)
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
+        : "=r"(w[i / 4])
+        : "f"(x[i]), "f"(x[i + 1]), "f"(x[i + 2]), "f"(x[i + 3]));
+}
+
+__device__ __forceinline__ void decode4(uint32_t four, float* x) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  x[0] = a.x;
+  x[1] = a.y;
+  x[2] = b.x;
+  x[3] = b.y;
+}
+__device__ __forceinline__ void decode16(const uint4& r, float (&x)[16]) {
+  decode4(r.x, x);
+  decode4(r.y, x + 4);
+  decode4(r.z, x + 8);
+  decode4(r.w, x + 12);
 }
 
 // Row index in the cache of position pos of request r and kv head g, or -1
@@ -142,11 +151,17 @@ __device__ __forceinline__ int token_row(const Dims& dm, const Cache& c,
 
 // Quantise and store: a row is held by LPR lanes of 16 bytes, which share its
 // maximum (as integers: an infinity or NaN is above every number). U rows' loads
-// a lane are in flight. Bound by HBM: d * sizeof(T) bytes in, d + 1 out.
+// a lane are in flight. Bound by HBM: d * sizeof(T) bytes in, d + 1 out; 262144
+// tokens of 8 heads, bf16, d = 128: 257 us, 6.2 TB/s. (A lane group a row of any
+// head, with a table look-up before each store and one-byte scale stores: 663.)
+//
+// sums: with 32 tokens a warp, also the sum of each warp's rows of K as stored,
+// [token / 32][head][d], which the block means are made of.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 cache_write_kernel(Dims dm, Cache c, const T* __restrict__ k, const T* __restrict__ v,
-                   const int32_t* __restrict__ cu_new, int tpw, int* status) {
+                   const int32_t* __restrict__ cu_new, int tpw, float* __restrict__ sums,
+                   int* status) {
   constexpr int VEC = Vec16<T>::N, LPR = D / VEC, RPS = 32 / LPR, U = 8;  // rows a step
   tc::grid_let_next();
   const int lane = threadIdx.x & 31, sub = lane % LPR, sel = lane / LPR;
@@ -157,6 +172,10 @@ cache_write_kernel(Dims dm, Cache c, const T* __restrict__ k, const T* __restric
   if (p.n <= 0) return;
   const T* base = src + ((int64_t)p.t0 * dm.Hkv + p.g) * D + sub * VEC;
   uint32_t mine = 255;  // lane t: scale byte of token t
+  const bool add = sums && blockIdx.y == 0;
+  float acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
   for (int s0 = 0; s0 < p.n; s0 += RPS * U) {
     uint4 x[U];
 #pragma unroll
@@ -174,15 +193,20 @@ cache_write_kernel(Dims dm, Cache c, const T* __restrict__ k, const T* __restric
       for (int off = LPR / 2; off > 0; off >>= 1)
         top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
       const bool fine = top < 0x7f800000u;
-      const int e = fine ? row_exponent(top) : -127;
+      const int e = row_exponent(top);
       float y[VEC];
-      widen(x[u], y);
-      if (!fine) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) y[i] = 0.f;
-      }
+      scaled(x[u], e, y);
       uint32_t w[VEC / 4];
-      encode<VEC>(y, e, w);
+      encode<VEC>(y, w);
+      // rare, so behind a branch of the whole warp: rows that are not finite,
+      // and codes above 240 (0x77) from e = 120 on
+      if (__any_sync(0xffffffffu, top >= 0x7e800000u)) {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+          if (e >= 120) w[i] = (w[i] & 0x80808080u) | __vminu4(w[i] & 0x7f7f7f7fu, 0x77777777u);
+          if (!fine) w[i] = 0;
+        }
+      }
       const int row = __shfl_sync(0xffffffffu, p.row, t & 31);
       if (t < p.n && row >= 0) {
         uint8_t* dst = codes + (int64_t)row * D + sub * VEC;
@@ -192,31 +216,53 @@ cache_write_kernel(Dims dm, Cache c, const T* __restrict__ k, const T* __restric
           *reinterpret_cast<uint32_t*>(dst) = w[0];
       }
       const uint32_t byte = fine ? (uint32_t)(e + 127) : 255u;
+      if (add && t < p.n && row >= 0) {
+        const float f = e8m0_value(byte);
 #pragma unroll
-      for (int q = 0; q < RPS; ++q) {
-        const uint32_t b = __shfl_sync(0xffffffffu, byte, q * LPR);
-        if (lane == s0 + u * RPS + q) mine = b;
+        for (int i = 0; i < VEC / 4; ++i) {
+          float z[4];
+          decode4(w[i], z);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[4 * i + q] = fmaf(z[q], f, acc[4 * i + q]);
+        }
       }
+      // lane t takes token t's byte from the lanes that hold its row
+      const uint32_t b = __shfl_sync(0xffffffffu, byte, lane % RPS * LPR);
+      if (lane / RPS == s0 / RPS + u) mine = b;
     }
   }
   if (lane < p.n && p.row >= 0) scales[p.row] = (uint8_t)mine;
+  if (add) {
+#pragma unroll
+    for (int off = LPR; off < 32; off <<= 1)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+    float* dst = sums + ((int64_t)(p.t0 / 32) * dm.Hkv + p.g) * D + sub * VEC;
+    if (sel == 0) {
+#pragma unroll
+      for (int i = 0; i < VEC; i += 4)
+        *reinterpret_cast<float4*>(dst + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+    }
+  }
 }
 
 // Mean of each block that the new rows complete, over the rows as the cache
 // holds them. Slot j of the grid: request r's completed blocks have slots
 // from cu_new[r] / B + r on (n / B + 1 of them at most). One cluster per
-// (slot, kv head), its CTAs taking equal parts of the block: LPR lanes of 16
-// bytes a row, fp32 sums of every G-th row, then the lane groups' sums and the
-// CTAs' sums in order. Bound by the codes' bytes for long prompts, by latency
-// for one block (a 4096-key block: four CTAs).
+// (slot, kv head), its CTAs taking equal parts of the block. Where the write
+// left sums of 32 packed rows, those inside a part are added up (1/8 of the
+// codes' bytes); the other rows are read: LPR lanes of 16 bytes a row, fp32 sums
+// of every G-th row, then the lane groups' sums and the CTAs' sums in order.
+// Reading all 268 MB of codes again cost 67 us behind the 257 of the write.
 constexpr int kMeanPages = 2048 / 16 + 1;  // pages looked up at a time
 
 template <int D>
 __global__ void __launch_bounds__(kMeanThreads, 4)
 cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
-                   float* __restrict__ kbar, int cs, int* status) {
+                   const float* __restrict__ sums, float* __restrict__ kbar, int cs, int* status) {
   constexpr int LPR = D / 16, G = kMeanThreads / LPR, U = 8;
-  __shared__ float sum[G][D + 4];
+  constexpr int LPS = D / 4, GS = kMeanThreads / LPS;  // lanes and streams of sums
+  __shared__ float sum[G + GS][D + 4];
   __shared__ float part[kMaxCluster][D];
   __shared__ int page_row[kMeanPages];
   const int g = blockIdx.y, B = dm.B, slot = blockIdx.x / cs, rank = blockIdx.x % cs;
@@ -230,61 +276,92 @@ cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
     r += k * step;
   }
   // every early return below is the whole cluster's
-  int blk = -1;
+  int blk = -1, begin = 0, row0 = 0;  // begin, row0: position and packed row of the first new row
   if (r < dm.batch) {
     const int n = cu_new[r + 1] - cu_new[r], len = c.lens[r];
     if (n > 0 && len >= n && len <= max_positions(dm, c)) {
-      blk = (len - n) / B + slot - (cu_new[r] / B + r);
+      begin = len - n;
+      row0 = cu_new[r];
+      blk = begin / B + slot - (row0 / B + r);
       if (blk >= len / B || blk >= dm.nb) blk = -1;
     }
   }
   tc::grid_wait();  // the rows
   if (blk < 0) return;
-  const int per = (B + cs - 1) / cs, first = blk * B + rank * per;
-  const int last = min(first + per, (blk + 1) * B);
+  const int per = (B + cs - 1) / cs, first = blk * B + min(rank * per, B);
+  const int last = blk * B + min(rank * per + per, B);
   const int sub = threadIdx.x % LPR, grp = threadIdx.x / LPR, mask = (1 << c.page_log2) - 1;
+  // groups of 32 packed rows that lie inside [first, last): [g0, g1)
+  int g0 = 0, g1 = 0, lo = last, hi = last;  // rows outside them: [first, lo), [hi, last)
+  if (sums && last > begin) {
+    g0 = (row0 + max(first, begin) - begin + 31) / 32;
+    g1 = (row0 + last - begin) / 32;
+    if (g1 > g0) {
+      lo = begin + g0 * 32 - row0;
+      hi = begin + g1 * 32 - row0;
+    }
+  }
   float acc[16];
 #pragma unroll
   for (int x = 0; x < 16; ++x) acc[x] = 0.f;
-  for (int c0 = first; c0 < last; c0 += 2048) {
-    const int c1 = min(c0 + 2048, last), p0 = c0 >> c.page_log2;
-    __syncthreads();
-    for (int i = threadIdx.x; i <= ((c1 - 1) >> c.page_log2) - p0; i += kMeanThreads) {
-      const int64_t row = cache_page_row(c, dm.Hkv, c.table[(int64_t)r * c.max_pages + p0 + i], g);
-      page_row[i] = (int)row;
-      if (row < 0) set_status(status, kStBadIndices);
-    }
-    __syncthreads();
-    for (int j0 = c0 + grp; j0 < c1; j0 += G * U) {
-      uint4 w[U];
-      float s[U];
+  auto add_rows = [&](int from, int to) {
+    for (int c0 = from; c0 < to; c0 += 2048) {
+      const int c1 = min(c0 + 2048, to), p0 = c0 >> c.page_log2;
+      __syncthreads();
+      for (int i = threadIdx.x; i <= ((c1 - 1) >> c.page_log2) - p0; i += kMeanThreads) {
+        const int64_t row =
+            cache_page_row(c, dm.Hkv, c.table[(int64_t)r * c.max_pages + p0 + i], g);
+        page_row[i] = (int)row;
+        if (row < 0) set_status(status, kStBadIndices);
+      }
+      __syncthreads();
+      for (int j0 = c0 + grp; j0 < c1; j0 += G * U) {
+        uint4 w[U];
+        float s[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * G;
-        const int pr = j < c1 ? page_row[(j >> c.page_log2) - p0] : -1;
-        w[u] = make_uint4(0, 0, 0, 0);
-        s[u] = 0.f;
-        if (pr >= 0) {
-          const int64_t row = pr + (j & mask);
-          w[u] = *reinterpret_cast<const uint4*>(c.k + row * D + sub * 16);
-          s[u] = e8m0_value(c.ks[row]);
+        for (int u = 0; u < U; ++u) {
+          const int j = j0 + u * G;
+          const int pr = j < c1 ? page_row[(j >> c.page_log2) - p0] : -1;
+          w[u] = make_uint4(0, 0, 0, 0);
+          s[u] = 0.f;
+          if (pr >= 0) {
+            const int64_t row = pr + (j & mask);
+            w[u] = *reinterpret_cast<const uint4*>(c.k + row * D + sub * 16);
+            s[u] = e8m0_value(c.ks[row]);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float x[16];
+          decode16(w[u], x);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[e] = fmaf(x[e], s[u], acc[e]);
         }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float x[16];
-        decode16(w[u], x);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[e] = fmaf(x[e], s[u], acc[e]);
-      }
     }
-  }
+  };
+  add_rows(first, lo);
+  add_rows(hi, last);
 #pragma unroll
   for (int x = 0; x < 16; ++x) sum[grp][sub * 16 + x] = acc[x];
+  {
+    const int ss = threadIdx.x % LPS, sg = threadIdx.x / LPS;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = g0 + sg; i < g1; i += GS) {
+      const float4 v =
+          __ldg(reinterpret_cast<const float4*>(sums + ((int64_t)i * dm.Hkv + g) * D) + ss);
+      t.x += v.x;
+      t.y += v.y;
+      t.z += v.z;
+      t.w += v.w;
+    }
+    *reinterpret_cast<float4*>(&sum[G + sg][ss * 4]) = t;
+  }
   tc::cluster_sync();
   for (int x = threadIdx.x; x < D; x += kMeanThreads) {
     float t = 0.f;
-    for (int i = 0; i < G; ++i) t += sum[i][x];
+    for (int i = 0; i < G + GS; ++i) t += sum[i][x];
     tc::store_first(&part[rank][x], t);
   }
   tc::cluster_sync();
@@ -364,10 +441,10 @@ dim3 warp_grid(const Dims& dm, int tpw) {
 
 template <typename T, int D>
 cudaError_t run_write(const Dims& dm, const Cache& c, const void* k, const void* v,
-                      const int32_t* cu_new, int* status, cudaStream_t st) {
+                      const int32_t* cu_new, float* sums, int* status, cudaStream_t st) {
   const int tpw = tokens_per_warp(dm);
   cache_write_kernel<T, D><<<warp_grid(dm, tpw), kThreads, 0, st>>>(
-      dm, c, static_cast<const T*>(k), static_cast<const T*>(v), cu_new, tpw, status);
+      dm, c, static_cast<const T*>(k), static_cast<const T*>(v), cu_new, tpw, sums, status);
   return cudaGetLastError();
 }
 
@@ -382,23 +459,27 @@ cudaError_t run_read(const Dims& dm, const Cache& c, const int32_t* cu_rows, voi
 
 }  // namespace
 
-cudaError_t launch_cache_write(const Dims& dm, const Cache& c, const void* k, const void* v,
-                               const int32_t* cu_new, int* status, cudaStream_t st) {
-  if (dm.dtype == kBF16)
-    return dm.d == 128 ? run_write<__nv_bfloat16, 128>(dm, c, k, v, cu_new, status, st)
-                       : run_write<__nv_bfloat16, 64>(dm, c, k, v, cu_new, status, st);
-  return dm.d == 128 ? run_write<float, 128>(dm, c, k, v, cu_new, status, st)
-                     : run_write<float, 64>(dm, c, k, v, cu_new, status, st);
+size_t cache_sums_floats(const Dims& dm) {
+  return tokens_per_warp(dm) == 32 ? (size_t)((dm.T + 31) / 32) * dm.Hkv * dm.d : 0;
 }
 
-cudaError_t launch_cache_means(const Dims& dm, const Cache& c, const int32_t* cu_new, float* kbar,
-                               int* status, cudaStream_t st) {
+cudaError_t launch_cache_write(const Dims& dm, const Cache& c, const void* k, const void* v,
+                               const int32_t* cu_new, float* sums, int* status, cudaStream_t st) {
+  if (dm.dtype == kBF16)
+    return dm.d == 128 ? run_write<__nv_bfloat16, 128>(dm, c, k, v, cu_new, sums, status, st)
+                       : run_write<__nv_bfloat16, 64>(dm, c, k, v, cu_new, sums, status, st);
+  return dm.d == 128 ? run_write<float, 128>(dm, c, k, v, cu_new, sums, status, st)
+                     : run_write<float, 64>(dm, c, k, v, cu_new, sums, status, st);
+}
+
+cudaError_t launch_cache_means(const Dims& dm, const Cache& c, const int32_t* cu_new,
+                               const float* sums, float* kbar, int* status, cudaStream_t st) {
   const int64_t slots = (int64_t)dm.T / dm.B + dm.batch;
   const int cs = dm.B >= 1024 && slots * dm.Hkv < 2 * tc::sm_count() ? 4 : 1;
   if (slots * cs > INT32_MAX) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(slots * cs), (unsigned)dm.Hkv);
   const auto kernel = dm.d == 128 ? cache_means_kernel<128> : cache_means_kernel<64>;
-  return tc::launch_beside(kernel, grid, kMeanThreads, 0, st, cs, dm, c, cu_new, kbar, cs, status);
+  return tc::launch_beside(kernel, grid, kMeanThreads, 0, st, cs, dm, c, cu_new, sums, kbar, cs, status);
 }
 
 cudaError_t launch_cache_read(const Dims& dm, const Cache& c, const int32_t* cu_rows, void* k,

@@ -341,11 +341,13 @@ cudaError_t launch_dense_bwd_simt(const Dims& dm, const void* q, const void* k, 
                                   void* dk, void* dv, int* status, cudaStream_t st);
 
 // Paged 8-bit cache (cache.cu, decode_cache.cu); dm.T: the call's rows.
+// sums: scratch of cache_sums_floats (or nullptr), from which launch_cache_means
+// then makes the means of the blocks that the new rows complete.
+size_t cache_sums_floats(const Dims& dm);
 cudaError_t launch_cache_write(const Dims& dm, const Cache& c, const void* k, const void* v,
-                               const int32_t* cu_new, int* status, cudaStream_t st);
-// Means of the blocks that the new rows complete.
-cudaError_t launch_cache_means(const Dims& dm, const Cache& c, const int32_t* cu_new, float* kbar,
-                               int* status, cudaStream_t st);
+                               const int32_t* cu_new, float* sums, int* status, cudaStream_t st);
+cudaError_t launch_cache_means(const Dims& dm, const Cache& c, const int32_t* cu_new,
+                               const float* sums, float* kbar, int* status, cudaStream_t st);
 cudaError_t launch_cache_read(const Dims& dm, const Cache& c, const int32_t* cu_rows, void* k,
                               void* v, int* status, cudaStream_t st);
 // The decode gate with cache lengths in place of packed offsets (decode.cu).

@@ -469,7 +469,9 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   const bool valid =
       tail_position(a.cu_q, cc.lens, dm.batch, a.max_len, qi, r, p, len,
                     a.gated ? nullptr : a.status, true);
-  tc::grid_wait();  // the chosen blocks
+  // a split of own blocks alone needs no choice, and the merge waits for others
+  // that did wait
+  if (s < a.sp.groups * a.sp.parts || a.sp.groups == 0) tc::grid_wait();
   if (!valid) return;
   const int32_t* list = a.idx + row0 * dm.topk;
   if (!a.gated && a.sp.groups > 0 && s < a.sp.groups * a.sp.parts) {

@@ -109,6 +109,34 @@ def test_write_is_exact_and_touches_nothing_else(new, old, heads, d, page, B, dt
                 assert (got == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.bfloat16, 64),
+                                     (torch.float32, 128), (torch.float32, 64)])
+@pytest.mark.parametrize("B", [1000, 64, 4096])
+def test_means_of_long_appends(dtype, d, B):
+    """Enough rows that the write leaves sums of 32: blocks that begin in older rows, end inside a
+    group or hold none, requests whose rows begin inside a group."""
+    old, new, heads, page = [0, 777, 4000, 31], [5003, 4100, 96, 3000], 8, 32
+    lens = [a + b for a, b in zip(old, new)]
+    pool, _ = filled(lens, heads, d, page, B, seed=41)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    k, v = ((torch.randn(sum(new), heads, d, generator=g, device=DEV) + 0.5).to(dtype)
+            for _ in range(2))
+    nb = -(-max(lens) // B)
+    kbar = torch.full((4, nb, heads, d), 7.0, device=DEV)
+    moba.moba_cache_write(pool.cache, k, v, pool.table, i32(lens), offsets(new), kbar, B)
+    assert moba.moba_device_status() == 0
+    for r in range(4):
+        rows = contents(pool, r, lens[r])[0]
+        for i in range(nb):
+            got = kbar[r, i].double().cpu()
+            if old[r] // B <= i < lens[r] // B:
+                blk = rows[i * B:(i + 1) * B]
+                tol = B * 2.0 ** -24 * blk.abs().mean(dim=0)
+                assert ((got - blk.mean(dim=0)).abs() <= tol).all()
+            else:
+                assert (got == 7.0).all()
+
+
 def test_rows_at_the_ends_of_the_number_range():
     """Largest, smallest, subnormal, infinite and NaN rows; reading back stays finite where the
     input was, and NaN rows read back as NaN."""

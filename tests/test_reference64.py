@@ -144,7 +144,7 @@ def test_entry_points_refuse_a_bad_cache_before_any_launch(cache):
     a, b = ctypes.byref(p), ctypes.byref(c)
     f = V(FAKE)
     for fn, args in (
-            (L.moba_cache_write, (a, b, f, f, f, f, None)),
+            (L.moba_cache_write, (a, b, f, f, f, f, f, ctypes.c_size_t(1 << 40), None)),
             (L.moba_cache_read, (a, b, f, f, f, None)),
             (L.moba_decode_cache, (a, f, b, f, f, f, None, None, f, ctypes.c_size_t(1 << 40), None))):
         fn.argtypes, fn.restype = None, ctypes.c_int
@@ -158,9 +158,10 @@ def test_entry_points_refuse_bad_pointers_workspaces_and_variants():
     dec, bwd = L.moba_decode_cache, L.dense_causal_backward
     dec.argtypes = bwd.argtypes = None
     dec.restype = bwd.restype = ctypes.c_int
-    for size in (L.moba_decode_cache_workspace_size, L.dense_causal_backward_workspace_size):
+    for size in (L.moba_decode_cache_workspace_size, L.dense_causal_backward_workspace_size,
+                 L.moba_cache_write_workspace_size):
         size.argtypes, size.restype = None, ctypes.c_size_t
-        assert size(ctypes.byref(_params())) > 0
+        assert size(ctypes.byref(_params(total_tokens=1 << 16))) > 0
         assert size(ctypes.byref(_params(head_dim=96))) == 0
     a = ctypes.byref(_params())
     assert dec(a, odd, b, f, f, f, None, None, f, big, None) == moba.MOBA_ERR_INVALID_ARG
@@ -170,6 +171,11 @@ def test_entry_points_refuse_bad_pointers_workspaces_and_variants():
     for bad in (dict(own_block=1), dict(head_dim=96), dict(topk=33), dict(dtype=5)):
         assert dec(ctypes.byref(_params(**bad)), f, b, f, f, f, None, None, f, big,
                    None) == moba.MOBA_ERR_UNSUPPORTED
+    wr, many = L.moba_cache_write, ctypes.byref(_params(total_tokens=1 << 16, num_q_heads=2))
+    wr.argtypes, wr.restype = None, ctypes.c_int
+    assert wr(many, b, f, f, f, f, f, Z(1), None) == moba.MOBA_ERR_WORKSPACE
+    assert wr(many, b, f, f, f, f, None, big, None) == moba.MOBA_ERR_WORKSPACE
+    assert wr(many, b, f, odd, f, f, f, big, None) == moba.MOBA_ERR_INVALID_ARG
     ptrs = [f] * 10  # q k v cu out lse dout dq dk dv
     assert bwd(a, *ptrs, f, Z(1), None) == moba.MOBA_ERR_WORKSPACE
     assert bwd(ctypes.byref(_params(kv_layout=1)), *ptrs, f, big, None) == \
