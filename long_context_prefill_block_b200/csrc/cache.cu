@@ -22,6 +22,7 @@ namespace {
 constexpr int kThreads = 128;  // write and read: four warps that share nothing
 constexpr int kMeanThreads = 256;
 constexpr int kMaxCluster = 8;
+constexpr int kSMs = 148;  // of a B200: what the work of a warp is sized by
 
 // Exponent of a row whose largest magnitude has the fp32 bits `top` (finite).
 __device__ __forceinline__ int row_exponent(uint32_t top) {
@@ -151,12 +152,14 @@ __device__ __forceinline__ int token_row(const Dims& dm, const Cache& c,
 
 // Quantise and store: a row is held by LPR lanes of 16 bytes, which share its
 // maximum (as integers: an infinity or NaN is above every number). U rows' loads
-// a lane are in flight. Bound by HBM: d * sizeof(T) bytes in, d + 1 out; 262144
-// tokens of 8 heads, bf16, d = 128: 257 us, 6.2 TB/s. (A lane group a row of any
-// head, with a table look-up before each store and one-byte scale stores: 663.)
+// a lane are in flight. Bound by HBM: d * sizeof(T) bytes in, d + 1 out. (A lane
+// group a row of any head, with a table look-up before each store and one-byte
+// scale stores, took 663 us for 262144 tokens of 8 heads, bf16, d = 128.)
 //
 // sums: with 32 tokens a warp, also the sum of each warp's rows of K as stored,
-// [token / 32][head][d], which the block means are made of.
+// [token / 32][head][d], which the block means are made of. With them that call
+// takes 285 us (5.7 TB/s) and the integer pipe is two thirds busy; without, 257,
+// but the means then read all codes again: 325 in all, against 287.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 cache_write_kernel(Dims dm, Cache c, const T* __restrict__ k, const T* __restrict__ v,
@@ -253,7 +256,7 @@ cache_write_kernel(Dims dm, Cache c, const T* __restrict__ k, const T* __restric
 // left sums of 32 packed rows, those inside a part are added up (1/8 of the
 // codes' bytes); the other rows are read: LPR lanes of 16 bytes a row, fp32 sums
 // of every G-th row, then the lane groups' sums and the CTAs' sums in order.
-// Reading all 268 MB of codes again cost 67 us behind the 257 of the write.
+// 12 us for 64 blocks of 4096 and 8 heads.
 constexpr int kMeanPages = 2048 / 16 + 1;  // pages looked up at a time
 
 template <int D>
@@ -430,9 +433,10 @@ cache_read_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_rows, T* __re
   }
 }
 
-// Tokens a warp takes: 32, or 8 where that leaves SMs without work.
+// Tokens a warp takes: 32, or 8 where that leaves SMs with fewer than 16 warps
+// (64 tokens of 8 heads: 9.4 -> 6.8 us).
 int tokens_per_warp(const Dims& dm) {
-  return (int64_t)dm.T * dm.Hkv < (int64_t)32 * 16 * tc::sm_count() ? 8 : 32;
+  return (int64_t)dm.T * dm.Hkv < (int64_t)32 * 16 * kSMs ? 8 : 32;
 }
 dim3 warp_grid(const Dims& dm, int tpw) {
   const int64_t warps = (int64_t)((dm.T + tpw - 1) / tpw) * dm.Hkv;
@@ -475,7 +479,7 @@ cudaError_t launch_cache_write(const Dims& dm, const Cache& c, const void* k, co
 cudaError_t launch_cache_means(const Dims& dm, const Cache& c, const int32_t* cu_new,
                                const float* sums, float* kbar, int* status, cudaStream_t st) {
   const int64_t slots = (int64_t)dm.T / dm.B + dm.batch;
-  const int cs = dm.B >= 1024 && slots * dm.Hkv < 2 * tc::sm_count() ? 4 : 1;
+  const int cs = dm.B >= 1024 && slots * dm.Hkv < 2 * kSMs ? 4 : 1;
   if (slots * cs > INT32_MAX) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(slots * cs), (unsigned)dm.Hkv);
   const auto kernel = dm.d == 128 ? cache_means_kernel<128> : cache_means_kernel<64>;

@@ -270,6 +270,32 @@ def test_more_blocks_than_fit_shared_memory(dtype, shared):
     check_decode(q, pool, lens, nq, B, topk, shared, *got)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_pages_past_four_gigabytes(dtype):
+    """Rows whose byte offsets pass 2^31 and 2^32: the last pages of a 4.4 GB pool of K."""
+    pages, page, heads, d, B, L = 4200, 1024, 8, 128, 64, 300
+    c = moba.moba_cache_alloc(pages, page, heads, d)
+    pool = Pool([1], 16, 1, 64)
+    pool.cache, pool.table = c, i32([[pages - 1], [2049]])
+    g = torch.Generator().manual_seed(3)
+    k, v = ((torch.randn(2 * L, heads, d, generator=g) * 0.7).to(dtype).to(DEV) for _ in range(2))
+    kbar = torch.zeros(2, 5, heads, d, device=DEV)
+    moba.moba_cache_write(c, k, v, pool.table, i32([L, L]), offsets([L, L]), kbar, B)
+    a, b = moba.moba_cache_read(c, pool.table, i32([L, L]), offsets([L, L]), 2 * L, dtype=dtype)
+    for x, y in ((a, k), (b, v)):
+        code, e, _ = ref.quantise(y.cpu())
+        assert torch.equal(x.cpu(), (code * torch.exp2(e.double())[..., None]).to(dtype))
+    q = (torch.randn(2, 16, d, generator=g) * 0.7).to(dtype).to(DEV)
+    out, lse, idx = moba.moba_decode_cache(q, c, pool.table, i32([L, L]), offsets([1, 1]), kbar, B,
+                                           3, return_lse=True, return_idx=True)
+    assert moba.moba_device_status() == 0
+    for r in range(2):
+        keys, values = (x[r * L:(r + 1) * L].double().cpu() for x in (a, b))
+        o, l, i = ref.decode(q[r:r + 1].cpu(), keys, values, B, 3, False)
+        assert torch.equal(idx[r:r + 1].cpu().long(), i) and ref.off(out[r:r + 1], o) <= TOL[dtype]
+        assert (lse[r:r + 1].double().cpu() - l).abs().max() <= LSE_TOL
+
+
 def test_many_requests_with_one_token_each():
     """70 requests, some without a row, in one call, with padded rows behind: three rounds of the
     search for a row's request."""
