@@ -135,8 +135,8 @@ __device__ __forceinline__ void load_pages(const Step& a, int r, int g, int lo, 
 // its row itself (choose_blocks), which costs it less than the launch and the
 // wait for it would.
 constexpr int kGateThreads = 256;
-constexpr int kGateRows = 16;      // q rows of a group at a time
-constexpr int kGateBlocks = 1024;  // blocks whose scores fit: 64 KB
+constexpr int kGateRows = 16;       // q rows of a group at a time, at most
+constexpr int kGateScores = 49152;  // scores that fit: 192 KB, rows times blocks
 
 constexpr int kOwnGate = 64;
 
@@ -218,20 +218,19 @@ __device__ __forceinline__ void choose_blocks(const Step& a, const T* __restrict
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kGateThreads)
-cache_gate_kernel(const Step a, const T* __restrict__ q, const int cs) {
-  extern __shared__ __align__(16) float score[];  // [rows][c]
+cache_gate_kernel(const Step a, const T* __restrict__ q, const int cs, const int max_rows) {
+  extern __shared__ __align__(16) float score[];  // [rows][c], then flags [rows][c / 32]
   __shared__ __align__(16) float qs[kGateRows][D];
-  __shared__ uint32_t chosen[kGateRows][kGateBlocks / 32];
   tc::grid_let_next();
   const Dims& dm = a.dm;
-  const int grp = dm.Hq / dm.Hkv, chunks = dm.shared ? 1 : (grp + kGateRows - 1) / kGateRows;
+  const int grp = dm.Hq / dm.Hkv, chunks = dm.shared ? 1 : (grp + max_rows - 1) / max_rows;
   const int rank = blockIdx.x % cs, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int unit = blockIdx.x / cs;
-  const int h_first = unit % chunks * kGateRows;
+  const int h_first = unit % chunks * max_rows;
   unit /= chunks;
   const int g = unit % dm.Hkv, qi = unit / dm.Hkv;
   const int h0 = g * grp + h_first;
-  const int rows = dm.shared ? 1 : min(kGateRows, grp - h_first);
+  const int rows = dm.shared ? 1 : min(max_rows, grp - h_first);
   for (int e = tid; e < rows * D; e += kGateThreads) {
     const T* src = q + ((int64_t)qi * dm.Hq + h0 + e / D) * D + e % D;
     float s = to_f32(*src);
@@ -251,7 +250,7 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const int cs) {
   };
   if (need > 0) {
     sync();  // also: CTA 0 runs, so its shared memory can be written
-    constexpr int LPB = D / 4, BPW = 32 / LPB, U = 4;  // lanes a mean, means a warp, steps in flight
+    constexpr int LPB = D / 4, BPW = 32 / LPB, U = 8;  // lanes a mean, means a warp, steps in flight
     const int sub = lane % LPB, per = (c + cs - 1) / cs;
     const int first = rank * per, end = min(c, first + per), stride = kGateThreads / 32 * BPW;
     for (int i0 = first + warp * BPW + lane / LPB; __any_sync(0xffffffffu, i0 < end);
@@ -284,55 +283,71 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const int cs) {
   }
   sync();
   if (rank != 0) return;
+  const int words = (c + 31) / 32;
   for (int j = warp; j < rows; j += kGateThreads / 32) {
-    const int words = (c + 31) / 32;
-    chosen[j][lane] = 0;  // kGateBlocks / 32 words, one a lane
+    uint32_t* flags = reinterpret_cast<uint32_t*>(score + (int64_t)rows * c) + j * words;
+    for (int w = lane; w < words; w += 32) flags[w] = 0;
     __syncwarp();
     float* sc = score + j * c;
-    int n = 0;
-    for (int k = 0; k < need; ++k) {
-      float bs = -INFINITY;
-      int bi = INT_MAX;
-      for (int i = lane; i < c; i += 32) {
-        const float s = sc[i];
-        if (s > bs || (s == bs && i < bi)) {
-          bs = s;
-          bi = i;
-        }
+    // a lane keeps the best of its blocks, lane, lane + 32, ...; when it is
+    // taken the whole warp looks that lane's blocks through again
+    auto best = [&](float s, int i, float& bs, int& bi) {
+      if (s > bs || (s == bs && i < bi)) {
+        bs = s;
+        bi = i;
       }
+    };
+    auto over_lanes = [&](float& bs, int& bi) {
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        const float os = __shfl_xor_sync(0xffffffffu, bs, off);
-        const int oi = __shfl_xor_sync(0xffffffffu, bi, off);
-        if (os > bs || (os == bs && oi < bi)) {
-          bs = os;
-          bi = oi;
-        }
-      }
+      for (int off = 16; off > 0; off >>= 1)
+        best(__shfl_xor_sync(0xffffffffu, bs, off), __shfl_xor_sync(0xffffffffu, bi, off), bs, bi);
+    };
+    float ms = -INFINITY;
+    int mi = INT_MAX, n = 0;
+    if (need > 0)
+      for (int i = lane; i < c; i += 32) best(sc[i], i, ms, mi);
+    for (; n < need; ++n) {
+      float bs = ms;
+      int bi = mi;
+      over_lanes(bs, bi);
       if (bi == INT_MAX) break;  // only NaN scores are left
-      if (lane == bi % 32) {
+      const int owner = bi & 31;
+      if (lane == owner) {
         sc[bi] = NAN;
-        chosen[j][bi / 32] |= 1u << lane;
+        flags[bi / 32] |= 1u << owner;
       }
-      ++n;
       __syncwarp();
+      float ts = -INFINITY;
+      int ti = INT_MAX;
+      for (int i = owner + 32 * lane; i < c; i += 1024) best(sc[i], i, ts, ti);
+      over_lanes(ts, ti);
+      if (lane == owner) {
+        ms = ts;
+        mi = ti;
+      }
     }
-    // lane w holds the flags of blocks 32 w ..: write them in ascending order
-    uint32_t f = lane < words ? chosen[j][lane] : 0u;
-    int at = __popc(f);
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, at, off);
-      if (lane >= off) at += o;
-    }
-    at -= __popc(f);
+    __syncwarp();
     const int copies = dm.shared ? grp : 1;
-    for (int x = 0; x < copies; ++x) {
-      int32_t* row = a.idx + ((int64_t)qi * dm.Hq + h0 + (dm.shared ? x : j)) * dm.topk;
-      int o = at;
-      for (uint32_t m = f; m; m &= m - 1) row[o++] = lane * 32 + __ffs(m) - 1;
-      if (n + lane < dm.topk) row[n + lane] = lane == 0 ? c : -1;
+    int32_t* row = a.idx + ((int64_t)qi * dm.Hq + h0 + (dm.shared ? 0 : j)) * dm.topk;
+    int done = 0;  // ascending: 32 words of flags at a time, one a lane
+    for (int w0 = 0; w0 < words && n > 0; w0 += 32) {
+      const uint32_t f = w0 + lane < words ? flags[w0 + lane] : 0u;
+      int at = __popc(f);
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, at, off);
+        if (lane >= off) at += o;
+      }
+      const int total = __shfl_sync(0xffffffffu, at, 31);
+      for (int x = 0; x < copies; ++x) {
+        int o = done + at - __popc(f);
+        for (uint32_t m = f; m; m &= m - 1)
+          row[(int64_t)x * dm.topk + o++] = (w0 + lane) * 32 + __ffs(m) - 1;
+      }
+      done += total;
     }
+    for (int x = 0; x < copies; ++x)
+      if (n + lane < dm.topk) row[(int64_t)x * dm.topk + n + lane] = lane == 0 ? c : -1;
   }
 }
 
@@ -1033,27 +1048,29 @@ cache_merge_kernel(const Step a, T* __restrict__ out, float* __restrict__ lse_ou
 template <typename T, int D>
 cudaError_t run_gate(const Step& a, const void* q, cudaStream_t st) {
   const Dims& dm = a.dm;
-  const int grp = dm.Hq / dm.Hkv, rows = dm.shared ? 1 : grp < kGateRows ? grp : kGateRows;
-  const int chunks = dm.shared ? 1 : (grp + kGateRows - 1) / kGateRows;
-  // CTAs a cluster: 16 to 32 blocks each, up to four a warp; one CTA to 64 blocks
+  const int grp = dm.Hq / dm.Hkv;
+  int rows = dm.shared ? 1 : grp < kGateRows ? grp : kGateRows;
+  if (rows > kGateScores / dm.nb) rows = kGateScores / dm.nb;
+  const int chunks = dm.shared ? 1 : (grp + rows - 1) / rows;
+  // CTAs a cluster: 16 to 32 blocks each and more, up to four a warp; one CTA to 64 blocks
   const int cs = dm.nb > 128 ? 8 : dm.nb > 64 ? 4 : 1;
   const int64_t grid = (int64_t)dm.T * dm.Hkv * chunks * cs;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  const size_t smem = sizeof(float) * rows * (size_t)dm.nb;
+  const size_t smem = sizeof(float) * rows * ((size_t)dm.nb + (dm.nb + 31) / 32);
   cudaError_t e;
   static std::atomic<bool> ready[tc::kMaxDevices];
-  if ((e = tc::allow_smem(cache_gate_kernel<T, D>, (int)sizeof(float) * kGateRows * kGateBlocks,
-                          ready)))
+  if ((e = tc::allow_smem(cache_gate_kernel<T, D>,
+                          (int)sizeof(float) * (kGateScores + kGateScores / 32 + kGateRows), ready)))
     return e;
   return tc::launch_cluster(cache_gate_kernel<T, D>, dim3((unsigned)grid), kGateThreads, smem, st, cs,
-                            a, static_cast<const T*>(q), cs);
+                            a, static_cast<const T*>(q), cs, rows);
 }
 
 template <typename T, int D>
 cudaError_t run(const Step& a, const void* q, void* out, float* lse, cudaStream_t st) {
   const Dims& dm = a.dm;
   cudaError_t e = cudaSuccess;
-  if (a.gated && dm.nb <= kGateBlocks)
+  if (a.gated && dm.nb <= kGateScores)
     e = run_gate<T, D>(a, q, st);
   else if (a.gated)  // lists in registers instead of all scores in shared memory
     e = launch_cache_gate(dm, q, a.kbar, a.c.lens, a.cu_q, a.idx, a.max_len, a.status, st);
@@ -1103,7 +1120,7 @@ cudaError_t launch_decode_cache(const Dims& dm, const Cache& c, const void* q, c
   a.cu_q = cu_q;
   a.kbar = kbar;
   a.idx = idx;
-  a.gated = dm.nb > kOwnGate;
+  a.gated = dm.nb > kOwnGate && dm.topk > 1;
   a.part_o = part_o;
   a.part_lse = part_lse;
   a.max_len = held < dm.max_seqlen ? (int)held : dm.max_seqlen;

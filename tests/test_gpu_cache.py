@@ -259,11 +259,15 @@ def test_decode_matches_the_definition(lens, nq, Hq, Hkv, d, page, B, topk, dtyp
 
 
 @pytest.mark.parametrize("dtype,shared", [(torch.bfloat16, False), (torch.float32, True)])
-def test_more_blocks_than_fit_shared_memory(dtype, shared):
-    """1100 blocks of 16 keys: the gate that keeps lists instead of all scores."""
-    lens, nq, B, topk = [17600, 200], [1, 2], 16, 6
+@pytest.mark.parametrize("lens,B,topk,Hq", [
+    ([17600, 200], 16, 6, 2), ([5000, 4097], 1, 32, 18), ([49300, 50], 1, 3, 2),
+    ([3000, 90], 20, 1, 4)])
+def test_many_blocks(lens, B, topk, Hq, dtype, shared):
+    """1100 and 5000 blocks, scores of all in shared memory (a part of the heads at a time); 49300,
+    lists in registers instead; 150 with nothing to choose."""
+    nq = [1, 2]
     pool, kbar = filled(lens, 1, 64, 64, B, seed=31)
-    q = (torch.randn(3, 2, 64, generator=torch.Generator().manual_seed(4)) * 0.7).to(dtype).to(DEV)
+    q = (torch.randn(3, Hq, 64, generator=torch.Generator().manual_seed(4)) * 0.7).to(dtype).to(DEV)
     got = moba.moba_decode_cache(q, pool.cache, pool.table, i32(lens), offsets(nq), kbar, B, topk,
                                  shared_routing=shared, return_lse=True, return_idx=True)
     assert moba.moba_device_status() == 0
