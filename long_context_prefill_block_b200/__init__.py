@@ -148,6 +148,7 @@ _SIGNATURES = {
     "moba_decode_cache_workspace_size": [_PARAMS],
     "moba_cache_write_workspace_size": [_PARAMS],
 }
+_CODE, _SCALE = torch.float8_e4m3fn, torch.float8_e8m0fnu  # of a cache's k, v and their scales
 _bound = {}  # entry points with their signatures set, by name
 
 
@@ -192,31 +193,33 @@ def _dev_i32(cu: torch.Tensor, device) -> torch.Tensor:
 
 
 def _check_inputs(*ts):
-    ts = [t for t in ts if t is not None]
+    devices = set()
     for t in ts:
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError("tensors must be contiguous CUDA tensors")
-    first = ts[0].get_device() if ts else 0
-    if any(t.get_device() != first for t in ts):
-        raise ValueError(f"tensors on different devices: {sorted({str(t.device) for t in ts})}")
+        if t is not None:
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("tensors must be contiguous CUDA tensors")
+            devices.add(t.get_device())
+    if len(devices) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(f'cuda:{i}' for i in devices)}")
 
 
 def _check_qkv(q, k, v=None, out=None):
     """Shapes and element types the C ABI takes on trust: a mismatch would make the
     kernels read or write past the end of a buffer, so it is refused here."""
-    if q.dim() != 3 or k.dim() != 3:
+    qs, ks, dtype = q.shape, k.shape, q.dtype
+    if len(qs) != 3 or len(ks) != 3:
         raise ValueError("q and k must be [tokens, heads, head_dim]")
-    if k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+    if k.dtype != dtype or (v is not None and v.dtype != dtype):
         raise TypeError(f"q, k, v must share one dtype (got {q.dtype}, {k.dtype}"
                         f"{'' if v is None else ', ' + str(v.dtype)})")
-    if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
-        raise ValueError(f"k {tuple(k.shape)} does not match q {tuple(q.shape)}")
-    if q.shape[1] % k.shape[1] != 0:
-        raise ValueError(f"{q.shape[1]} q heads are not a multiple of {k.shape[1]} kv heads")
-    if v is not None and v.shape != k.shape:
-        raise ValueError(f"v {tuple(v.shape)} does not match k {tuple(k.shape)}")
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype):
-        raise ValueError(f"out must be {tuple(q.shape)} {q.dtype}")
+    if ks[0] != qs[0] or ks[2] != qs[2]:
+        raise ValueError(f"k {tuple(ks)} does not match q {tuple(qs)}")
+    if qs[1] % ks[1] != 0:
+        raise ValueError(f"{qs[1]} q heads are not a multiple of {ks[1]} kv heads")
+    if v is not None and v.shape != ks:
+        raise ValueError(f"v {tuple(v.shape)} does not match k {tuple(ks)}")
+    if out is not None and (out.shape != qs or out.dtype != dtype):
+        raise ValueError(f"out must be {tuple(qs)} {dtype}")
 
 
 def _check_cu(cu_seqlens: torch.Tensor, total_tokens: int) -> None:
@@ -538,28 +541,29 @@ def _check_cache(cache, heads: int, head_dim: int, page_table, seqlens, cu, *oth
     """Shapes, types and devices of a call on a cache (`others` share its device); returns its C
     description."""
     k, v, ks, vs = cache
-    shape = k.shape
+    shape, table = k.shape, page_table.shape
     if len(shape) != 4 or shape[1] != heads or shape[3] != head_dim or v.shape != shape:
         raise ValueError(f"cache codes {tuple(shape)}, {tuple(v.shape)} must be "
                          f"[pages, {heads}, page_size, {head_dim}]")
-    if k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
+    if k.dtype != _CODE or v.dtype != _CODE:
         raise TypeError("cache codes must be float8_e4m3fn")
-    if ks.shape != shape[:3] or vs.shape != shape[:3]:
-        raise ValueError(f"cache scales must be {tuple(shape[:3])}")
-    if ks.dtype != torch.float8_e8m0fnu or vs.dtype != torch.float8_e8m0fnu:
+    pages, page, rows = shape[0], shape[2], shape[:3]
+    if ks.shape != rows or vs.shape != rows:
+        raise ValueError(f"cache scales must be {tuple(rows)}")
+    if ks.dtype != _SCALE or vs.dtype != _SCALE:
         raise TypeError("cache scales must be float8_e8m0fnu")
-    page = shape[2]
     if page < 16 or page > 65536 or page & (page - 1):
         raise ValueError(f"page_size must be a power of two from 16 to 65536 (got {page})")
-    if page_table.dim() != 2 or page_table.dtype != torch.int32:
+    i32 = torch.int32
+    if len(table) != 2 or page_table.dtype != i32:
         raise ValueError("page_table must be int32 [batch, max_pages]")
-    batch, max_pages = page_table.shape
-    if seqlens.shape != (batch,) or seqlens.dtype != torch.int32:
+    batch, max_pages = table
+    if seqlens.shape != (batch,) or seqlens.dtype != i32:
         raise ValueError(f"seqlens must be int32 [{batch}]")
-    if cu.shape != (batch + 1,) or cu.dtype != torch.int32:
+    if cu.shape != (batch + 1,) or cu.dtype != i32:
         raise ValueError(f"row offsets must be int32 [{batch + 1}]")
     _check_inputs(k, v, ks, vs, page_table, seqlens, cu, *others)
-    return _CacheStruct(shape[0], page, max_pages, k.data_ptr(), v.data_ptr(), ks.data_ptr(),
+    return _CacheStruct(pages, page, max_pages, k.data_ptr(), v.data_ptr(), ks.data_ptr(),
                         vs.data_ptr(), page_table.data_ptr(), seqlens.data_ptr())
 
 
@@ -574,12 +578,13 @@ def _cache_params(batch, rows, hq, hkv, d, dtype, block_size, topk, max_seqlen,
 
 def _check_kbar(kbar, batch: int, heads: int, head_dim: int, block_size: int) -> int:
     """Checks the block means of a cache; returns the longest length they have blocks for."""
-    if kbar.dim() != 4 or kbar.shape[0] != batch or kbar.shape[2:] != (heads, head_dim) or \
+    shape = kbar.shape
+    if len(shape) != 4 or shape[0] != batch or shape[2] != heads or shape[3] != head_dim or \
             kbar.dtype != torch.float32:
         raise ValueError(f"kbar must be float32 [{batch}, num_blocks, {heads}, {head_dim}]")
     if block_size < 1:
         raise ValueError("block_size must be at least 1")
-    return min(kbar.shape[1] * block_size, 2**31 - 1)
+    return min(shape[1] * block_size, 2**31 - 1)
 
 
 def moba_cache_write(cache: MobaCache, k, v, page_table, seqlens, cu_new,
