@@ -10,8 +10,10 @@
 //                      into each warp's own ring, products on the tensor core
 //   cache_attn_kernel  fp32 queries: the same split, fp32 FMA
 //
-// Bound by the bytes of the chosen rows: 2 (d + 1) a key. The last split of a
-// row to finish merges the row's partials (no CTA waits for another).
+//   cache_merge_kernel joins the splits' partials of each row, where it has more
+//                      than one
+//
+// Bound by the bytes of the chosen rows: 2 (d + 1) a key.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 

@@ -5,8 +5,9 @@
         --block-size 512 --call gate
 
 Draws the workload's inputs on cuda:0, then makes --iters calls of one entry
-point through the public binding (forward, gate, backward or decode) and
-prints the mean time per call (CUDA events) and the device status word. The
+point through the public binding (forward, gate, backward, decode, the dense
+forward and its gradient, or the write, read and decode of an 8-bit cache that
+holds the workload's K and V in pages in random order) and prints the mean time per call (CUDA events) and the device status word. The
 shape options override the named workload, so that a profiler can capture a
 kernel on a case a few GB in size that keeps the per-row work of the full
 workload (e.g. the million-token gate's 256 blocks at 131,072 tokens with
@@ -49,7 +50,10 @@ def main():
     ap.add_argument("--tokens", type=int, default=None, help="one sequence of this length")
     ap.add_argument("--block-size", type=int, default=None)
     ap.add_argument("--topk", type=int, default=None)
-    ap.add_argument("--call", default="forward", choices=["forward", "gate", "backward", "decode"])
+    ap.add_argument("--call", default="forward", choices=["forward", "gate", "backward", "decode", "dense", "dense_backward",
+                             "cache_write", "cache_read", "cache_decode"])
+    ap.add_argument("--queries", type=int, default=1, help="cache_decode: queries per request")
+    ap.add_argument("--page-size", type=int, default=64, help="of the 8-bit cache")
     ap.add_argument("--iters", type=int, default=2)
     args = ap.parse_args()
     w = workload(args.workload, args.tokens, args.block_size, args.topk)
@@ -68,6 +72,37 @@ def main():
                            device=dev, dtype=torch.float32).to(out.dtype)
         call = lambda: moba.moba_backward(q, k, v, cu_d, out, lse, dout, B, K, idx=idx,
                                           max_seqlen=S)
+    elif args.call == "dense":
+        call = lambda: moba.dense_causal_forward(q, k, v, cu_d, max_seqlen=S)
+    elif args.call == "dense_backward":
+        out, lse = moba.dense_causal_forward(q, k, v, cu_d, max_seqlen=S, return_lse=True)
+        dout = torch.randn(out.shape, generator=torch.Generator(device=dev).manual_seed(5),
+                           device=dev, dtype=torch.float32).to(out.dtype)
+        call = lambda: moba.dense_causal_backward(q, k, v, cu_d, out, lse, dout, max_seqlen=S)
+    elif args.call.startswith("cache_"):
+        lens, page = cu_d.diff(), args.page_size
+        per = -(-w.max_seqlen // page)
+        table = torch.randperm(per * w.batch, device=dev,
+                               generator=torch.Generator(device=dev).manual_seed(7))
+        table = table.to(torch.int32).view(w.batch, per)
+        cache = moba.moba_cache_alloc(per * w.batch, page, k.shape[1], k.shape[2], dev)
+        kbar = torch.zeros((w.batch, -(-w.max_seqlen // B), *k.shape[1:]), device=dev)
+        write = lambda: moba.moba_cache_write(cache, k, v, table, lens, cu_d, kbar, B)
+        if args.call == "cache_write":
+            call = write
+        elif args.call == "cache_read":
+            write()
+            kr, vr = torch.empty_like(k), torch.empty_like(v)
+            call = lambda: moba.moba_cache_read(cache, table, lens, cu_d, k.shape[0], k.dtype,
+                                                kr, vr)
+        else:
+            write()
+            n = args.queries
+            cu_q = torch.arange(w.batch + 1, dtype=torch.int32, device=dev) * n
+            rows = (cu_d[1:, None].long() - n + torch.arange(n, device=dev)).flatten()
+            qd = q[rows].contiguous()
+            call = lambda: moba.moba_decode_cache(qd, cache, table, lens, cu_q, kbar, B, K,
+                                                  max_seqlen=S)
     else:
         # one query per request: the last position of each sequence
         last = (cu_d[1:] - 1).long()
