@@ -249,10 +249,40 @@ cache_write_kernel(Dims dm, Cache c, const T* __restrict__ k, const T* __restric
   }
 }
 
+// Which block a slot stands for. Request r's completed blocks have slots from
+// cu_new[r] / B + r on (n / B + 1 of them at most). Called by whole warps.
+struct Slot {
+  int r, blk;       // blk: -1 for none
+  int begin, row0;  // position and packed row of the request's first new row
+};
+__device__ __forceinline__ Slot find_slot(const Dims& dm, const Cache& c,
+                                          const int32_t* __restrict__ cu_new, int slot) {
+  const int B = dm.B;
+  Slot s{0, -1, 0, 0};
+  int r = 0;  // the largest with cu_new[r] / B + r <= slot, 32 requests a round
+  for (int n = dm.batch + 1; n > 1;) {
+    const int lane = threadIdx.x & 31, step = (n + 31) / 32, at = r + lane * step;
+    const uint32_t le =
+        __ballot_sync(0xffffffffu, lane * step < n && cu_new[at] / B + at <= slot);
+    const int k = le ? 31 - __clz(le) : 0;
+    n = min(step, n - k * step);
+    r += k * step;
+  }
+  if (r < dm.batch) {
+    const int n = cu_new[r + 1] - cu_new[r], len = c.lens[r];
+    if (n > 0 && len >= n && len <= max_positions(dm, c)) {
+      s.begin = len - n;
+      s.row0 = cu_new[r];
+      s.blk = s.begin / B + slot - (s.row0 / B + r);
+      if (s.blk >= len / B || s.blk >= dm.nb) s.blk = -1;
+    }
+  }
+  s.r = r;
+  return s;
+}
+
 // Mean of each block that the new rows complete, over the rows as the cache
-// holds them. Slot j of the grid: request r's completed blocks have slots
-// from cu_new[r] / B + r on (n / B + 1 of them at most). One cluster per
-// (slot, kv head), its CTAs taking equal parts of the block. Where the write
+// holds them. One cluster per (slot, kv head), its CTAs taking equal parts of the block. Where the write
 // left sums of 32 packed rows, those inside a part are added up (1/8 of the
 // codes' bytes); the other rows are read: LPR lanes of 16 bytes a row, fp32 sums
 // of every G-th row, then the lane groups' sums and the CTAs' sums in order.
@@ -268,29 +298,11 @@ cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
   __shared__ float sum[G + GS][D + 4];
   __shared__ float part[kMaxCluster][D];
   __shared__ int page_row[kMeanPages];
-  const int g = blockIdx.y, B = dm.B, slot = blockIdx.x / cs, rank = blockIdx.x % cs;
-  int r = 0;  // the largest with cu_new[r] / B + r <= slot, 32 requests a round
-  for (int n = dm.batch + 1; n > 1;) {
-    const int lane = threadIdx.x & 31, step = (n + 31) / 32, at = r + lane * step;
-    const uint32_t le =
-        __ballot_sync(0xffffffffu, lane * step < n && cu_new[at] / B + at <= slot);
-    const int k = le ? 31 - __clz(le) : 0;
-    n = min(step, n - k * step);
-    r += k * step;
-  }
-  // every early return below is the whole cluster's
-  int blk = -1, begin = 0, row0 = 0;  // begin, row0: position and packed row of the first new row
-  if (r < dm.batch) {
-    const int n = cu_new[r + 1] - cu_new[r], len = c.lens[r];
-    if (n > 0 && len >= n && len <= max_positions(dm, c)) {
-      begin = len - n;
-      row0 = cu_new[r];
-      blk = begin / B + slot - (row0 / B + r);
-      if (blk >= len / B || blk >= dm.nb) blk = -1;
-    }
-  }
+  const int g = blockIdx.y, B = dm.B, rank = blockIdx.x % cs;
+  const Slot at = find_slot(dm, c, cu_new, blockIdx.x / cs);
+  const int r = at.r, blk = at.blk, begin = at.begin, row0 = at.row0;
   tc::grid_wait();  // the rows
-  if (blk < 0) return;
+  if (blk < 0) return;  // the whole cluster
   const int per = (B + cs - 1) / cs, first = blk * B + min(rank * per, B);
   const int last = blk * B + min(rank * per + per, B);
   const int sub = threadIdx.x % LPR, grp = threadIdx.x / LPR, mask = (1 << c.page_log2) - 1;
@@ -373,6 +385,110 @@ cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
     float t = 0.f;
     for (int i = 0; i < cs; ++i) t += part[i][x];
     kbar[(((int64_t)r * dm.nb + blk) * dm.Hkv + g) * D + x] = t / (float)B;
+  }
+}
+
+// The same for blocks of up to kSmallBlock rows, one warp per (slot, kv head):
+// their work is too little for a CTA's start and its two barriers. Write and
+// means of 262144 rows of 8 heads in blocks of 64: 487 us with a CTA, 308 with a
+// warp; 8192 rows after 1000 old ones in each of 4 requests: 91, 49. A warp is the
+// slower one where a few requests each end one block of old rows: 8 requests of
+// 200 rows, blocks of 128: 11 us with a CTA, 13 with a warp.
+constexpr int kSmallBlock = 256;
+constexpr int kSmallWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kSmallWarps * 32)
+cache_small_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
+                         const float* __restrict__ sums, float* __restrict__ kbar, int* status) {
+  constexpr int LPR = D / 16, G = 32 / LPR, U = 4;  // lanes of a row of codes, rows a load
+  constexpr int LPS = D / 4, GS = 32 / LPS;         // the same for sums
+  const int lane = threadIdx.x & 31, B = dm.B;
+  const int64_t w = (int64_t)blockIdx.x * kSmallWarps + (threadIdx.x >> 5);
+  const int64_t slot = w / dm.Hkv;
+  const int g = (int)(w % dm.Hkv);
+  Slot at{0, -1, 0, 0};
+  if (slot < (int64_t)dm.T / B + dm.batch) at = find_slot(dm, c, cu_new, (int)slot);
+  const int blk = at.blk, first = blk * B, last = first + B;
+  // the block's pages, at most 17: lane x looks page x up
+  int pages = -1;
+  const int p0 = first >> c.page_log2;
+  if (blk >= 0 && lane <= ((last - 1) >> c.page_log2) - p0) {
+    const int64_t row =
+        cache_page_row(c, dm.Hkv, c.table[(int64_t)at.r * c.max_pages + p0 + lane], g);
+    pages = (int)row;
+    if (row < 0) set_status(status, kStBadIndices);
+  }
+  tc::grid_wait();  // the rows
+  if (blk < 0) return;
+  // groups of 32 packed rows inside the block: [g0, g1); rows outside them are read
+  int g0 = 0, g1 = 0, lo = last, hi = last;
+  if (sums && last > at.begin) {
+    g0 = (at.row0 + max(first, at.begin) - at.begin + 31) / 32;
+    g1 = (at.row0 + last - at.begin) / 32;
+    if (g1 > g0) {
+      lo = at.begin + g0 * 32 - at.row0;
+      hi = at.begin + g1 * 32 - at.row0;
+    }
+  }
+  float t[4] = {0.f, 0.f, 0.f, 0.f};  // dims ss * 4 .. + 3
+  const int ss = lane % LPS, sg = lane / LPS;
+#pragma unroll 4
+  for (int i = g0 + sg; i < g1; i += GS) {
+    const float4 v =
+        __ldg(reinterpret_cast<const float4*>(sums + ((int64_t)i * dm.Hkv + g) * D) + ss);
+    t[0] += v.x;
+    t[1] += v.y;
+    t[2] += v.z;
+    t[3] += v.w;
+  }
+  if (GS == 2) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] += __shfl_xor_sync(0xffffffffu, t[e], 16);
+  }
+  const int rest = lo - first + last - hi;  // row x of them: first + x, or hi + x - (lo - first)
+  if (rest > 0) {
+    const int sub = lane % LPR, grp = lane / LPR, mask = (1 << c.page_log2) - 1;
+    float acc[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    for (int x0 = 0; x0 < rest; x0 += G * U) {
+      uint4 q[U];
+      float s[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int x = x0 + u * G + grp;
+        const int j = x < lo - first ? first + x : hi + x - (lo - first);
+        const int pr = __shfl_sync(0xffffffffu, pages, ((j >> c.page_log2) - p0) & 31);
+        q[u] = make_uint4(0, 0, 0, 0);
+        s[u] = 0.f;
+        if (x < rest && pr >= 0) {
+          const int64_t row = pr + (j & mask);
+          q[u] = *reinterpret_cast<const uint4*>(c.k + row * D + sub * 16);
+          s[u] = e8m0_value(c.ks[row]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float y[16];
+        decode16(q[u], y);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] = fmaf(y[e], s[u], acc[e]);
+      }
+    }
+    // lane l has the dims 16 (l % LPR) .. of every G-th row, and wants 4 (l % LPS) ..
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+#pragma unroll
+      for (int off = LPR; off < 32; off *= 2) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], off);
+      const float v = __shfl_sync(0xffffffffu, acc[e], ss / 4);
+      if (ss % 4 == e / 4) t[e % 4] += v;
+    }
+  }
+  if (sg == 0) {
+    float* o = kbar + (((int64_t)at.r * dm.nb + blk) * dm.Hkv + g) * D + ss * 4;
+    const float n = (float)B;
+    *reinterpret_cast<float4*>(o) = make_float4(t[0] / n, t[1] / n, t[2] / n, t[3] / n);
   }
 }
 
@@ -488,6 +604,13 @@ cudaError_t launch_cache_means(const Dims& dm, const Cache& c, const int32_t* cu
   const int64_t slots = (int64_t)dm.T / dm.B + dm.batch;
   const int cs = dm.B >= 1024 && slots * dm.Hkv < 2 * kSMs ? 4 : 1;
   if (slots * cs > INT32_MAX) return cudaErrorInvalidValue;
+  if (dm.B <= kSmallBlock) {
+    const int64_t x = (slots * dm.Hkv + kSmallWarps - 1) / kSmallWarps;
+    if (x > INT32_MAX) return cudaErrorInvalidValue;
+    const auto kernel = dm.d == 128 ? cache_small_means_kernel<128> : cache_small_means_kernel<64>;
+    return tc::launch_beside(kernel, dim3((unsigned)x), kSmallWarps * 32, 0, st, 1, dm, c, cu_new, sums,
+                             kbar, status);
+  }
   const dim3 grid((unsigned)(slots * cs), (unsigned)dm.Hkv);
   const auto kernel = dm.d == 128 ? cache_means_kernel<128> : cache_means_kernel<64>;
   return tc::launch_beside(kernel, grid, kMeanThreads, 0, st, cs, dm, c, cu_new, sums, kbar, cs, status);

@@ -137,6 +137,14 @@ def test_means_of_long_appends(dtype, d, B):
                 assert (got == 7.0).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B", [4, 33, 100, 256, 257])
+def test_means_of_small_blocks(d, B):
+    """Blocks that one warp sums: none, one or several groups of 32 inside, pages that end in them
+    (the last size is past what a warp takes)."""
+    test_means_of_long_appends(torch.bfloat16, d, B)
+
+
 def test_rows_at_the_ends_of_the_number_range():
     """Largest, smallest, subnormal, infinite and NaN rows; reading back stays finite where the
     input was, and NaN rows read back as NaN."""
