@@ -606,7 +606,7 @@ moba_status dense_causal_backward(const moba_params* p, const void* q, const voi
   int* status = status_word();
   if (!status) return MOBA_ERR_CUDA;
   float* stat = static_cast<float*>(ws);
-  MOBA_TRY(launch_dense_bwd_stat(dm, out, dout, lse, cu_seqlens, stat, dq, dk, dv, st));
+  MOBA_TRY(launch_dense_bwd_stat(dm, out, dout, lse, cu_seqlens, stat, dq, dk, dv, status, st));
   const auto launch = dm.dtype == kBF16 ? launch_dense_bwd_tc : launch_dense_bwd_simt;
   return cuda_status(launch(dm, q, k, v, dout, stat, cu_seqlens, dq, dk, dv, status, st));
 }

@@ -163,6 +163,67 @@ __device__ __forceinline__ int find_request_warp(const int32_t* __restrict__ cu,
   return lo;
 }
 
+// Place x of a launch over the tiles (of ROWS rows) of every sequence, for each
+// of `heads` heads: tile_slots() x heads places. Every sequence has `slots` of
+// them a head, at least as many as tiles, and takes rest in [0, slots * heads).
+// By whole warps. slots == 0: no such place, or a sequence whose length is not in
+// [0, max_seqlen] (which is for the caller to report).
+//
+// Lengths that are about even: each sequence has as many slots as the longest one
+// may have tiles, and the place follows from x. Else, when those would be over
+// twice the tiles that there can be, sequence b has the slots from cu[b] / ROWS + b
+// on, which costs a search (one round of loads for up to 31 sequences): the
+// gradient of 692 + 88 + 6 + 10 + 40 tokens, 24 on 8 heads, 68 -> 58 us without the
+// empty CTAs, that of 4 x 8192 tokens, 16 heads, 3.64 -> 3.70 ms with the search.
+struct TilePlace {
+  int start, len, slots, rest;
+};
+template <int ROWS>
+__host__ __device__ inline bool even_lengths(const Dims& dm) {
+  return (int64_t)((dm.max_seqlen + ROWS - 1) / ROWS) * dm.batch <=
+         2 * ((int64_t)(dm.T / ROWS) + dm.batch);
+}
+template <int ROWS>
+__host__ __device__ inline int64_t tile_slots(const Dims& dm) {
+  return even_lengths<ROWS>(dm) ? (int64_t)((dm.max_seqlen + ROWS - 1) / ROWS) * dm.batch
+                                : (int64_t)(dm.T / ROWS) + dm.batch;
+}
+// TILE_MAJOR: with even lengths tile 0 of every sequence comes first, then tile
+// 1; else one sequence after the other.
+template <int ROWS, bool TILE_MAJOR>
+__device__ __forceinline__ TilePlace find_tile(const Dims& dm, const int32_t* __restrict__ cu,
+                                               int heads, int x) {
+  int b, slots, rest;
+  if (even_lengths<ROWS>(dm)) {
+    slots = (dm.max_seqlen + ROWS - 1) / ROWS;
+    if (TILE_MAJOR) {
+      b = x / heads % dm.batch;
+      rest = x / heads / dm.batch * heads + x % heads;
+    } else {
+      b = x / (slots * heads);
+      rest = x % (slots * heads);
+    }
+  } else {
+    const int lane = threadIdx.x & 31, slot = x / heads;
+    b = 0;  // the largest with cu[b] / ROWS + b <= slot
+    for (int n = dm.batch + 1; n > 1;) {
+      const int step = (n + 31) / 32, at = b + lane * step;
+      const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && cu[at] / ROWS + at <= slot);
+      const int k = le ? 31 - __clz(le) : 0;
+      n = min(step, n - k * step);
+      b += k * step;
+    }
+    if (b >= dm.batch) return {0, 0, 0, 0};
+    const int base = cu[b] / ROWS + b;
+    slots = cu[b + 1] / ROWS + b + 1 - base;
+    rest = x - base * heads;
+    if (rest < 0 || rest >= slots * heads) return {0, 0, 0, 0};  // offsets that fall
+  }
+  const int start = cu[b], len = cu[b + 1] - start;
+  if (len < 0 || len > dm.max_seqlen) return {0, 0, 0, 0};
+  return {start, len, slots, rest};
+}
+
 // Request r and cache position of row i of a call on a paged cache: request
 // r's rows cu[r] .. cu[r+1]-1 stand at the last positions of its seqlens[r].
 // False for a row that no request owns (a padded batch), and, with a status
@@ -331,7 +392,30 @@ constexpr int kSimtTileM = 32;
 // that no sequence owns; the gradients have the inputs' type.
 cudaError_t launch_dense_bwd_stat(const Dims& dm, const void* out, const void* dout,
                                   const float* lse, const int32_t* cu, float* stat, void* dq,
-                                  void* dk, void* dv, cudaStream_t st);
+                                  void* dk, void* dv, int* status, cudaStream_t st);
+// CTAs that share a tile (a power of two up to `most`) of the gradient's passes,
+// of `at_once` that run together: what takes least by a rough account in items
+// (a tile of queries against a tile of keys), the longest tile's share or the
+// mean of all, and `start` items for each round of CTAs. The number of CTAs sets
+// the order of the sums, so T counts as the next power of two: a batch's padding
+// seldom changes its bits.
+template <int ROWS>
+inline int cluster_for(Dims dm, int64_t at_once, int most, int start) {
+  int T = 1;
+  while (T < dm.T && T < 1 << 30) T *= 2;
+  dm.T = T;
+  const int64_t tiles = (dm.max_seqlen + ROWS - 1) / ROWS, longest = tiles * (dm.Hq / dm.Hkv);
+  const int64_t clusters = tile_slots<ROWS>(dm) * (dm.Hq + dm.Hkv);
+  const int64_t all = (int64_t)(dm.T / ROWS + 1) * dm.Hq * (tiles + 1);  // sequences of max_seqlen
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int cs = 1; cs <= most; cs *= 2) {
+    const int64_t share = (longest + cs - 1) / cs, mean = all / at_once;
+    const int64_t t = (share > mean ? share : mean) + start * ((clusters * cs + at_once - 1) / at_once);
+    if (t < least) least = t, best = cs;
+  }
+  return best;
+}
 // bf16 inputs (dense_bwd_tc.cu), then fp32 inputs.
 cudaError_t launch_dense_bwd_tc(const Dims& dm, const void* q, const void* k, const void* v,
                                 const void* dout, const float* stat, const int32_t* cu, void* dq,

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads)
 dense_bwd_stat_kernel(Dims dm, const T* __restrict__ out, const T* __restrict__ dout,
                       const float* __restrict__ lse, const int32_t* __restrict__ cu,
                       float* __restrict__ stat, T* __restrict__ dq, T* __restrict__ dk,
-                      T* __restrict__ dv) {
+                      T* __restrict__ dv, int* status) {
   constexpr int VEC = Vec16<T>::N, LPR = D / VEC, RPS = kThreads / LPR;  // rows per step
   __shared__ float ds[32];
   __shared__ bool owned[32];
@@ -44,6 +44,11 @@ dense_bwd_stat_kernel(Dims dm, const T* __restrict__ out, const T* __restrict__ 
   // read the statistics
   tc::grid_let_next();
   const int h = blockIdx.y, t0 = blockIdx.x * 32;
+  if (h == 0 && t0 == 0) {  // every sequence, those that get no tile too
+    int64_t start;
+    int len;
+    for (int b = threadIdx.x; b < dm.batch; b += kThreads) seq_bounds(dm, cu, b, start, len, status);
+  }
   const int sub = threadIdx.x % LPR, rr = threadIdx.x / LPR;
   for (int r = rr; r < 32; r += RPS) {
     const int t = t0 + r;
@@ -99,15 +104,6 @@ struct Args {
   int* status;
   int cs;  // CTAs a cluster
 };
-
-// Place x of tiles x batch x heads, tile-major: the tiles with the most work
-// come first when the tile index grows with falling work.
-struct Place {
-  int tile, b, h;
-};
-__device__ __forceinline__ Place place(int x, int batch, int heads) {
-  return {x / (batch * heads), x / heads % batch, x % heads};
-}
 
 // 64 rows of one head (row stride in elements) into shared memory, rows at
 // or past n as zeros.
@@ -257,13 +253,12 @@ __device__ __forceinline__ void store_rows(const float (&acc)[4][D / 16], float 
 template <int D>
 __device__ __forceinline__ void kv_pass(const Args& a, Smem<D>& sm, int x, int rank) {
   const Dims& dm = a.dm;
-  const Place pl = place(x, dm.batch, dm.Hkv);
-  const int g = pl.h, b = pl.b;
-  int64_t start;
-  int len;
-  if (!seq_bounds(dm, a.cu, b, start, len, a.status) || !MOBA_CHECK(start + len <= dm.T, a.status))
-    return;
-  const int k0 = pl.tile * BK;
+  const TilePlace at = find_tile<BK, true>(dm, a.cu, dm.Hkv, x);
+  if (at.slots == 0) return;
+  const int64_t start = at.start;
+  const int len = at.len, g = at.rest % dm.Hkv;  // the longest tiles of a sequence first
+  if (!MOBA_CHECK(start + len <= dm.T, a.status)) return;
+  const int k0 = at.rest / dm.Hkv * BK;
   if (k0 >= len) return;
   const int nk = min(BK, len - k0);
   const int64_t krow = (start + k0) * dm.Hkv + g;
@@ -321,14 +316,13 @@ __device__ __forceinline__ void kv_pass(const Args& a, Smem<D>& sm, int x, int r
 template <int D>
 __device__ __forceinline__ void q_pass(const Args& a, Smem<D>& sm, int x, int rank) {
   const Dims& dm = a.dm;
-  const Place pl = place(x, dm.batch, dm.Hq);
-  const int h = pl.h, b = pl.b, g = h / (dm.Hq / dm.Hkv);
-  int64_t start;
-  int len;
-  if (!seq_bounds(dm, a.cu, b, start, len, a.status) || !MOBA_CHECK(start + len <= dm.T, a.status))
-    return;
-  const int q0 = ((dm.max_seqlen + BR - 1) / BR - 1 - pl.tile) * BR;
-  if (q0 >= len) return;
+  const TilePlace at = find_tile<BR, true>(dm, a.cu, dm.Hq, x);
+  if (at.slots == 0) return;
+  const int64_t start = at.start;
+  const int len = at.len, h = at.rest % dm.Hq, g = h / (dm.Hq / dm.Hkv);
+  if (!MOBA_CHECK(start + len <= dm.T, a.status)) return;
+  const int q0 = ((len + BR - 1) / BR - 1 - at.rest / dm.Hq) * BR;
+  if (q0 < 0) return;
   load_queries<D>(a, sm, start, q0, len, h);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // queries ty * 4 .., dims tx * 4 + 64 w
   constexpr int NW = D / 64;
@@ -384,12 +378,12 @@ dense_bwd_kernel(const Args a, const int n_kv) {
 
 template <typename T, int D>
 cudaError_t run_stat(const Dims& dm, const void* out, const void* dout, const float* lse,
-                     const int32_t* cu, float* stat, void* dq, void* dk, void* dv,
+                     const int32_t* cu, float* stat, void* dq, void* dk, void* dv, int* status,
                      cudaStream_t st) {
   dense_bwd_stat_kernel<T, D><<<dim3((unsigned)((dm.T + 31) / 32), (unsigned)dm.Hq), kThreads, 0,
                                 st>>>(dm, static_cast<const T*>(out), static_cast<const T*>(dout),
                                       lse, cu, stat, static_cast<T*>(dq), static_cast<T*>(dk),
-                                      static_cast<T*>(dv));
+                                      static_cast<T*>(dv), status);
   return cudaGetLastError();
 }
 
@@ -400,15 +394,12 @@ cudaError_t run_simt(Args a, cudaStream_t st) {
   constexpr int smem = (int)sizeof(Smem<D>);
   static std::atomic<bool> ready[tc::kMaxDevices];
   if ((e = tc::allow_smem(dense_bwd_kernel<D>, smem, ready))) return e;
-  const int64_t tiles = (dm.max_seqlen + BK - 1) / BK, nt = tiles * dm.batch;
-  // CTAs a tile: while one tile's work is more than an SM's share of all (with
-  // T tokens in sequences of the longest length). 1024 + 777 tokens, 4 heads,
-  // d = 64: 318 us with one, 158 with four.
-  const int64_t longest = tiles * (dm.Hq / dm.Hkv);
-  const int64_t share = (int64_t)(dm.T / BK + 1) * dm.Hq * (tiles + 1) / tc::sm_count();
-  a.cs = 1;
-  while (a.cs < 8 && longest > a.cs && longest > a.cs * share) a.cs *= 2;
-  const int64_t clusters = nt * (dm.Hq + dm.Hkv);
+  static_assert(BK == BR, "one number of slots for both passes");
+  const int64_t nt = tile_slots<BK>(dm), clusters = nt * (dm.Hq + dm.Hkv);
+  // 109 + 13 + 64 + 1 tokens, 8 on 2 heads, d = 128: 137 us with one CTA a tile, 46
+  // with four, 80 with eight; 1024 + 777, 4 heads, d = 64: 222 with one, 148 with two
+  // or four. A start costs about as much as an item.
+  a.cs = cluster_for<BK>(dm, tc::sm_count() * (D == 64 ? 2 : 1), 8, 1);
   if (clusters * a.cs > INT32_MAX) return cudaErrorInvalidValue;
   return tc::launch_cluster(dense_bwd_kernel<D>, dim3((unsigned)(clusters * a.cs)), kThreads, smem, st,
                             a.cs, a, (int)(nt * dm.Hkv));
@@ -418,13 +409,13 @@ cudaError_t run_simt(Args a, cudaStream_t st) {
 
 cudaError_t launch_dense_bwd_stat(const Dims& dm, const void* out, const void* dout,
                                   const float* lse, const int32_t* cu, float* stat, void* dq,
-                                  void* dk, void* dv, cudaStream_t st) {
+                                  void* dk, void* dv, int* status, cudaStream_t st) {
   if (dm.dtype == kBF16)
     return dm.d == 128
-               ? run_stat<__nv_bfloat16, 128>(dm, out, dout, lse, cu, stat, dq, dk, dv, st)
-               : run_stat<__nv_bfloat16, 64>(dm, out, dout, lse, cu, stat, dq, dk, dv, st);
-  return dm.d == 128 ? run_stat<float, 128>(dm, out, dout, lse, cu, stat, dq, dk, dv, st)
-                     : run_stat<float, 64>(dm, out, dout, lse, cu, stat, dq, dk, dv, st);
+               ? run_stat<__nv_bfloat16, 128>(dm, out, dout, lse, cu, stat, dq, dk, dv, status, st)
+               : run_stat<__nv_bfloat16, 64>(dm, out, dout, lse, cu, stat, dq, dk, dv, status, st);
+  return dm.d == 128 ? run_stat<float, 128>(dm, out, dout, lse, cu, stat, dq, dk, dv, status, st)
+                     : run_stat<float, 64>(dm, out, dout, lse, cu, stat, dq, dk, dv, status, st);
 }
 
 cudaError_t launch_dense_bwd_simt(const Dims& dm, const void* q, const void* k, const void* v,

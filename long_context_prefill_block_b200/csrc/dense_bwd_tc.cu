@@ -257,12 +257,11 @@ __device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // heads outermost: the CTAs that run together read the same Q and dO, and
   // within a head the tiles with the most queries come first
-  const int nt = (dm.max_seqlen + TT - 1) / TT;
-  const int kt = cta % nt, g = cta / nt % dm.Hkv, b = cta / nt / dm.Hkv;
-  int64_t start;
-  int len;
-  if (!seq_bounds(dm, a.cu, b, start, len, a.status) || !MOBA_CHECK(start + len <= dm.T, a.status))
-    return;
+  const TilePlace at = find_tile<TT, false>(dm, a.cu, dm.Hkv, cta);
+  if (at.slots == 0) return;
+  const int64_t start = at.start;
+  const int len = at.len, kt = at.rest % at.slots, g = at.rest / at.slots;
+  if (!MOBA_CHECK(start + len <= dm.T, a.status)) return;
   const int k0 = kt * TT;
   if (k0 >= len) return;
   const uint32_t sK = sb, sV = sb + kTile, sQ = sb + 2 * kTile, sO = sQ + NA * kTile;
@@ -505,14 +504,13 @@ __device__ __forceinline__ void q_pass(Shared& sh, const uint32_t sb, const int 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // the heads of a group outermost but one: CTAs that run together read the
   // same K and V; the longest tiles of a head come first
-  const int nt = (dm.max_seqlen + TT - 1) / TT;
-  const int qt = nt - 1 - cta % nt, h = cta / nt % dm.Hq, b = cta / nt / dm.Hq;
-  int64_t start;
-  int len;
-  if (!seq_bounds(dm, a.cu, b, start, len, a.status) || !MOBA_CHECK(start + len <= dm.T, a.status))
-    return;
-  const int q0 = qt * TT;
-  if (q0 >= len) return;
+  const TilePlace at = find_tile<TT, false>(dm, a.cu, dm.Hq, cta);
+  if (at.slots == 0) return;
+  const int64_t start = at.start;
+  const int len = at.len, h = at.rest / at.slots;
+  if (!MOBA_CHECK(start + len <= dm.T, a.status)) return;
+  const int qt = (len + TT - 1) / TT - 1 - at.rest % at.slots, q0 = qt * TT;
+  if (qt < 0) return;
   const int g = h / (dm.Hq / dm.Hkv);
   const int n_items = (qt + 1 - rank + cs - 1) / cs;  // key tiles rank, rank + cs, ..; 0 is possible
   const bool diagonal = rank == qt % cs;              // the last of them is the diagonal
@@ -706,18 +704,13 @@ cudaError_t run(const Args& a, const void* q, const void* k, const void* v, cons
   constexpr int smem = (int)Cfg<D>::kSmem;
   static std::atomic<bool> ready[kMaxDevices];
   if ((e = allow_smem(dense_bwd_tc<D>, smem, ready))) return e;
-  const int64_t tiles = (dm.max_seqlen + TT - 1) / TT, nt = tiles * dm.batch;
-  // CTAs a tile: while one tile's items are more than twice an SM's share of
-  // all (with T tokens in sequences of the longest length), and worth a sum.
-  // 300 + 212 tokens, 4 on 2 heads: 20 us with one CTA, 15.5 with four, 27 with
-  // eight (clusters of eight leave SMs without one); 8191 tokens, 4 on 1 head:
-  // 225 us with two, the rule's choice, 274 with four.
-  const int64_t longest = tiles * (dm.Hq / dm.Hkv);
-  const int64_t share = (int64_t)(dm.T / TT + 1) * dm.Hq * (tiles + 1) / sm_count();
-  int cs = 1;
-  while (cs < 4 && longest > cs * 2 && longest > cs * 2 * share) cs *= 2;
-  if (nt * (dm.Hq + dm.Hkv) * cs > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_beside(dense_bwd_tc<D>, dim3((unsigned)(nt * (dm.Hq + dm.Hkv) * cs)), kThreads, smem,
+  // 300 + 212 tokens, 4 on 2 heads: 21 us with one CTA a tile, 15 with four; 692 +
+  // 88 + 6 + 10 + 40, 24 on 8 heads: 44 with one, 58 with two; 8191, 4 on 1 head: 436
+  // with one, 222 with two, 274 with four. Clusters of eight leave SMs without one.
+  const int64_t nt = tile_slots<TT>(dm), clusters = nt * (dm.Hq + dm.Hkv);
+  const int cs = cluster_for<TT>(dm, sm_count(), 4, 5);  // a start costs as much as five items
+  if (clusters * cs > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_beside(dense_bwd_tc<D>, dim3((unsigned)(clusters * cs)), kThreads, smem,
                        st, cs, mq, mk, mv, mo, a, (int)(nt * dm.Hkv), cs);
 }
 

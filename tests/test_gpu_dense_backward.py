@@ -175,6 +175,16 @@ def test_many_tiles_and_a_generous_max_seqlen():
     check(q, k, v, do, cu, out, lse, grads)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens,Hq,Hkv,d", [
+    ((600,) + (0, 1, 3) * 15, 4, 2, 64), ((0, 0, 2) * 12 + (900, 127, 128, 129, 0), 2, 2, 128),
+    ((700, 5, 5, 5), 9, 3, 128), ((1,) * 33 + (770, 0) + (2,) * 40, 1, 1, 64)])
+def test_one_long_sequence_among_short_ones(lens, Hq, Hkv, d, dtype):
+    """Far fewer tiles than the longest sequence's in each: places are searched, over more than 31
+    sequences too."""
+    test_gradients_match_the_formulas(lens, Hq, Hkv, d, dtype)
+
+
 def test_two_layers_trained_together():
     """A block-attention layer and a dense layer in a row, as a hybrid stack has them: the loss's
     gradient at the inputs through both, fp32, against 64-bit autograd of the same stack with all
