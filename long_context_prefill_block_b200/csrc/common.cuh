@@ -180,12 +180,12 @@ struct TilePlace {
 };
 template <int ROWS>
 __host__ __device__ inline bool even_lengths(const Dims& dm) {
-  return (int64_t)((dm.max_seqlen + ROWS - 1) / ROWS) * dm.batch <=
+  return ((int64_t)dm.max_seqlen + ROWS - 1) / ROWS * dm.batch <=
          2 * ((int64_t)(dm.T / ROWS) + dm.batch);
 }
 template <int ROWS>
 __host__ __device__ inline int64_t tile_slots(const Dims& dm) {
-  return even_lengths<ROWS>(dm) ? (int64_t)((dm.max_seqlen + ROWS - 1) / ROWS) * dm.batch
+  return even_lengths<ROWS>(dm) ? ((int64_t)dm.max_seqlen + ROWS - 1) / ROWS * dm.batch
                                 : (int64_t)(dm.T / ROWS) + dm.batch;
 }
 // TILE_MAJOR: with even lengths tile 0 of every sequence comes first, then tile
@@ -195,7 +195,7 @@ __device__ __forceinline__ TilePlace find_tile(const Dims& dm, const int32_t* __
                                                int heads, int x) {
   int b, slots, rest;
   if (even_lengths<ROWS>(dm)) {
-    slots = (dm.max_seqlen + ROWS - 1) / ROWS;
+    slots = (int)(((int64_t)dm.max_seqlen + ROWS - 1) / ROWS);
     if (TILE_MAJOR) {
       b = x / heads % dm.batch;
       rest = x / heads / dm.batch * heads + x % heads;
@@ -404,7 +404,8 @@ inline int cluster_for(Dims dm, int64_t at_once, int most, int start) {
   int T = 1;
   while (T < dm.T && T < 1 << 30) T *= 2;
   dm.T = T;
-  const int64_t tiles = (dm.max_seqlen + ROWS - 1) / ROWS, longest = tiles * (dm.Hq / dm.Hkv);
+  const int64_t top = dm.max_seqlen < T ? dm.max_seqlen : T;  // the bound may be generous
+  const int64_t tiles = (top + ROWS - 1) / ROWS, longest = tiles * (dm.Hq / dm.Hkv);
   const int64_t clusters = tile_slots<ROWS>(dm) * (dm.Hq + dm.Hkv);
   const int64_t all = (int64_t)(dm.T / ROWS + 1) * dm.Hq * (tiles + 1);  // sequences of max_seqlen
   int best = 1;

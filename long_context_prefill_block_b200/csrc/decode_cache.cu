@@ -33,7 +33,7 @@ constexpr int kMaxPages = kMaxKeys / 16 + 2 * kMaxSlots;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // How a row's keys are divided. Its slots are the topk - 1 places for chosen
-// earlier blocks and, last, the own block, which with shared routing is one
+// earlier blocks (no more than there can be such blocks) and, last, the own block, which with shared routing is one
 // slot among them and else is read apart, once for all heads of a group. Split
 // x: of group x / parts of `slots` slots, part x % parts of each block (parts
 // > 1 only where a group is one slot).
@@ -41,6 +41,7 @@ struct Split {
   int keys;    // of a part
   int parts;   // of a block
   int slots;   // of a group
+  int own;     // the own block's slot
   int groups;  // before the own block's
   int per_row;
 };
@@ -49,14 +50,21 @@ struct Split {
 // loads) is small beside its keys, while two CTAs an SM are left: large blocks
 // in parts of up to 2048 keys, small ones together. 48 x 32768 tokens, three
 // shared blocks of 512: 54 us with a block a CTA, 41 with all three (which
-// also need no merge). The rule asks for the call's sizes alone, so that the
-// workspace does not depend on the device that is current.
+// also need no merge). No slots for blocks that cannot exist: 8 requests of 778
+// tokens, four queries, blocks of 2048, topk 3: 33 us with them, 17.5 without.
+// fp32 queries have a CTA per q head with shared routing too (40 on 8 heads, eight
+// of 282 blocks: 101 us when counted by kv heads, 40). The rule asks for the
+// call's sizes alone, so that the workspace does not depend on the device that is
+// current.
 Split split_of(const Dims& dm) {
-  const int64_t units = (int64_t)dm.T * (dm.shared ? dm.Hkv : dm.Hq), least = 2 * kSMs;
-  const int listed = dm.shared ? dm.topk : dm.topk - 1;
-  Split s{128, 1, 1, 0, 0};
+  // fp32 queries have a CTA per q head in either case
+  const int64_t units = (int64_t)dm.T * (dm.shared && dm.dtype == kBF16 ? dm.Hkv : dm.Hq);
+  const int64_t least = 2 * kSMs;
+  const int k = dm.nb < 1 ? 1 : dm.topk < dm.nb ? dm.topk : dm.nb;
+  const int listed = dm.shared ? k : k - 1;
+  Split s{128, 1, 1, k - 1, 0, 0};
   while (s.keys < kMaxKeys && s.keys < dm.B &&
-         units * dm.topk * (((int64_t)dm.B + 2 * s.keys - 1) / (2 * s.keys)) >= 2 * least)
+         units * k * (((int64_t)dm.B + 2 * s.keys - 1) / (2 * s.keys)) >= 2 * least)
     s.keys *= 2;
   if (s.keys > dm.B) s.keys = dm.B;
   s.parts = (int)(((int64_t)dm.B + s.keys - 1) / s.keys);
@@ -86,9 +94,9 @@ struct Step {
 
 // Slots [first, last) of split x.
 __device__ __forceinline__ void split_slots(const Step& a, int x, int& first, int& last) {
-  const int group = x / a.sp.parts, listed = a.dm.shared ? a.dm.topk : a.dm.topk - 1;
-  first = group < a.sp.groups ? group * a.sp.slots : a.dm.topk - 1;
-  last = group < a.sp.groups ? min(first + a.sp.slots, listed) : a.dm.topk;
+  const int group = x / a.sp.parts, own = a.sp.own, listed = a.dm.shared ? own + 1 : own;
+  first = group < a.sp.groups ? group * a.sp.slots : own;
+  last = group < a.sp.groups ? min(first + a.sp.slots, listed) : own + 1;
 }
 
 // Keys [lo, hi) of one slot of split x, for a row at position p (empty: lo >= hi).
@@ -97,9 +105,9 @@ __device__ __forceinline__ void split_slots(const Step& a, int x, int& first, in
 __device__ __forceinline__ void slot_range(const Step& a, const int32_t* list, int x, int slot,
                                            int p, int& lo, int& hi) {
   const int B = a.dm.B, own = p / B;
-  const int e = slot == a.dm.topk - 1 ? own : list[slot];
+  const int e = slot == a.sp.own ? own : list[slot];
   lo = hi = 0;
-  if (slot == a.dm.topk - 1 || (e >= 0 && e < own)) {
+  if (slot == a.sp.own || (e >= 0 && e < own)) {
     lo = e * B + x % a.sp.parts * a.sp.keys;
     hi = min(lo + a.sp.keys, e < own ? (e + 1) * B : p + 1);
   }
@@ -508,7 +516,8 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   }
   if (!a.gated && s == 0)
     for (int e = tid; e < nh * dm.topk; e += kW * 32)
-      a.idx[row0 * dm.topk + e] = a.sp.groups > 0 ? og.list[e % dm.topk] : p / dm.B;
+      a.idx[row0 * dm.topk + e] = a.sp.groups > 0 ? og.list[e % dm.topk]
+                                              : e % dm.topk == 0 ? p / dm.B : -1;
   const int page = 1 << cc.page_log2;
   // lane x of every warp: slot x of the split, its keys, steps and page entries
   int my_lo = 0, my_hi = 0, my_step, my_page;  // step: one past the slot's last; page: its first
@@ -881,7 +890,7 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
   }
   if (!a.gated && s == 0)
     for (int e = tid; e < dm.topk; e += kThreads)
-      a.idx[row * dm.topk + e] = a.sp.groups > 0 ? og.list[e] : p / dm.B;
+      a.idx[row * dm.topk + e] = a.sp.groups > 0 ? og.list[e] : e == 0 ? p / dm.B : -1;
   const int grp_id = warp * GPW + lane / LPK, sub = lane % LPK;
   const float sl2 = kLog2e * rsqrtf((float)D);
   float qv[16];

@@ -266,6 +266,16 @@ def test_decode_matches_the_definition(lens, nq, Hq, Hkv, d, page, B, topk, dtyp
     assert ref.off(mine[:n], out.double().cpu()) <= 2 * TOL[dtype]
 
 
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens,nq,Hq,Hkv,d,page,B,topk", [
+    ([100, 3, 128], [2, 3, 1], 4, 2, 128, 16, 128, 5),
+    ([300, 17, 512], [1, 0, 2], 10, 2, 64, 32, 256, 8),
+    ([700, 1500], [3, 1], 8, 8, 128, 64, 1024, 12)])
+def test_topk_past_the_blocks_there_are(lens, nq, Hq, Hkv, d, page, B, topk, dtype, shared):
+    test_decode_matches_the_definition(lens, nq, Hq, Hkv, d, page, B, topk, dtype, shared)
+
+
 @pytest.mark.parametrize("dtype,shared", [(torch.bfloat16, False), (torch.float32, True)])
 @pytest.mark.parametrize("lens,B,topk,Hq", [
     ([17600, 200], 16, 6, 2), ([5000, 4097], 1, 32, 18), ([49300, 50], 1, 3, 2),

@@ -176,6 +176,13 @@ def test_many_tiles_and_a_generous_max_seqlen():
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_largest_bound_on_the_lengths(dtype):
+    q, k, v, do, cu = case((300, 20), 4, 2, 64, dtype, seed=3)
+    out, lse, grads = run(q, k, v, do, cu, max_seqlen=2 ** 31 - 1)
+    check(q, k, v, do, cu, out, lse, grads)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("lens,Hq,Hkv,d", [
     ((600,) + (0, 1, 3) * 15, 4, 2, 64), ((0, 0, 2) * 12 + (900, 127, 128, 129, 0), 2, 2, 128),
     ((700, 5, 5, 5), 9, 3, 128), ((1,) * 33 + (770, 0) + (2,) * 40, 1, 1, 64)])
