@@ -189,18 +189,25 @@ def _at(x: Optional[torch.Tensor]):
 
 
 def _dev_i32(cu: torch.Tensor, device) -> torch.Tensor:
-    return cu.to(device=device, dtype=torch.int32).contiguous()
+    if cu.dtype != torch.int32 or cu.device != device:  # what to() costs even for nothing
+        cu = cu.to(device=device, dtype=torch.int32)
+    return cu.contiguous()
 
 
 def _check_inputs(*ts):
-    devices = set()
+    first, mixed = None, False
     for t in ts:
         if t is not None:
-            if not t.is_cuda or not t.is_contiguous():
+            at = t.get_device()  # -1: not on a GPU
+            if at < 0 or not t.is_contiguous():
                 raise ValueError("tensors must be contiguous CUDA tensors")
-            devices.add(t.get_device())
-    if len(devices) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(f'cuda:{i}' for i in devices)}")
+            if first is None:
+                first = at
+            elif at != first:
+                mixed = True
+    if mixed:
+        names = sorted({str(t.device) for t in ts if t is not None})
+        raise ValueError(f"tensors on different devices: {names}")
 
 
 def _check_qkv(q, k, v=None, out=None):
@@ -627,8 +634,8 @@ def moba_cache_read(cache: MobaCache, page_table, seqlens, cu_rows, total_rows: 
     c = _check_cache(cache, hkv, d, page_table, seqlens, cu_rows, k, v)
     dev = cache.k.device
     p = _cache_params(page_table.shape[0], total_rows, hkv, hkv, d, dtype, 1, 1, 2**31 - 1)
-    k = torch.empty((total_rows, hkv, d), dtype=dtype, device=dev) if k is None else k
-    v = torch.empty((total_rows, hkv, d), dtype=dtype, device=dev) if v is None else v
+    k = torch.empty(total_rows, hkv, d, dtype=dtype, device=dev) if k is None else k
+    v = torch.empty(total_rows, hkv, d, dtype=dtype, device=dev) if v is None else v
     _call("moba_cache_read", dev, p, c, _at(cu_rows), _at(k), _at(v))
     return k, v
 
@@ -661,8 +668,8 @@ def moba_decode_cache(q, cache: MobaCache, page_table, seqlens, cu_q, kbar, bloc
     p = _cache_params(batch, n, hq, hkv, d, q.dtype, block_size, topk, max_seqlen, shared_routing)
     ws = _workspace("moba_decode_cache_workspace_size", p, dev, ws)
     out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((n, hq), dtype=torch.float32, device=dev) if return_lse else None
-    idx = torch.empty((n, hq, topk), dtype=torch.int32, device=dev) if return_idx else None
+    lse = torch.empty(n, hq, dtype=torch.float32, device=dev) if return_lse else None
+    idx = torch.empty(n, hq, topk, dtype=torch.int32, device=dev) if return_idx else None
     _call("moba_decode_cache", dev, p, _at(q), c, _at(cu_q), _at(kbar), _at(out), _at(lse), _at(idx),
           _at(ws), _nbytes(ws))
     res = (out,)
