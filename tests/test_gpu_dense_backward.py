@@ -192,6 +192,17 @@ def test_one_long_sequence_among_short_ones(lens, Hq, Hkv, d, dtype):
     test_gradients_match_the_formulas(lens, Hq, Hkv, d, dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cu", [[0], [0, 0], [0, 0, 0]])
+def test_rows_of_no_sequence_at_all_get_zeros(cu, dtype):
+    q, k, v, do, _ = (x.to(DEV) for x in case((70,), 4, 2, 64, dtype, seed=2))
+    lse = torch.zeros(70, 4, device=DEV)
+    grads = moba.dense_causal_backward(q, k, v, torch.tensor(cu, dtype=torch.int32, device=DEV), q,
+                                       lse, do, max_seqlen=70)
+    assert moba.moba_device_status() == 0
+    assert not any(x.any() for x in grads)
+
+
 def test_two_layers_trained_together():
     """A block-attention layer and a dense layer in a row, as a hybrid stack has them: the loss's
     gradient at the inputs through both, fp32, against 64-bit autograd of the same stack with all
