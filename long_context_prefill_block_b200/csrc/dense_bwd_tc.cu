@@ -372,11 +372,20 @@ __device__ __forceinline__ void kv_pass(Shared& sh, const uint32_t sb, const int
       const int s = it & 1, n = i == per - 1 ? last_rows : TT;
       bool ok = it < 2 || mbar_wait(&sh.stat_empty[s], (it / 2 - 1) & 1, abort, status);
       if (!__all_sync(0xffffffffu, ok)) break;
+      // ordinary loads: the launch that writes these may run beside this one, so
+      // they are not read-only for it
       const float* src = st + (int64_t)h * dm.T + i * TT;
+      float l2[TT / 32], dd[TT / 32];
 #pragma unroll
-      for (int r = lane; r < TT; r += 32) {
-        sh.lse2[s][r] = r < n ? __ldg(src + r) : 0.f;
-        sh.D[s][r] = r < n ? __ldg(src + (int64_t)dm.Hq * dm.T + r) : 0.f;
+      for (int x = 0; x < TT / 32; ++x) {
+        const int r = lane + 32 * x;
+        l2[x] = r < n ? src[r] : 0.f;
+        dd[x] = r < n ? src[(int64_t)dm.Hq * dm.T + r] : 0.f;
+      }
+#pragma unroll
+      for (int x = 0; x < TT / 32; ++x) {
+        sh.lse2[s][lane + 32 * x] = l2[x];
+        sh.D[s][lane + 32 * x] = dd[x];
       }
       warp_arrive(&sh.stat_full[s]);
       if (n < TT) {
@@ -605,8 +614,8 @@ __device__ __forceinline__ void q_pass(Shared& sh, const uint32_t sb, const int 
     grid_wait();  // the statistics are the launch before this one
     if (on) {
       const float* st = a.stat + (int64_t)h * dm.T + start + q0 + r;
-      l2 = __ldg(st);
-      dd = __ldg(st + (int64_t)dm.Hq * dm.T);
+      l2 = st[0];  // ordinary loads, as in the key pass
+      dd = st[(int64_t)dm.Hq * dm.T];
     }
     bool ok = true;
     for (int j = 0; j < n_items; ++j) {

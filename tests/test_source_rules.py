@@ -1,0 +1,41 @@
+"""Rules that the kernels' sources keep and that no run shows broken reliably, checked on the text."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "long_context_prefill_block_b200", "csrc")
+
+
+def source(name):
+    """A kernel file without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+
+
+def arguments(text, call):
+    """The argument text of every `call(...)`."""
+    res = []
+    for m in re.finditer(re.escape(call) + r"\(", text):
+        at, depth = m.end(), 1
+        while depth:
+            depth += {"(": 1, ")": -1}.get(text[at], 0)
+            at += 1
+        res.append(text[m.end():at - 1])
+    return res
+
+
+# what the launch ahead of an overlapped one writes and the overlapped one reads, by its names
+OVERLAPPED = [("dense_bwd_tc.cu", "stat|st|src")]
+
+
+@pytest.mark.parametrize("name,written", OVERLAPPED)
+def test_results_of_an_overlapped_launch_are_read_by_ordinary_loads(name, written):
+    """The read-only path (__ldg, or const __restrict__ parameters) is for memory that nothing writes
+    while the kernel runs. A kernel that begins beside the launch it depends on is not that."""
+    text = source(name)
+    assert "grid_wait()" in text
+    names = re.compile(rf"\b({written})\b")
+    assert not [a for a in arguments(text, "__ldg") if names.search(a)]
+    assert not re.search(rf"\bconst\s+\w+\s*\*\s*__restrict__\s+({written})\b", text)
