@@ -286,13 +286,16 @@ __device__ __forceinline__ Slot find_slot(const Dims& dm, const Cache& c,
 // left sums of 32 packed rows, those inside a part are added up (1/8 of the
 // codes' bytes); the other rows are read: LPR lanes of 16 bytes a row, fp32 sums
 // of every G-th row, then the lane groups' sums and the CTAs' sums in order.
-// 12 us for 64 blocks of 4096 and 8 heads.
+// 11 us for 64 blocks of 4096 and 8 heads.
+//
+// Both kernels of the means begin beside the write, which still stores codes,
+// scales and sums then: they read these by ordinary loads, after the wait.
 constexpr int kMeanPages = 2048 / 16 + 1;  // pages looked up at a time
 
 template <int D>
 __global__ void __launch_bounds__(kMeanThreads, 4)
 cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
-                   const float* __restrict__ sums, float* __restrict__ kbar, int cs, int* status) {
+                   const float* sums, float* __restrict__ kbar, int cs, int* status) {
   constexpr int LPR = D / 16, G = kMeanThreads / LPR, U = 8;
   constexpr int LPS = D / 4, GS = kMeanThreads / LPS;  // lanes and streams of sums
   __shared__ float sum[G + GS][D + 4];
@@ -365,7 +368,7 @@ cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
 #pragma unroll 4
     for (int i = g0 + sg; i < g1; i += GS) {
       const float4 v =
-          __ldg(reinterpret_cast<const float4*>(sums + ((int64_t)i * dm.Hkv + g) * D) + ss);
+          reinterpret_cast<const float4*>(sums + ((int64_t)i * dm.Hkv + g) * D)[ss];
       t.x += v.x;
       t.y += v.y;
       t.z += v.z;
@@ -400,7 +403,7 @@ constexpr int kSmallWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(kSmallWarps * 32)
 cache_small_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
-                         const float* __restrict__ sums, float* __restrict__ kbar, int* status) {
+                         const float* sums, float* __restrict__ kbar, int* status) {
   constexpr int LPR = D / 16, G = 32 / LPR, U = 4;  // lanes of a row of codes, rows a load
   constexpr int LPS = D / 4, GS = 32 / LPS;         // the same for sums
   const int lane = threadIdx.x & 31, B = dm.B;
@@ -436,7 +439,7 @@ cache_small_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
 #pragma unroll 4
   for (int i = g0 + sg; i < g1; i += GS) {
     const float4 v =
-        __ldg(reinterpret_cast<const float4*>(sums + ((int64_t)i * dm.Hkv + g) * D) + ss);
+        reinterpret_cast<const float4*>(sums + ((int64_t)i * dm.Hkv + g) * D)[ss];
     t[0] += v.x;
     t[1] += v.y;
     t[2] += v.z;

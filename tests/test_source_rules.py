@@ -27,7 +27,7 @@ def arguments(text, call):
 
 
 # what the launch ahead of an overlapped one writes and the overlapped one reads, by its names
-OVERLAPPED = [("dense_bwd_tc.cu", "stat|st|src")]
+OVERLAPPED = [("dense_bwd_tc.cu", "stat|st|src"), ("cache.cu", r"sums|c\.ks?")]
 
 
 @pytest.mark.parametrize("name,written", OVERLAPPED)
