@@ -298,7 +298,7 @@ cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
                    const float* sums, float* __restrict__ kbar, int cs, int* status) {
   constexpr int LPR = D / 16, G = kMeanThreads / LPR, U = 8;
   constexpr int LPS = D / 4, GS = kMeanThreads / LPS;  // lanes and streams of sums
-  __shared__ float sum[G + GS][D + 4];
+  __shared__ __align__(16) float sum[G + GS][D + 4];
   __shared__ float part[kMaxCluster][D];
   __shared__ int page_row[kMeanPages];
   const int g = blockIdx.y, B = dm.B, rank = blockIdx.x % cs;

@@ -39,3 +39,13 @@ def test_results_of_an_overlapped_launch_are_read_by_ordinary_loads(name, writte
     names = re.compile(rf"\b({written})\b")
     assert not [a for a in arguments(text, "__ldg") if names.search(a)]
     assert not re.search(rf"\bconst\s+\w+\s*\*\s*__restrict__\s+({written})\b", text)
+
+
+@pytest.mark.parametrize("name", sorted(x for x in os.listdir(CSRC) if x.endswith(".cu")))
+def test_shared_arrays_read_in_16_bytes_are_aligned_to_them(name):
+    """An array of 4-byte elements is aligned to 4 bytes unless its declaration says more."""
+    text = source(name)
+    wide = set(re.findall(r"reinterpret_cast<(?:const )?(?:float4|uint4)\s*\*>\(&?(\w+)\s*[\[,)+]", text))
+    for statement in re.findall(r"__shared__ ([^;]*);", text):
+        names = set(re.findall(r"\b(\w+)\s*\[", statement)) & wide
+        assert not names or "__align__" in statement, names
