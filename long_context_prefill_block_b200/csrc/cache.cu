@@ -145,7 +145,8 @@ __device__ __forceinline__ int token_row(const Dims& dm, const Cache& c,
   const int lane = threadIdx.x & 31;
   int r, pos, len;
   if (lane >= p.n ||
-      !tail_position(cu, c.lens, dm.batch, max_positions(dm, c), p.t0 + lane, r, pos, len, status))
+      !tail_position(cu, c.lens, dm.batch, dm.T, max_positions(dm, c), p.t0 + lane, r, pos, len,
+                     status))
     return -1;
   return (int)cache_row(c, dm.Hkv, r, pos, p.g, status);
 }
@@ -250,13 +251,16 @@ cache_write_kernel(Dims dm, Cache c, const T* __restrict__ k, const T* __restric
 }
 
 // Which block a slot stands for. Request r's completed blocks have slots from
-// cu_new[r] / B + r on (n / B + 1 of them at most). Called by whole warps.
+// cu_new[r] / B + r on (n / B + 1 of them at most). A request that the write
+// skipped has none; one whose rows are not all among the call's is reported here
+// too, since the write sees none of a request behind them. Called by whole warps.
 struct Slot {
   int r, blk;       // blk: -1 for none
   int begin, row0;  // position and packed row of the request's first new row
 };
 __device__ __forceinline__ Slot find_slot(const Dims& dm, const Cache& c,
-                                          const int32_t* __restrict__ cu_new, int slot) {
+                                          const int32_t* __restrict__ cu_new, int slot,
+                                          int* status) {
   const int B = dm.B;
   Slot s{0, -1, 0, 0};
   int r = 0;  // the largest with cu_new[r] / B + r <= slot, 32 requests a round
@@ -270,7 +274,9 @@ __device__ __forceinline__ Slot find_slot(const Dims& dm, const Cache& c,
   }
   if (r < dm.batch) {
     const int n = cu_new[r + 1] - cu_new[r], len = c.lens[r];
-    if (n > 0 && len >= n && len <= max_positions(dm, c)) {
+    if (n > 0 && (cu_new[r] < 0 || cu_new[r + 1] > dm.T)) {
+      set_status(status, kStInvalidArg);
+    } else if (n > 0 && len >= n && len <= max_positions(dm, c)) {
       s.begin = len - n;
       s.row0 = cu_new[r];
       s.blk = s.begin / B + slot - (s.row0 / B + r);
@@ -302,7 +308,7 @@ cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
   __shared__ float part[kMaxCluster][D];
   __shared__ int page_row[kMeanPages];
   const int g = blockIdx.y, B = dm.B, rank = blockIdx.x % cs;
-  const Slot at = find_slot(dm, c, cu_new, blockIdx.x / cs);
+  const Slot at = find_slot(dm, c, cu_new, blockIdx.x / cs, status);
   const int r = at.r, blk = at.blk, begin = at.begin, row0 = at.row0;
   tc::grid_wait();  // the rows
   if (blk < 0) return;  // the whole cluster
@@ -411,7 +417,7 @@ cache_small_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
   const int64_t slot = w / dm.Hkv;
   const int g = (int)(w % dm.Hkv);
   Slot at{0, -1, 0, 0};
-  if (slot < (int64_t)dm.T / B + dm.batch) at = find_slot(dm, c, cu_new, (int)slot);
+  if (slot < (int64_t)dm.T / B + dm.batch) at = find_slot(dm, c, cu_new, (int)slot, status);
   const int blk = at.blk, first = blk * B, last = first + B;
   // the block's pages, at most 17: lane x looks page x up
   int pages = -1;

@@ -227,17 +227,18 @@ __device__ __forceinline__ TilePlace find_tile(const Dims& dm, const int32_t* __
 // Request r and cache position of row i of a call on a paged cache: request
 // r's rows cu[r] .. cu[r+1]-1 stand at the last positions of its seqlens[r].
 // False for a row that no request owns (a padded batch), and, with a status
-// code, for a request whose length does not hold its rows or passes max_len.
+// code, for a request whose length does not hold its rows or passes max_len, or
+// whose rows are not all among the call's `rows`.
 // whole_warp: every lane of the warp asks for the same i.
 __device__ __forceinline__ bool tail_position(const int32_t* __restrict__ cu,
                                               const int32_t* __restrict__ seqlens, int batch,
-                                              int max_len, int i, int& r, int& pos, int& len,
-                                              int* status, bool whole_warp = false) {
+                                              int rows, int max_len, int i, int& r, int& pos,
+                                              int& len, int* status, bool whole_warp = false) {
   r = whole_warp ? find_request_warp(cu, batch, i) : find_request(cu, batch, i);
   if (r >= batch || i < cu[r]) return false;
   const int n = cu[r + 1] - cu[r];
   len = seqlens[r];
-  if (len < n || len > max_len) {
+  if (len < n || len > max_len || cu[r] < 0 || cu[r + 1] > rows) {
     set_status(status, kStInvalidArg);
     return false;
   }

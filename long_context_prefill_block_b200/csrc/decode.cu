@@ -89,7 +89,7 @@ decode_gate_kernel(Dims dm, const T* __restrict__ q, const float* __restrict__ k
   const int qi = blockIdx.x / H, u = blockIdx.x % H;
   int r, len, p;
   if constexpr (kPaged) {  // whole CTA
-    if (!tail_position(cu_q, cu, dm.batch, max_len, qi, r, p, len, status)) return;
+    if (!tail_position(cu_q, cu, dm.batch, dm.T, max_len, qi, r, p, len, status)) return;
   } else {
     int64_t start;
     if (!decode_position(dm, cu, cu_q, qi, r, start, len, p, status)) return;

@@ -249,7 +249,8 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const int cs, const int
     qs[e / D][e % D] = s;
   }
   int r, len, p;
-  if (!tail_position(a.cu_q, a.c.lens, dm.batch, a.max_len, qi, r, p, len, a.status, true))
+  if (!tail_position(a.cu_q, a.c.lens, dm.batch, dm.T, a.max_len, qi, r, p, len, a.status,
+                     true))
     return;
   const int c = p / dm.B, need = min(dm.topk - 1, c);
   auto sync = [&] {
@@ -502,7 +503,7 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   tc::mbar_fence_init();
   int r, len, p;
   const bool valid =
-      tail_position(a.cu_q, cc.lens, dm.batch, a.max_len, qi, r, p, len,
+      tail_position(a.cu_q, cc.lens, dm.batch, dm.T, a.max_len, qi, r, p, len,
                     a.gated ? nullptr : a.status, true);
   // a split of own blocks alone needs no choice, and the merge waits for others
   // that did wait
@@ -877,7 +878,7 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = (int64_t)qi * dm.Hq + h, prow = row * S + s;
   int r, len, p;
-  const bool valid = tail_position(a.cu_q, c.lens, dm.batch, a.max_len, qi, r, p, len,
+  const bool valid = tail_position(a.cu_q, c.lens, dm.batch, dm.T, a.max_len, qi, r, p, len,
                                    a.gated ? nullptr : a.status, true);
   tc::grid_wait();  // the chosen blocks
   if (!valid) return;
@@ -1016,7 +1017,7 @@ cache_merge_kernel(const Step a, T* __restrict__ out, float* __restrict__ lse_ou
   const int64_t row = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = a.sp.per_row;
   int r, len, p;
-  const bool valid = tail_position(a.cu_q, a.c.lens, a.dm.batch, a.max_len,
+  const bool valid = tail_position(a.cu_q, a.c.lens, a.dm.batch, a.dm.T, a.max_len,
                                    (int)(row / a.dm.Hq), r, p, len, nullptr, true);
   tc::grid_wait();  // the partials
   if (!valid) return;

@@ -502,3 +502,66 @@ def test_two_streams_at_once():
                 got.append(moba.moba_decode_cache(q[i], *args))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("rows,heads,B", [([40, 30], 2, 16), ([40, 30], 2, 300),
+                                          ([6000, 3500], 8, 512), ([6000, 3500], 8, 64)])
+@pytest.mark.parametrize("where", ["inside", "behind", "before"])
+def test_offsets_past_the_rows_of_a_call_are_reported_and_skipped(rows, heads, B, where):
+    """Offsets on the device that promise more rows than the call has: the request that reaches past
+    them is left alone in every call, the other one is served. The larger calls make block means
+    from sums of 32 rows, which exist for the call's rows only."""
+    d, n = 64, sum(rows)
+    lens = [rows[0] + 5, rows[1] + 700]
+    cu = {"inside": [0, rows[0], n + 600],  # its first rows are there
+          "behind": [0, n, n + 600],        # none of its rows is there
+          "before": [-600, rows[0], n]}[where]
+    bad = 0 if where == "before" else 1
+    good = 1 - bad
+    lens[good] = max(lens[good], cu[good + 1] - cu[good])
+    lens[0] += 600 if where == "before" else 0
+    pool, _ = filled([x + 8 for x in lens], heads, d, 32, B, seed=5)
+    before = pool.bits()
+    g = torch.Generator(device=DEV).manual_seed(1)
+    k, v = (torch.randn(n, heads, d, generator=g, device=DEV).bfloat16() for _ in range(2))
+    kbar = torch.full((2, -(-max(lens) // B), heads, d), 7.0, device=DEV)
+    assert moba.moba_device_status() == 0
+    moba.moba_cache_write(pool.cache, k, v, pool.table, i32(lens), i32(cu), kbar, B)
+    assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG
+    # the same as a call in which the other request has no rows
+    alone = list(cu)
+    alone[2 * bad] = alone[1]
+    want, mine = torch.full_like(kbar, 7.0), pool.bits()
+    for x, y in zip(pool.cache, before):
+        x.view(torch.uint8).copy_(y)
+    moba.moba_cache_write(pool.cache, k, v, pool.table, i32(lens), i32(alone), want, B)
+    assert moba.moba_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(pool.bits(), mine))
+    assert torch.equal(kbar, want) and (kbar[bad] == 7.0).all()
+    if cu[good + 1] - cu[good] >= B:
+        assert (kbar[good] != 7.0).any()
+    got, want = ([torch.full_like(k, 3.0) for _ in range(2)] for _ in range(2))
+    moba.moba_cache_read(pool.cache, pool.table, i32(lens), i32(cu), n, k=got[0], v=got[1])
+    # a read asks for rows that the call has: it cannot see a request behind them
+    seen = moba.MOBA_OK if where == "behind" else moba.MOBA_ERR_INVALID_ARG
+    assert moba.moba_device_status() == seen
+    moba.moba_cache_read(pool.cache, pool.table, i32(lens), i32(alone), n, k=want[0], v=want[1])
+    assert moba.moba_device_status() == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B", [64, 8])  # choice inside each split, and in a launch of its own
+def test_decode_offsets_past_the_queries_are_reported_and_skipped(B, dtype):
+    lens = [300, 900]
+    pool, kbar = filled(lens, 2, 64, 32, B, seed=6)
+    q = torch.randn(4, 4, 64, generator=torch.Generator().manual_seed(2)).to(dtype).to(DEV)
+    args = (kbar, B, 3)
+    want = moba.moba_decode_cache(q, pool.cache, pool.table, i32(lens), i32([0, 2, 4]), *args)
+    out = torch.full_like(q, 9.0)
+    moba.moba_decode_cache(q, pool.cache, pool.table, i32(lens), i32([0, 2, 5]), *args, out=out)
+    assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG
+    assert torch.equal(out[:2], want[:2]) and (out[2:] == 9).all()
+    out.fill_(9.0)
+    moba.moba_decode_cache(q, pool.cache, pool.table, i32(lens), i32([-1, 2, 4]), *args, out=out)
+    assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG
+    assert torch.equal(out[2:], want[2:]) and (out[:2] == 9).all()
