@@ -282,8 +282,8 @@ MOBA_API moba_status dense_causal_forward(const moba_params* p, const void* q, c
  *   dout [T][Hq][d]: p->dtype.
  *   dq [T][Hq][d], dk, dv [T][Hkv][d]: p->dtype (summed in fp32, rounded once),
  *   overwritten; rows that no sequence owns get zeros, and so do those of a
- *   sequence longer than max_seqlen, which is skipped and recorded
- *   (MOBA_ERR_INVALID_ARG in the status word).
+ *   sequence longer than max_seqlen, or one whose rows are not all among the T,
+ *   which is skipped and recorded (MOBA_ERR_INVALID_ARG in the status word).
  *   ws: dense_causal_backward_workspace_size(p) bytes, 32-byte aligned.
  * Every gradient row is summed in a fixed order, without atomics: equal calls
  * give equal bits. block_size and topk in p must be valid but do not change the

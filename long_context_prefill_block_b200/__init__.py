@@ -505,7 +505,8 @@ def dense_causal_backward(q, k, v, cu_seqlens, out, lse, dout, max_seqlen=None,
     """Gradients of sum(dout * out) through dense causal attention: (dq [T,Hq,d], dk, dv
     [T,Hkv,d]) in the inputs' type, summed in fp32 and rounded once. out, lse: what
     dense_causal_forward(..., return_lse=True) returned. Rows that no sequence owns, or that stand
-    in a sequence longer than max_seqlen (skipped, and recorded in the status word), get zeros.
+    in a sequence that is skipped (longer than max_seqlen, or by offsets on the device past the
+    T rows; recorded in the status word), get zeros.
     The sums have a fixed order: equal calls give equal bits."""
     _check_qkv(q, k, v, out)
     _check_cu(cu_seqlens, q.shape[0])

@@ -166,8 +166,8 @@ __device__ __forceinline__ int find_request_warp(const int32_t* __restrict__ cu,
 // Place x of a launch over the tiles (of ROWS rows) of every sequence, for each
 // of `heads` heads: tile_slots() x heads places. Every sequence has `slots` of
 // them a head, at least as many as tiles, and takes rest in [0, slots * heads).
-// By whole warps. slots == 0: no such place, or a sequence whose length is not in
-// [0, max_seqlen] (which is for the caller to report).
+// By whole warps. slots == 0: no such place, or a sequence that has_place() says no
+// to (which is for the caller to report).
 //
 // Lengths that are about even: each sequence has as many slots as the longest one
 // may have tiles, and the place follows from x. Else, when those would be over
@@ -178,6 +178,10 @@ __device__ __forceinline__ int find_request_warp(const int32_t* __restrict__ cu,
 struct TilePlace {
   int start, len, slots, rest;
 };
+// A sequence of a length in [0, max_seqlen] whose rows are all among the call's.
+__device__ __forceinline__ bool has_place(const Dims& dm, int start, int end) {
+  return start >= 0 && end >= start && end <= dm.T && end - start <= dm.max_seqlen;
+}
 template <int ROWS>
 __host__ __device__ inline bool even_lengths(const Dims& dm) {
   return ((int64_t)dm.max_seqlen + ROWS - 1) / ROWS * dm.batch <=
@@ -219,9 +223,9 @@ __device__ __forceinline__ TilePlace find_tile(const Dims& dm, const int32_t* __
     rest = x - base * heads;
     if (rest < 0 || rest >= slots * heads) return {0, 0, 0, 0};  // offsets that fall
   }
-  const int start = cu[b], len = cu[b + 1] - start;
-  if (len < 0 || len > dm.max_seqlen) return {0, 0, 0, 0};
-  return {start, len, slots, rest};
+  const int start = cu[b], end = cu[b + 1];
+  if (!has_place(dm, start, end)) return {0, 0, 0, 0};
+  return {start, end - start, slots, rest};
 }
 
 // Request r and cache position of row i of a call on a paged cache: request

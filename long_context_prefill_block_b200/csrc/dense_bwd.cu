@@ -29,7 +29,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // stat[0][h][t] = lse * log2(e), stat[1][h][t] = D = dO . out, laid out head
 // by head so that a tile of one head's queries reads contiguous floats. Also
 // writes the gradients of rows that no sequence owns (a padded batch) or that
-// stand in a sequence longer than max_seqlen, which is skipped: zeros.
+// stand in a sequence that is skipped (longer than max_seqlen, or with rows that
+// are not all among the call's): zeros.
 // One CTA: 32 tokens of one head; 16 bytes of a row per lane.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
@@ -45,9 +46,8 @@ dense_bwd_stat_kernel(Dims dm, const T* __restrict__ out, const T* __restrict__ 
   tc::grid_let_next();
   const int h = blockIdx.y, t0 = blockIdx.x * 32;
   if (h == 0 && t0 == 0) {  // every sequence, those that get no tile too
-    int64_t start;
-    int len;
-    for (int b = threadIdx.x; b < dm.batch; b += kThreads) seq_bounds(dm, cu, b, start, len, status);
+    for (int b = threadIdx.x; b < dm.batch; b += kThreads)
+      if (!has_place(dm, cu[b], cu[b + 1])) set_status(status, kStInvalidArg);
   }
   const int sub = threadIdx.x % LPR, rr = threadIdx.x / LPR;
   for (int r = rr; r < 32; r += RPS) {
@@ -73,7 +73,7 @@ dense_bwd_stat_kernel(Dims dm, const T* __restrict__ out, const T* __restrict__ 
       stat[(int64_t)h * dm.T + t] = lse[(int64_t)t * dm.Hq + h] * kLog2e;
       stat[((int64_t)dm.Hq + h) * dm.T + t] = ds[threadIdx.x];
       const int b = find_request(cu, dm.batch, t);
-      mine = b < dm.batch && t >= cu[b] && cu[b + 1] - cu[b] <= dm.max_seqlen;
+      mine = b < dm.batch && t >= cu[b] && has_place(dm, cu[b], cu[b + 1]);
     }
     owned[threadIdx.x] = mine;
   }

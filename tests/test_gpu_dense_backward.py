@@ -231,3 +231,27 @@ def _autograd_dense(q, k, v, cu):
         s = s.masked_fill(torch.ones(e - a, e - a, dtype=torch.bool).triu(1), float("-inf"))
         res.append(torch.einsum("hij,jhd->ihd", torch.softmax(s, -1), v[a:e]))
     return torch.cat(res)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens", [(150, 333), (700, 5, 5, 5, 40)])  # places that follow, that are searched
+def test_offsets_on_the_device_past_the_rows_are_reported_and_skipped(lens, dtype):
+    q, k, v, do, cu = case(lens, 4, 2, 64, dtype, seed=8)
+    out, lse, want = run(q, k, v, do, cu)
+    a = [x.to(DEV) for x in (q, k, v, do)]
+    last, T = int(cu[-2]), int(cu[-1])
+    for bad in (T + 100, T + 1, 2 ** 31 - 1):
+        c = cu.clone()
+        c[-1] = bad
+        got = moba.dense_causal_backward(*a[:3], c.to(DEV), out, lse, a[3], max_seqlen=max(lens) + 100)
+        assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG
+        for x, y in zip(got, want):  # another bound, another order of sums: see above
+            assert ref.off(x[:last], y[:last].double().cpu()) <= 2 * TOL[dtype]
+            assert not x[last:].any()
+    c = cu.clone()
+    c[0] = -3
+    got = moba.dense_causal_backward(*a[:3], c.to(DEV), out, lse, a[3], max_seqlen=max(lens) + 100)
+    assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG
+    for x, y in zip(got, want):
+        assert ref.off(x[lens[0]:], y[lens[0]:].double().cpu()) <= 2 * TOL[dtype]
+        assert not x[:lens[0]].any()
