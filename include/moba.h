@@ -313,10 +313,10 @@ MOBA_API moba_status dense_causal_backward(const moba_params* p, const void* q, 
  * append), and request r's rows cu[r] .. cu[r+1]-1 stand at its last
  * positions. Rows at or past cu[batch] (a padded batch) are left alone. A
  * request with more rows than positions, with rows that are not all among the
- * call's, or longer than p->max_seqlen or its max_pages pages, is skipped and
- * records MOBA_ERR_INVALID_ARG in the status word; a table entry that names no
- * page is skipped and records MOBA_ERR_BAD_INDICES. Page table entries behind a
- * request's length are not read. */
+ * call's, or longer than p->max_seqlen, its max_pages pages or 2^31 - 4096
+ * positions, is skipped and records MOBA_ERR_INVALID_ARG in the status word; a
+ * table entry that names no page is skipped and records MOBA_ERR_BAD_INDICES.
+ * Page table entries behind a request's length are not read. */
 typedef struct {
   int num_pages;
   int page_size;   /* a power of two, 16 .. 65536 */

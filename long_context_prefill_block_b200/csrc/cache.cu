@@ -114,13 +114,6 @@ __device__ __forceinline__ int64_t cache_row(const Cache& c, int Hkv, int r, int
   return row + (pos & ((1 << c.page_log2) - 1));
 }
 
-// Positions a request can have: what its pages hold, and what the caller's
-// max_seqlen allows.
-__device__ __forceinline__ int max_positions(const Dims& dm, const Cache& c) {
-  const int64_t held = (int64_t)c.max_pages << c.page_log2;
-  return held < dm.max_seqlen ? (int)held : dm.max_seqlen;
-}
-
 // Warp of a write or read: head and tokens it takes. blockIdx.y: K or V.
 // A warp takes `tpw` consecutive tokens of one head, so that their rows are
 // neighbours in a page; lane t looks token t's row up (-1: none) while the

@@ -263,6 +263,15 @@ struct Cache {
   int pages, page_log2, max_pages;
 };
 
+// Positions a request can have: what its pages hold and what the caller's
+// max_seqlen allows, up to 2^31 - 4096: kernels step past a request's end by up to
+// 2048 positions before they compare, in 32 bits.
+__host__ __device__ __forceinline__ int max_positions(const Dims& dm, const Cache& c) {
+  const int64_t held = (int64_t)c.max_pages << c.page_log2;
+  const int most = dm.max_seqlen < INT32_MAX - 4095 ? dm.max_seqlen : INT32_MAX - 4095;
+  return held < most ? (int)held : most;
+}
+
 // Row index of page slot `page` (an entry of the table) for kv head g, or -1
 // for an entry that names no page.
 __device__ __forceinline__ int64_t cache_page_row(const Cache& c, int Hkv, int page, int g) {

@@ -108,8 +108,12 @@ __device__ __forceinline__ void slot_range(const Step& a, const int32_t* list, i
   const int e = slot == a.sp.own ? own : list[slot];
   lo = hi = 0;
   if (slot == a.sp.own || (e >= 0 && e < own)) {
-    lo = e * B + x % a.sp.parts * a.sp.keys;
-    hi = min(lo + a.sp.keys, e < own ? (e + 1) * B : p + 1);
+    // counted inside the block: where its last parts would begin need not be a position
+    const int n = e < own ? B : p - own * B + 1, from = x % a.sp.parts * a.sp.keys;
+    if (from < n) {
+      lo = e * B + from;
+      hi = lo + min(a.sp.keys, n - from);
+    }
   }
 }
 
@@ -1124,7 +1128,6 @@ size_t decode_cache_partial_rows(const Dims& dm) {
 cudaError_t launch_decode_cache(const Dims& dm, const Cache& c, const void* q, const float* kbar,
                                 const int32_t* cu_q, int32_t* idx, float* part_o, float* part_lse,
                                 void* out, float* lse, int* status, cudaStream_t st) {
-  const int64_t held = (int64_t)c.max_pages << c.page_log2;
   Step a{};
   a.dm = dm;
   a.c = c;
@@ -1135,7 +1138,7 @@ cudaError_t launch_decode_cache(const Dims& dm, const Cache& c, const void* q, c
   a.gated = dm.nb > kOwnGate && dm.topk > 1;
   a.part_o = part_o;
   a.part_lse = part_lse;
-  a.max_len = held < dm.max_seqlen ? (int)held : dm.max_seqlen;
+  a.max_len = max_positions(dm, c);
   a.status = status;
   if (dm.dtype == kBF16)
     return dm.d == 128 ? run<__nv_bfloat16, 128>(a, q, out, lse, st)

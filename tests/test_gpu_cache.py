@@ -565,3 +565,35 @@ def test_decode_offsets_past_the_queries_are_reported_and_skipped(B, dtype):
     moba.moba_decode_cache(q, pool.cache, pool.table, i32(lens), i32([-1, 2, 4]), *args, out=out)
     assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG
     assert torch.equal(out[2:], want[2:]) and (out[:2] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_block_that_would_end_past_two_to_the_31(dtype):
+    """Blocks of 1.2e9 positions, the query in the second one: most parts of its block lie past the
+    largest position. Every page of the table is the same one, so a row counts as often as it is
+    named: its logit plus the logarithm of that. (49 parts hold keys: the sums are as long as the
+    tolerance says.)"""
+    B, page, d, more = 1_200_000_000, 65536, 64, 100_000
+    L = B + more
+    pool = Pool([page], page, 1, d, spare=0)
+    g = torch.Generator().manual_seed(2)
+    k, v = ((torch.randn(page, 1, d, generator=g) * 0.7).to(DEV) for _ in range(2))
+    moba.moba_cache_write(pool.cache, k, v, pool.table, i32([page]), offsets([page]))
+    keys, values = contents(pool, 0, page)
+    q = (torch.randn(1, 2, d, generator=g) * 0.7).to(dtype).to(DEV)
+    table = torch.zeros(1, -(-L // page), dtype=torch.int32, device=DEV)
+    out, lse = moba.moba_decode_cache(q, pool.cache, table, i32([L]), offsets([1]),
+                                      torch.zeros(1, 2, 1, d, device=DEV), B, 1, return_lse=True)
+    assert moba.moba_device_status() == 0
+    times = torch.bincount(torch.arange(B, L) % page, minlength=page).double()
+    for h in range(2):
+        z = keys[:, 0] @ q[0, h].double().cpu() / d ** 0.5 + times.log()
+        want = torch.logsumexp(z, 0)
+        assert abs(float(lse[0, h]) - float(want)) <= LSE_TOL
+        assert ref.off(out[0, h], torch.exp(z - want) @ values[:, 0]) <= TOL[dtype]
+    # longer than any position may be
+    long = torch.zeros(1, 1 << 15, dtype=torch.int32, device=DEV)
+    mine = torch.full_like(q, 9.0)
+    moba.moba_decode_cache(q, pool.cache, long, i32([2 ** 31 - 4095]), offsets([1]),
+                           torch.zeros(1, 2, 1, d, device=DEV), B, 1, out=mine)
+    assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG and (mine == 9).all()
