@@ -592,7 +592,10 @@ def _check_kbar(kbar, batch: int, heads: int, head_dim: int, block_size: int) ->
         raise ValueError(f"kbar must be float32 [{batch}, num_blocks, {heads}, {head_dim}]")
     if block_size < 1:
         raise ValueError("block_size must be at least 1")
-    return min(shape[1] * block_size, 2**31 - 1)
+    longest = min(shape[1] * block_size, 2**31 - 1)
+    if -(-longest // block_size) != shape[1]:  # the kernels would step through it by fewer blocks
+        raise ValueError(f"kbar has {shape[1]} blocks of {block_size}: more than there are positions")
+    return longest
 
 
 def moba_cache_write(cache: MobaCache, k, v, page_table, seqlens, cu_new,

@@ -191,3 +191,13 @@ def test_entry_points_refuse_bad_pointers_workspaces_and_variants():
     empty = ctypes.byref(_params(total_tokens=0))
     assert dec(empty, None, None, None, None, None, None, None, None, Z(0), None) == moba.MOBA_OK
     assert bwd(empty, *([None] * 11), Z(0), None) == moba.MOBA_OK
+
+
+@pytest.mark.parametrize("B,nb", [(65536, 32769), (2 ** 30, 3), (2 ** 31 - 1, 2)])
+def test_means_of_more_blocks_than_positions_are_refused(B, nb):
+    """A length ends at 2^31 - 1, so the kernels count at most that many positions' blocks: with more
+    in kbar, its second request's means would be looked for in the wrong place."""
+    kbar = torch.zeros(3, 1, 2, 64).expand(3, nb, 2, 64)
+    assert moba._check_kbar(kbar[:, :-1], 3, 2, 64, B) == min((nb - 1) * B, 2 ** 31 - 1)
+    with pytest.raises(ValueError, match="more than there are positions"):
+        moba._check_kbar(kbar, 3, 2, 64, B)
