@@ -366,6 +366,19 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const int cs, const int
   }
 }
 
+// The exponent that takes a q row whose largest magnitude is `top` into [1, 2),
+// as far as 2^-e and 2^e are normal numbers; 0 for one that is infinite or zero.
+// A logit is (q 2^-e . codes) (2^e key scale): the sum cannot overflow, and where
+// the large query meets a small scale neither does the factor (q . codes taken
+// first gave infinities for queries of 2^120 on keys of 2^-118).
+__device__ __forceinline__ int q_exponent(float top) {
+  const int e = (int)(__float_as_uint(top) >> 23) - 127;
+  return e == 128 || top == 0.f ? 0 : min(max(e, -126), 126);
+}
+__device__ __forceinline__ float power_of_two(int e) {  // e in [-126, 127]
+  return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
 // ---- bf16 queries ------------------------------------------------------------
 // One CTA per split: of one head for the chosen blocks (each head has its own),
 // of up to 8 heads of a kv head for the own block, which they share, and for
@@ -489,10 +502,9 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    int e = (int)(__float_as_uint(top) >> 23) - 127;
-    e = e == 128 || top == 0.f ? 0 : min(max(e, -126), 126);  // infinite, or nothing to scale
-    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-    qe = __uint_as_float((uint32_t)(127 + e) << 23) * (kLog2e * rsqrtf((float)D));
+    const int e = q_exponent(top);
+    const float f = power_of_two(-e);
+    qe = power_of_two(e) * (kLog2e * rsqrtf((float)D));
 #pragma unroll
     for (int i = 0; i < NC * 8; ++i) {
       const __half2 h = __floats2half2_rn(x[2 * i] * f, x[2 * i + 1] * f);
@@ -661,7 +673,7 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         ev[t][y] = vb == 255 ? NAN : (float)((int)vb - 127);
 #pragma unroll
         for (int z = 0; z < NCOL; ++z)
-          x[t][y][z] = on[t][y] ? sc[2 * y + z] * qc[z] * ks : -INFINITY;
+          x[t][y][z] = on[t][y] ? sc[2 * y + z] * (qc[z] * ks) : -INFINITY;
       }
     }
     // ---- references: raised when a value passes one by 2^8 (the first always does)
@@ -897,10 +909,18 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
     for (int e = tid; e < dm.topk; e += kThreads)
       a.idx[row * dm.topk + e] = a.sp.groups > 0 ? og.list[e] : e == 0 ? p / dm.B : -1;
   const int grp_id = warp * GPW + lane / LPK, sub = lane % LPK;
-  const float sl2 = kLog2e * rsqrtf((float)D);
-  float qv[16];
+  float qv[16], top = 0.f;
 #pragma unroll
-  for (int x = 0; x < 16; ++x) qv[x] = q[row * D + sub * 16 + x] * sl2;
+  for (int x = 0; x < 16; ++x) {
+    qv[x] = q[row * D + sub * 16 + x];
+    top = fmaxf(top, fabsf(qv[x]));
+  }
+#pragma unroll
+  for (int off = LPK / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const int qx = q_exponent(top);
+  const float qe = power_of_two(qx) * (kLog2e * rsqrtf((float)D));
+#pragma unroll
+  for (int x = 0; x < 16; ++x) qv[x] *= power_of_two(-qx);
   float m = -INFINITY, l = 0.f, o[16];
 #pragma unroll
   for (int x = 0; x < 16; ++x) o[x] = 0.f;
@@ -940,7 +960,7 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
       for (int i = 0; i < 16; ++i) acc = fmaf(qv[i], x[i], acc);
 #pragma unroll
       for (int off = LPK / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-      d[u] = on[u] ? acc * ks[u] : -INFINITY;
+      d[u] = on[u] ? acc * (qe * ks[u]) : -INFINITY;
       mn = fmaxf(mn, d[u]);
     }
     if (mn == -INFINITY) {

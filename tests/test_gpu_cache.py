@@ -597,3 +597,23 @@ def test_a_block_that_would_end_past_two_to_the_31(dtype):
     moba.moba_decode_cache(q, pool.cache, long, i32([2 ** 31 - 4095]), offsets([1]),
                            torch.zeros(1, 2, 1, d, device=DEV), B, 1, out=mine)
     assert moba.moba_device_status() == moba.MOBA_ERR_INVALID_ARG and (mine == 9).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B", [64, 4])  # choice inside each split, and in a launch of its own
+def test_queries_near_the_largest_number(B, dtype):
+    """Queries of 2^120 and keys 2^118 times smaller than usual give ordinary logits (of up to about
+    16, so that a product without the key's scale passes 2^128): powers of two, as above."""
+    lens = [300]
+    pool, kbar = filled(lens, 2, 128, 32, B, seed=8)
+    q = (4 * torch.randn(1, 4, 128, generator=torch.Generator().manual_seed(3))).to(dtype).to(DEV)
+    args = (pool.table, i32(lens), offsets([1]))
+    kw = dict(return_lse=True, return_idx=True)
+    a = moba.moba_decode_cache(q, pool.cache, *args, kbar, B, 5, **kw)
+    keys = contents(pool, 0, 300)[0]
+    assert (torch.einsum("hd,lgd->hlg", q[0].double().cpu(), keys).abs().max() / 128 ** 0.5) > 8
+    pool.cache.k_scale.view(torch.uint8).sub_(118)
+    b = moba.moba_decode_cache(q * 2.0 ** 118, pool.cache, *args, kbar * 2.0 ** -118, B, 5, **kw)
+    assert torch.isfinite(b[0]).all() and torch.equal(a[2], b[2])
+    assert ref.off(b[0], a[0].double().cpu()) <= TOL[dtype]
+    assert (a[1] - b[1]).abs().max() <= LSE_TOL
