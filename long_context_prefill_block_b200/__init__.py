@@ -650,8 +650,8 @@ def moba_decode_cache(q, cache: MobaCache, page_table, seqlens, cu_q, kbar, bloc
                       ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
     """moba_decode over a MobaCache: request r's queries (rows cu_q[r] .. cu_q[r+1]-1 of q
     [n, Hq, d]) stand at its last positions; kbar [batch, num_blocks, Hkv, d]: the block means
-    that moba_cache_write keeps. max_seqlen, a bound on the lengths, must have kbar's number of
-    blocks. Rows behind cu_q[batch] are not written: a given out keeps them, fresh results hold
+    that moba_cache_write keeps. max_seqlen, a bound on the lengths (default: what kbar has blocks
+    for), must have kbar's number of blocks. Rows behind cu_q[batch] are not written: a given out keeps them, fresh results hold
     nothing defined there. Returns out [n, Hq, d] (and lse [n, Hq], idx [n, Hq, topk])."""
     if q.dim() != 3 or cache.k.dim() != 4 or q.shape[2] != cache.k.shape[3]:
         raise ValueError("q must be [n, Hq, d] with the cache's head dim")
@@ -665,7 +665,11 @@ def moba_decode_cache(q, cache: MobaCache, page_table, seqlens, cu_q, kbar, bloc
     batch = page_table.shape[0]
     longest = _check_kbar(kbar, batch, hkv, d, block_size)
     if max_seqlen is None:
-        max_seqlen = longest
+        # no longer than the pages hold, as far as that leaves kbar its blocks; a caller's workspace
+        # was sized for kbar's length
+        held = page_table.shape[1] * cache.k.shape[2]
+        least = (kbar.shape[1] - 1) * block_size + 1
+        max_seqlen = min(longest, max(held, least)) if ws is None else longest
     elif -(-max_seqlen // block_size) != kbar.shape[1]:
         raise ValueError(f"max_seqlen {max_seqlen} has not the {kbar.shape[1]} blocks of kbar")
     dev = q.device

@@ -53,23 +53,25 @@ struct Split {
 // also need no merge). No slots for blocks that cannot exist: 8 requests of 778
 // tokens, four queries, blocks of 2048, topk 3: 33 us with them, 17.5 without.
 // fp32 queries have a CTA per q head with shared routing too (40 on 8 heads, eight
-// of 282 blocks: 101 us when counted by kv heads, 40). The rule asks for the
-// call's sizes alone, so that the workspace does not depend on the device that is
-// current.
+// of 282 blocks: 101 us when counted by kv heads, 40). No parts of a block behind
+// max_seqlen either: 4 requests of 200 tokens with blocks of 4096 had 32 a row, two
+// of them with keys. The rule asks for the call's sizes alone, so that the workspace
+// does not depend on the device that is current.
 Split split_of(const Dims& dm) {
+  const int64_t B = dm.B < dm.max_seqlen ? dm.B : dm.max_seqlen > 1 ? dm.max_seqlen : 1;
   // fp32 queries have a CTA per q head in either case
   const int64_t units = (int64_t)dm.T * (dm.shared && dm.dtype == kBF16 ? dm.Hkv : dm.Hq);
   const int64_t least = 2 * kSMs;
   const int k = dm.nb < 1 ? 1 : dm.topk < dm.nb ? dm.topk : dm.nb;
   const int listed = dm.shared ? k : k - 1;
   Split s{128, 1, 1, k - 1, 0, 0};
-  while (s.keys < kMaxKeys && s.keys < dm.B &&
-         units * k * (((int64_t)dm.B + 2 * s.keys - 1) / (2 * s.keys)) >= 2 * least)
+  while (s.keys < kMaxKeys && s.keys < B &&
+         units * k * ((B + 2 * s.keys - 1) / (2 * s.keys)) >= 2 * least)
     s.keys *= 2;
-  if (s.keys > dm.B) s.keys = dm.B;
-  s.parts = (int)(((int64_t)dm.B + s.keys - 1) / s.keys);
+  if (s.keys > B) s.keys = (int)B;
+  s.parts = (int)((B + s.keys - 1) / s.keys);
   if (s.parts == 1)
-    while (s.slots < kMaxSlots && s.slots < listed && (s.slots + 1) * (int64_t)dm.B <= kMaxKeys &&
+    while (s.slots < kMaxSlots && s.slots < listed && (s.slots + 1) * B <= kMaxKeys &&
            units * ((listed + s.slots) / (s.slots + 1)) >= least)
       ++s.slots;
   s.groups = listed > 0 ? (listed + s.slots - 1) / s.slots : 0;

@@ -617,3 +617,25 @@ def test_queries_near_the_largest_number(B, dtype):
     assert torch.isfinite(b[0]).all() and torch.equal(a[2], b[2])
     assert ref.off(b[0], a[0].double().cpu()) <= TOL[dtype]
     assert (a[1] - b[1]).abs().max() <= LSE_TOL
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("bound", [None, 200])
+def test_blocks_far_longer_than_any_request(bound, shared, dtype):
+    """A block that is never completed: the parts that a row's keys are divided into follow the
+    lengths there can be (max_seqlen, or what the pages hold), not the block size."""
+    lens, nq, B = [200, 1, 130], [1, 1, 2], 1 << 30
+    pool, kbar = filled(lens, 2, 128, 16, B, seed=4)
+    assert kbar.shape[1] == 1
+    q = (torch.randn(4, 8, 128, generator=torch.Generator().manual_seed(1)) * 0.7).to(dtype).to(DEV)
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    got = moba.moba_decode_cache(q, pool.cache, pool.table, i32(lens), offsets(nq), kbar, B, 2,
+                                 max_seqlen=bound, shared_routing=shared, return_lse=True,
+                                 return_idx=True)
+    # partials of 32 rows in two parts, 129 floats each, and the results
+    assert torch.cuda.max_memory_allocated() - held < 1 << 20
+    assert moba.moba_device_status() == 0
+    check_decode(q, pool, lens, nq, B, 2, shared, *got)

@@ -201,3 +201,17 @@ def test_means_of_more_blocks_than_positions_are_refused(B, nb):
     assert moba._check_kbar(kbar[:, :-1], 3, 2, 64, B) == min((nb - 1) * B, 2 ** 31 - 1)
     with pytest.raises(ValueError, match="more than there are positions"):
         moba._check_kbar(kbar, 3, 2, 64, B)
+
+
+@pytest.mark.parametrize("dtype", [moba.MOBA_BF16, moba.MOBA_F32])
+@pytest.mark.parametrize("length", [1, 200, 5000])
+@pytest.mark.parametrize("B", [8192, 1 << 20, 1 << 30])
+def test_decode_workspace_is_bounded_by_the_length(B, length, dtype):
+    """Blocks longer than any request: one part at least 128 keys long each, so no more partials a
+    row than ceil(length / 128), whatever the block size."""
+    size = moba.lib().moba_decode_cache_workspace_size
+    size.argtypes, size.restype = None, ctypes.c_size_t
+    rows = 4 * 8 * -(-length // 128)
+    p = _params(batch=4, total_tokens=4, max_seqlen=length, num_q_heads=8, num_kv_heads=8,
+                block_size=B, topk=1, dtype=dtype)
+    assert 0 < size(ctypes.byref(p)) <= rows * 65 * 4 + 4 * 8 * 4 + 3 * 256
