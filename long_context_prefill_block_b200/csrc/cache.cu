@@ -105,13 +105,15 @@ __device__ __forceinline__ void decode16(const uint4& r, float (&x)[16]) {
 // (and a status code) where the page table names no page.
 __device__ __forceinline__ int64_t cache_row(const Cache& c, int Hkv, int r, int pos, int g,
                                              int* status) {
+  if (!MOBA_CHECK(pos >= 0 && (pos >> c.page_log2) < c.max_pages, status)) return -1;
   const int page = c.table[(int64_t)r * c.max_pages + (pos >> c.page_log2)];
-  const int64_t row = cache_page_row(c, Hkv, page, g);
-  if (row < 0) {
+  const int64_t first = cache_page_row(c, Hkv, page, g);
+  if (first < 0) {
     set_status(status, kStBadIndices);
     return -1;
   }
-  return row + (pos & ((1 << c.page_log2) - 1));
+  const int64_t row = first + (pos & ((1 << c.page_log2) - 1));
+  return MOBA_CHECK(cache_holds(c, Hkv, row), status) ? row : -1;
 }
 
 // Warp of a write or read: head and tokens it takes. blockIdx.y: K or V.
@@ -235,7 +237,7 @@ cache_write_kernel(Dims dm, Cache c, const T* __restrict__ k, const T* __restric
 #pragma unroll
       for (int i = 0; i < VEC; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
     float* dst = sums + ((int64_t)(p.t0 / 32) * dm.Hkv + p.g) * D + sub * VEC;
-    if (sel == 0) {
+    if (sel == 0 && MOBA_CHECK(p.t0 / 32 < (dm.T + 31) / 32, status)) {
 #pragma unroll
       for (int i = 0; i < VEC; i += 4)
         *reinterpret_cast<float4*>(dst + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
@@ -313,6 +315,7 @@ cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
   if (sums && last > begin) {
     g0 = (row0 + max(first, begin) - begin + 31) / 32;
     g1 = (row0 + last - begin) / 32;
+    if (!MOBA_CHECK(g0 >= 0 && g1 <= (dm.T + 31) / 32, status)) g0 = g1 = 0;
     if (g1 > g0) {
       lo = begin + g0 * 32 - row0;
       hi = begin + g1 * 32 - row0;
@@ -326,6 +329,7 @@ cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
       const int c1 = min(c0 + 2048, to), p0 = c0 >> c.page_log2;
       __syncthreads();
       for (int i = threadIdx.x; i <= ((c1 - 1) >> c.page_log2) - p0; i += kMeanThreads) {
+        if (!MOBA_CHECK(i < kMeanPages && p0 + i < c.max_pages, status)) break;
         const int64_t row =
             cache_page_row(c, dm.Hkv, c.table[(int64_t)r * c.max_pages + p0 + i], g);
         page_row[i] = (int)row;
@@ -341,7 +345,7 @@ cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
           const int pr = j < c1 ? page_row[(j >> c.page_log2) - p0] : -1;
           w[u] = make_uint4(0, 0, 0, 0);
           s[u] = 0.f;
-          if (pr >= 0) {
+          if (pr >= 0 && MOBA_CHECK(cache_holds(c, dm.Hkv, pr + (j & mask)), status)) {
             const int64_t row = pr + (j & mask);
             w[u] = *reinterpret_cast<const uint4*>(c.k + row * D + sub * 16);
             s[u] = e8m0_value(c.ks[row]);
@@ -382,7 +386,7 @@ cache_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
     tc::store_first(&part[rank][x], t);
   }
   tc::cluster_sync();
-  if (rank != 0) return;
+  if (rank != 0 || !MOBA_CHECK(r < dm.batch && blk < dm.nb, status)) return;
   for (int x = threadIdx.x; x < D; x += kMeanThreads) {
     float t = 0.f;
     for (int i = 0; i < cs; ++i) t += part[i][x];
@@ -415,7 +419,8 @@ cache_small_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
   // the block's pages, at most 17: lane x looks page x up
   int pages = -1;
   const int p0 = first >> c.page_log2;
-  if (blk >= 0 && lane <= ((last - 1) >> c.page_log2) - p0) {
+  if (blk >= 0 && lane <= ((last - 1) >> c.page_log2) - p0 &&
+      MOBA_CHECK(p0 + lane < c.max_pages, status)) {
     const int64_t row =
         cache_page_row(c, dm.Hkv, c.table[(int64_t)at.r * c.max_pages + p0 + lane], g);
     pages = (int)row;
@@ -428,6 +433,7 @@ cache_small_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
   if (sums && last > at.begin) {
     g0 = (at.row0 + max(first, at.begin) - at.begin + 31) / 32;
     g1 = (at.row0 + last - at.begin) / 32;
+    if (!MOBA_CHECK(g0 >= 0 && g1 <= (dm.T + 31) / 32, status)) g0 = g1 = 0;
     if (g1 > g0) {
       lo = at.begin + g0 * 32 - at.row0;
       hi = at.begin + g1 * 32 - at.row0;
@@ -464,7 +470,7 @@ cache_small_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
         const int pr = __shfl_sync(0xffffffffu, pages, ((j >> c.page_log2) - p0) & 31);
         q[u] = make_uint4(0, 0, 0, 0);
         s[u] = 0.f;
-        if (x < rest && pr >= 0) {
+        if (x < rest && pr >= 0 && MOBA_CHECK(cache_holds(c, dm.Hkv, pr + (j & mask)), status)) {
           const int64_t row = pr + (j & mask);
           q[u] = *reinterpret_cast<const uint4*>(c.k + row * D + sub * 16);
           s[u] = e8m0_value(c.ks[row]);
@@ -487,7 +493,7 @@ cache_small_means_kernel(Dims dm, Cache c, const int32_t* __restrict__ cu_new,
       if (ss % 4 == e / 4) t[e % 4] += v;
     }
   }
-  if (sg == 0) {
+  if (sg == 0 && MOBA_CHECK(at.r < dm.batch && blk < dm.nb, status)) {
     float* o = kbar + (((int64_t)at.r * dm.nb + blk) * dm.Hkv + g) * D + ss * 4;
     const float n = (float)B;
     *reinterpret_cast<float4*>(o) = make_float4(t[0] / n, t[1] / n, t[2] / n, t[3] / n);

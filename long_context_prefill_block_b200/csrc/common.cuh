@@ -279,6 +279,11 @@ __device__ __forceinline__ int64_t cache_page_row(const Cache& c, int Hkv, int p
   return ((int64_t)page * Hkv + g) << c.page_log2;
 }
 
+// Whether a row index is one of the cache's (for the checked build).
+__device__ __forceinline__ bool cache_holds(const Cache& c, int Hkv, int64_t row) {
+  return row >= 0 && row < ((int64_t)c.pages * Hkv) << c.page_log2;
+}
+
 // The value of a scale byte.
 __device__ __forceinline__ float e8m0_value(uint32_t b) {
   return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);

@@ -107,8 +107,9 @@ __device__ __forceinline__ void split_slots(const Step& a, int x, int& first, in
 __device__ __forceinline__ void slot_range(const Step& a, const int32_t* list, int x, int slot,
                                            int p, int& lo, int& hi) {
   const int B = a.dm.B, own = p / B;
-  const int e = slot == a.sp.own ? own : list[slot];
   lo = hi = 0;
+  if (!MOBA_CHECK(slot <= a.sp.own && a.sp.own < a.dm.topk, a.status)) return;
+  const int e = slot == a.sp.own ? own : list[slot];
   if (slot == a.sp.own || (e >= 0 && e < own)) {
     // counted inside the block: where its last parts would begin need not be a position
     const int n = e < own ? B : p - own * B + 1, from = x % a.sp.parts * a.sp.keys;
@@ -120,13 +121,14 @@ __device__ __forceinline__ void slot_range(const Step& a, const int32_t* list, i
 }
 
 // First rows of the pages that hold keys [lo, hi) of request r, kv head g: -1
-// (and a status code) where the table names no page.
+// (and a status code) where the table names no page. room: entries of page_row.
 template <int kThreads>
 __device__ __forceinline__ void load_pages(const Step& a, int r, int g, int lo, int hi,
-                                           int* page_row) {
+                                           int* page_row, int room) {
   const Cache& c = a.c;
   const int p0 = lo >> c.page_log2, np = lo < hi ? ((hi - 1) >> c.page_log2) - p0 + 1 : 0;
   for (int i = threadIdx.x; i < np; i += kThreads) {
+    if (!MOBA_CHECK(i < room && p0 + i < c.max_pages, a.status)) break;
     const int64_t row =
         cache_page_row(c, a.dm.Hkv, c.table[(int64_t)r * c.max_pages + p0 + i], g);
     page_row[i] = (int)row;  // rows of a cache fit 31 bits (checked on the host)
@@ -167,7 +169,9 @@ __device__ __forceinline__ void choose_blocks(const Step& a, const T* __restrict
                                               int h0, int n, int p, float* qs, OwnGate& og) {
   const Dims& dm = a.dm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = h0 / (dm.Hq / dm.Hkv), c = p / dm.B, need = min(dm.topk - 1, c);
+  const int g = h0 / (dm.Hq / dm.Hkv), c = p / dm.B;
+  int need = min(dm.topk - 1, c);
+  if (need > 0 && !MOBA_CHECK(c <= kOwnGate && c < dm.nb && r < dm.batch, a.status)) need = 0;
   for (int x = tid; x < D; x += kThreads) {
     float s = 0.f;
     for (int j = 0; j < n; ++j) s += to_f32(q[((int64_t)qi * dm.Hq + h0 + j) * D + x]);
@@ -259,6 +263,7 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const int cs, const int
                      true))
     return;
   const int c = p / dm.B, need = min(dm.topk - 1, c);
+  if (!MOBA_CHECK(c < dm.nb && rows * c <= kGateScores && r < dm.batch, a.status)) return;
   auto sync = [&] {
     if (cs == 1)
       __syncthreads();
@@ -560,7 +565,8 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   }
   const int n_steps = __shfl_sync(0xffffffffu, my_step, kMaxSlots - 1);
   if (n_steps == 0) {  // no keys (uniform over the CTA; never the only split of a row)
-    if (tid < nh) a.part_lse[(row0 + tid) * a.sp.per_row + s] = -INFINITY;
+    if (tid < nh && MOBA_CHECK(row0 + tid < (int64_t)dm.T * dm.Hq && s < a.sp.per_row, a.status))
+      a.part_lse[(row0 + tid) * a.sp.per_row + s] = -INFINITY;
     return;
   }
   // A walk over the steps: the slot of the current one.
@@ -578,7 +584,8 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   Walk wr, wc;  // of the requests, of the computation
   enter(wr, 0);
   for (int x = 0;; enter(wr, ++x)) {
-    load_pages<kW * 32>(a, r, g, wr.lo & ~15, wr.hi, page_row + wr.page + (wr.lo >> cc.page_log2));
+    const int at = wr.page + (wr.lo >> cc.page_log2);
+    load_pages<kW * 32>(a, r, g, wr.lo & ~15, wr.hi, page_row + at, kMaxPages - at);
     if (wr.end == n_steps) break;
   }
   enter(wr, 0);
@@ -593,8 +600,8 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   // the cache row that 16 keys from pos begin at, or -1: nothing to read
   auto tile_row = [&](const Walk& w, int pos) {
     if (pos >= w.hi) return -1;
-    const int pr = page_row[w.page + (pos >> cc.page_log2)];
-    return pr < 0 ? -1 : pr + (pos & (page - 1));
+    const int pr = page_row[w.page + (pos >> cc.page_log2)], row = pr + (pos & (page - 1));
+    return pr < 0 || !MOBA_CHECK(cache_holds(cc, dm.Hkv, (int64_t)row + 15), a.status) ? -1 : row;
   };
   // the loads of step i, one lane a copy: tile lane / 4, then K, V and their scales
   auto request = [&](int i, int st) {
@@ -826,6 +833,7 @@ cache_attn_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   if (*abort) return;
   for (int e = tid; e < nh * (D / 4); e += kW * 32) {
     const int h = e / (D / 4), d4 = e % (D / 4);
+    if (!MOBA_CHECK(row0 + h < (int64_t)dm.T * dm.Hq && s < a.sp.per_row, a.status)) break;
     float M = -INFINITY, L = 0.f;
 #pragma unroll
     for (int w = 0; w < kW; ++w) M = fmaxf(M, wm[w][h]);
@@ -907,6 +915,7 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
                                       &wo[0][0], og);
     list = og.list;
   }
+  if (!MOBA_CHECK(prow < (int64_t)dm.T * dm.Hq * S, a.status)) return;
   if (!a.gated && s == 0)
     for (int e = tid; e < dm.topk; e += kThreads)
       a.idx[row * dm.topk + e] = a.sp.groups > 0 ? og.list[e] : e == 0 ? p / dm.B : -1;
@@ -934,7 +943,7 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
   slot_range(a, list, s, slot, p, lo, hi);
   const int p0 = lo >> c.page_log2;
   __syncthreads();
-  load_pages<kThreads>(a, r, g, lo, hi, page_row);
+  load_pages<kThreads>(a, r, g, lo, hi, page_row, kMaxPages);
   __syncthreads();
   for (int base = lo; base < hi; base += U * G) {
     uint4 kr[U], vr[U];
@@ -945,8 +954,9 @@ cache_attn_kernel(const Step a, const float* __restrict__ q) {
       const int j = base + grp_id + u * G;
       const int jj = j < hi ? j : lo;
       const int pr = page_row[(jj >> c.page_log2) - p0];
-      on[u] = j < hi && pr >= 0;
-      const int64_t at = pr < 0 ? 0 : pr + (jj & mask);
+      const bool there = pr >= 0 && MOBA_CHECK(cache_holds(c, dm.Hkv, pr + (jj & mask)), a.status);
+      on[u] = j < hi && there;
+      const int64_t at = there ? pr + (jj & mask) : 0;
       kr[u] = __ldg(reinterpret_cast<const uint4*>(c.k + at * D + sub * 16));
       vr[u] = __ldg(reinterpret_cast<const uint4*>(c.v + at * D + sub * 16));
       ks[u] = e8m0_value(__ldg(c.ks + at));

@@ -49,3 +49,21 @@ def test_shared_arrays_read_in_16_bytes_are_aligned_to_them(name):
     for statement in re.findall(r"__shared__ ([^;]*);", text):
         names = set(re.findall(r"\b(\w+)\s*\[", statement)) & wide
         assert not names or "__align__" in statement, names
+
+
+# accesses that the bounds-checked build is tested to keep inside, by the limits their checks name
+CHECKED = {
+    "cache.cu": [r"c\.max_pages", r"kMeanPages", r"\(dm\.T \+ 31\) / 32", r"dm\.nb", r"dm\.batch",
+                 r"cache_holds\("],
+    "decode_cache.cu": [r"c\.max_pages", r"\broom\b", r"kOwnGate", r"kGateScores", r"dm\.nb", r"dm\.topk",
+                        r"dm\.batch", r"per_row|\* S\b", r"cache_holds\("],
+    "dense_bwd.cu": [r"dm\.T"],
+    "dense_bwd_tc.cu": [r"dm\.T"],
+}
+
+
+@pytest.mark.parametrize("name", CHECKED)
+def test_the_checked_build_has_checks_to_fire(name):
+    checks = arguments(source(name), "MOBA_CHECK")
+    for limit in CHECKED[name]:
+        assert [c for c in checks if re.search(limit, c)], limit
