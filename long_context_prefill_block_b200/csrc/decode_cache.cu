@@ -264,14 +264,8 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const int cs, const int
     return;
   const int c = p / dm.B, need = min(dm.topk - 1, c);
   if (!MOBA_CHECK(c < dm.nb && rows * c <= kGateScores && r < dm.batch, a.status)) return;
-  auto sync = [&] {
-    if (cs == 1)
-      __syncthreads();
-    else
-      tc::cluster_sync();
-  };
   if (need > 0) {
-    sync();  // also: CTA 0 runs, so its shared memory can be written
+    tc::cluster_sync();  // also: CTA 0 runs, so its shared memory can be written
     constexpr int LPB = D / 4, BPW = 32 / LPB, U = 8;  // lanes a mean, means a warp, steps in flight
     const int sub = lane % LPB, per = (c + cs - 1) / cs;
     const int first = rank * per, end = min(c, first + per), stride = kGateThreads / 32 * BPW;
@@ -292,18 +286,13 @@ cache_gate_kernel(const Step a, const T* __restrict__ q, const int cs, const int
           float acc = fmaf(kv[u].w, qv.w, fmaf(kv[u].z, qv.z, fmaf(kv[u].y, qv.y, kv[u].x * qv.x)));
 #pragma unroll
           for (int off = LPB / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-          if (sub == 0 && i0 + u * stride < end) {
-            float* at = &score[j * c + i0 + u * stride];
-            if (cs == 1)
-              *at = acc;
-            else
-              tc::store_first(at, acc);
-          }
+          if (sub == 0 && i0 + u * stride < end)
+            tc::store_first(&score[j * c + i0 + u * stride], acc);
         }
       }
     }
   }
-  sync();
+  tc::cluster_sync();
   if (rank != 0) return;
   const int words = (c + 31) / 32;
   for (int j = warp; j < rows; j += kGateThreads / 32) {
@@ -1100,8 +1089,8 @@ cudaError_t run_gate(const Step& a, const void* q, cudaStream_t st) {
   int rows = dm.shared ? 1 : grp < kGateRows ? grp : kGateRows;
   if (rows > kGateScores / dm.nb) rows = kGateScores / dm.nb;
   const int chunks = dm.shared ? 1 : (grp + rows - 1) / rows;
-  // CTAs a cluster: 16 to 32 blocks each and more, up to four a warp; one CTA to 64 blocks
-  const int cs = dm.nb > 128 ? 8 : dm.nb > 64 ? 4 : 1;
+  // CTAs a cluster: 16 to 32 blocks each and more, up to four a warp
+  const int cs = dm.nb > 128 ? 8 : 4;
   const int64_t grid = (int64_t)dm.T * dm.Hkv * chunks * cs;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   const size_t smem = sizeof(float) * rows * ((size_t)dm.nb + (dm.nb + 31) / 32);
