@@ -178,9 +178,10 @@ __device__ __forceinline__ int find_request_warp(const int32_t* __restrict__ cu,
 struct TilePlace {
   int start, len, slots, rest;
 };
-// A sequence of a length in [0, max_seqlen] whose rows are all among the call's.
-__device__ __forceinline__ bool has_place(const Dims& dm, int start, int end) {
-  return start >= 0 && end >= start && end <= dm.T && end - start <= dm.max_seqlen;
+// A sequence of a length in [0, max_seqlen] whose rows are all among the call's;
+// a negative start or length is past every bound.
+__device__ __forceinline__ bool has_place(const Dims& dm, uint32_t start, uint32_t len) {
+  return len <= (uint32_t)min(dm.max_seqlen, dm.T) && start <= (uint32_t)dm.T - len;
 }
 template <int ROWS>
 __host__ __device__ inline bool even_lengths(const Dims& dm) {
@@ -223,9 +224,9 @@ __device__ __forceinline__ TilePlace find_tile(const Dims& dm, const int32_t* __
     rest = x - base * heads;
     if (rest < 0 || rest >= slots * heads) return {0, 0, 0, 0};  // offsets that fall
   }
-  const int start = cu[b], end = cu[b + 1];
-  if (!has_place(dm, start, end)) return {0, 0, 0, 0};
-  return {start, end - start, slots, rest};
+  const uint32_t start = cu[b], len = (uint32_t)cu[b + 1] - start;
+  if (!has_place(dm, start, len)) return {0, 0, 0, 0};
+  return {(int)start, (int)len, slots, rest};
 }
 
 // Request r and cache position of row i of a call on a paged cache: request

@@ -47,7 +47,7 @@ dense_bwd_stat_kernel(Dims dm, const T* __restrict__ out, const T* __restrict__ 
   const int h = blockIdx.y, t0 = blockIdx.x * 32;
   if (h == 0 && t0 == 0) {  // every sequence, those that get no tile too
     for (int b = threadIdx.x; b < dm.batch; b += kThreads)
-      if (!has_place(dm, cu[b], cu[b + 1])) set_status(status, kStInvalidArg);
+      if (!has_place(dm, cu[b], (uint32_t)cu[b + 1] - cu[b])) set_status(status, kStInvalidArg);
   }
   const int sub = threadIdx.x % LPR, rr = threadIdx.x / LPR;
   for (int r = rr; r < 32; r += RPS) {
@@ -73,7 +73,7 @@ dense_bwd_stat_kernel(Dims dm, const T* __restrict__ out, const T* __restrict__ 
       stat[(int64_t)h * dm.T + t] = lse[(int64_t)t * dm.Hq + h] * kLog2e;
       stat[((int64_t)dm.Hq + h) * dm.T + t] = ds[threadIdx.x];
       const int b = find_request(cu, dm.batch, t);
-      mine = b < dm.batch && t >= cu[b] && has_place(dm, cu[b], cu[b + 1]);
+      mine = b < dm.batch && t >= cu[b] && has_place(dm, cu[b], (uint32_t)cu[b + 1] - cu[b]);
     }
     owned[threadIdx.x] = mine;
   }
