@@ -255,3 +255,58 @@ def test_offsets_on_the_device_past_the_rows_are_reported_and_skipped(lens, dtyp
     for x, y in zip(got, want):
         assert ref.off(x[lens[0]:], y[lens[0]:].double().cpu()) <= 2 * TOL[dtype]
         assert not x[:lens[0]].any()
+
+
+def formulas_in_pieces(q, k, v, cu, out, lse, do, piece=1024):
+    """ref.dense_backward and, with sizes, the sums its errors are relative to, on the GPU for
+    `piece` queries at a time: (gradients, sums), float64."""
+    Hq, d = q.shape[1:]
+    grp = Hq // k.shape[1]
+    res = []
+    for sizes in (False, True):
+        f = torch.abs if sizes else (lambda x: x)
+        dq, dk, dv = (torch.zeros(x.shape, dtype=torch.float64, device=DEV) for x in (q, k, v))
+        for a, e in zip(cu.tolist(), cu.tolist()[1:]):
+            for i in range(a, e, piece):
+                j = min(i + piece, e)
+                seen = torch.arange(a, j, device=DEV)[None] <= torch.arange(i, j, device=DEV)[:, None]
+                for h in range(Hq):
+                    g = h // grp
+                    qh, oh, doh = (x[i:j, h].double() for x in (q, out, do))
+                    kh, vh = (x[a:j, g].double() for x in (k, v))
+                    p = torch.exp(qh @ kh.T / d ** 0.5 - lse[i:j, h].double()[:, None]) * seen
+                    D = (f(doh) * f(oh)).sum(1, keepdim=True) * (-1 if sizes else 1)
+                    ds = p * (f(doh) @ f(vh).T - D)
+                    dq[i:j, h] = ds @ f(kh) / d ** 0.5
+                    dk[a:j, g] += ds.T @ f(qh) / d ** 0.5
+                    dv[a:j, g] += p.T @ doh
+        res.append((dq, dk, dv))
+    return res
+
+
+def test_the_pieces_are_the_formulas():
+    q, k, v, do, cu = case((130, 1, 70), 4, 2, 64, torch.float32, seed=15)
+    out, lse, _ = run(q, k, v, do, cu)
+    got = formulas_in_pieces(*(x.to(DEV) for x in (q, k, v)), cu, out, lse, do.to(DEV), piece=33)
+    for sizes, mine in zip((False, True), got):
+        want = ref.dense_backward(q, k, v, cu, out.cpu(), lse.cpu(), do, sizes=sizes)
+        assert all(ref.off(x, y) < 1e-12 for x, y in zip(mine[:2 if sizes else 3], want))
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,dtype", [
+    ((8192,), 4, 4, 128, torch.bfloat16), ((16383,), 4, 1, 128, torch.bfloat16),
+    ((4001, 1, 2500, 129), 6, 2, 64, torch.bfloat16), ((5000, 8192), 2, 2, 64, torch.bfloat16),
+    ((8191,), 2, 1, 128, torch.float32), ((5000, 3000), 2, 2, 64, torch.float32)])
+def test_long_sequences_match_the_formulas(lens, Hq, Hkv, d, dtype):
+    """The lengths that training has. The tolerances above count a sum over 700 rows, 700 * 2^-24:
+    here over the longest sequence, and over every q head of a group."""
+    q, k, v, do, cu = (x.to(DEV) for x in case(lens, Hq, Hkv, d, dtype, seed=16))
+    out, lse = moba.dense_causal_forward(q, k, v, cu.cpu(), return_lse=True)
+    grads = moba.dense_causal_backward(q, k, v, cu.cpu(), out, lse, do)
+    assert moba.moba_device_status() == 0
+    want, sums = formulas_in_pieces(q, k, v, cu, out, lse, do)
+    tol = TOL[dtype] + (max(lens) * Hq // Hkv - 700) * 2.0 ** -24
+    for name, x, y, r in zip(("dq", "dk", "dv"), grads, want, (*sums[:2], None)):
+        err = float((x.double() - y).norm())
+        extra = d * 2.0 ** -24 * float(r.norm()) if r is not None else 0.0
+        assert err <= tol * float(y.norm()) + extra, (name, err / float(y.norm()), tol)
