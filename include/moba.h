@@ -332,8 +332,8 @@ typedef struct {
 /* Quantises the new rows k, v [total_tokens][Hkv][d] (p->dtype) into the
  * cache. kbar, if not NULL (fp32 [batch][moba_num_blocks(p)][Hkv][d]): the
  * mean of every block that these rows complete, over the rows as the cache
- * holds them (what a decode query of a later position scores); other entries
- * are left alone. cu_new: device int32 [batch + 1]. ws: with kbar,
+ * holds them, summed in fp32 (what a decode query of a later position scores);
+ * other entries are left alone. cu_new: device int32 [batch + 1]. ws: with kbar,
  * moba_cache_write_workspace_size(p) bytes (0 for a few rows), 32-byte aligned;
  * else not used. */
 MOBA_API size_t moba_cache_write_workspace_size(const moba_params* p);
@@ -350,7 +350,13 @@ MOBA_API moba_status moba_cache_read(const moba_params* p, const moba_cache* c,
  * [batch][moba_num_blocks(p)][Hkv][d], kept by moba_cache_write; only complete
  * blocks before each query's own block are read, and one whose score is NaN
  * is not chosen), then one softmax over the chosen blocks' keys, causal in
- * the own block. q, out [total_tokens][Hq][d] (p->dtype); lse fp32
+ * the own block. Codes and sums are exact or 32-bit; fp32 queries have nothing
+ * rounded to less. A bf16 query is rounded to f16 after a power of two has taken
+ * its largest entry to [1, 2) (entries below 2^-14 of that lose bits, down to
+ * 2^-24 of it), and a weight times its value's scale to f16 (half a step of
+ * 2^-11). Where a logit, or a sum of weights times values before it is
+ * normalised, passes 2^128, the result is an infinity or NaN.
+ * q, out [total_tokens][Hq][d] (p->dtype, not overlapping); lse fp32
  * [total_tokens][Hq] or NULL; idx int32 [total_tokens][Hq][k] or NULL;
  * cu_q: device int32 [batch + 1]; p->own_block must be 0.
  * ws: moba_decode_cache_workspace_size(p) bytes, 32-byte aligned. */

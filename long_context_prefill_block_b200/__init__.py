@@ -651,8 +651,8 @@ def moba_decode_cache(q, cache: MobaCache, page_table, seqlens, cu_q, kbar, bloc
     """moba_decode over a MobaCache: request r's queries (rows cu_q[r] .. cu_q[r+1]-1 of q
     [n, Hq, d]) stand at its last positions; kbar [batch, num_blocks, Hkv, d]: the block means
     that moba_cache_write keeps. max_seqlen, a bound on the lengths (default: what kbar has blocks
-    for), must have kbar's number of blocks. Rows behind cu_q[batch] are not written: a given out keeps them, fresh results hold
-    nothing defined there. Returns out [n, Hq, d] (and lse [n, Hq], idx [n, Hq, topk])."""
+    for), must have kbar's number of blocks. Rows behind cu_q[batch] are not written: a given out
+    (which must not overlap q) keeps them, fresh results hold nothing defined there. Returns out [n, Hq, d] (and lse [n, Hq], idx [n, Hq, topk])."""
     if q.dim() != 3 or cache.k.dim() != 4 or q.shape[2] != cache.k.shape[3]:
         raise ValueError("q must be [n, Hq, d] with the cache's head dim")
     n, hq, d = q.shape

@@ -22,7 +22,10 @@ namespace {
 constexpr int kThreads = 128;  // write and read: four warps that share nothing
 constexpr int kMeanThreads = 256;
 constexpr int kMaxCluster = 8;
-constexpr int kSMs = 148;  // of a B200: what the work of a warp is sized by
+// SMs of a B200: what the work of a warp is sized by. A constant, so that the size of
+// the write's workspace follows from the call alone and not from the device that is
+// current when it is asked for.
+constexpr int kSMs = 148;
 
 // Exponent of a row whose largest magnitude has the fp32 bits `top` (finite).
 __device__ __forceinline__ int row_exponent(uint32_t top) {
@@ -610,6 +613,13 @@ cudaError_t launch_cache_write(const Dims& dm, const Cache& c, const void* k, co
 cudaError_t launch_cache_means(const Dims& dm, const Cache& c, const int32_t* cu_new,
                                const float* sums, float* kbar, int* status, cudaStream_t st) {
   const int64_t slots = (int64_t)dm.T / dm.B + dm.batch;
+  // Four CTAs a block where blocks are long and few, which pays where their rows have
+  // to be read (one CTA, four): 4096 rows, too few for sums, in blocks of 1024 28.4 ->
+  // 17.8 us, one row each for 4 requests that ends a block of 4096 41.3 -> 15.1. Where
+  // sums are there it hardly matters: 16384 rows in blocks of 1024 25.2, 25.8; 65536 in
+  // blocks of 4096 80.9, 79.4; 32768 in blocks of 1024, the last below the limit, 44.8,
+  // 48.9. Above it: 65536 rows in blocks of 1024 79.6, 90.3, but one row each for 64
+  // requests that ends a block of 4096 44.4, 21.0.
   const int cs = dm.B >= 1024 && slots * dm.Hkv < 2 * kSMs ? 4 : 1;
   if (slots * cs > INT32_MAX) return cudaErrorInvalidValue;
   if (dm.B <= kSmallBlock) {

@@ -52,8 +52,8 @@ struct Split {
 // shared blocks of 512: 54 us with a block a CTA, 41 with all three (which
 // also need no merge). No slots for blocks that cannot exist: 8 requests of 778
 // tokens, four queries, blocks of 2048, topk 3: 33 us with them, 17.5 without.
-// fp32 queries have a CTA per q head with shared routing too (40 on 8 heads, eight
-// of 282 blocks: 101 us when counted by kv heads, 40). No parts of a block behind
+// fp32 queries have a CTA per q head with shared routing too (40 on 8 heads, d = 64,
+// eight of 282 blocks: 101 us when counted by kv heads, 40). No parts of a block behind
 // max_seqlen either: 4 requests of 200 tokens with blocks of 4096 had 32 a row, two
 // of them with keys. The rule asks for the call's sizes alone, so that the workspace
 // does not depend on the device that is current.
@@ -151,7 +151,12 @@ __device__ __forceinline__ void load_pages(const Step& a, int r, int g, int lo, 
 //
 // With at most kOwnGate blocks there is no such launch: every split chooses for
 // its row itself (choose_blocks), which costs it less than the launch and the
-// wait for it would.
+// wait for it would. us in a graph, chosen by a launch -> by each split: 48 requests,
+// two of 32, 48, 64 blocks of 512, shared, 53.7 -> 35.9, 54.7 -> 37.6, 54.7 -> 38.2; 4
+// requests, 11 of 64, 54.3 -> 45.8; 4 short ones, two of 64 blocks of 128, 15.6 -> 10.6.
+// 64 is what two words of a warp's flags hold. With four words the split's own choice
+// was still the quicker one at 65 and 128 blocks (54.2 -> 38.1 and 56.2 -> 41.2; 53.6 ->
+// 45.5 and 55.5 -> 49.4): it is not taken that far yet.
 constexpr int kGateThreads = 256;
 constexpr int kGateRows = 16;       // q rows of a group at a time, at most
 constexpr int kGateScores = 49152;  // scores that fit: 192 KB, rows times blocks
@@ -399,8 +404,8 @@ __device__ __forceinline__ float power_of_two(int e) {  // e in [-126, 127]
 //
 // Four queries on a million-token cache (32 heads, 12 of 256 blocks of 4096,
 // 1.44 GB of rows): 237 us, 6.1 TB/s; the same loop with fp32 FMA and loads to
-// registers, 462. What it took: the conversion instruction written out (through
-// the toolkit's structs it is taken apart again: 396 -> 325), references raised
+// registers, 462. What it took: the conversion instruction written out in place of
+// the toolkit's function (396 -> 325), references raised
 // only when passed and whole steps without masks, two-step rings for three CTAs
 // an SM instead of three-step ones for two (325 -> 236).
 constexpr int kW = 4;        // warps
@@ -1089,7 +1094,10 @@ cudaError_t run_gate(const Step& a, const void* q, cudaStream_t st) {
   int rows = dm.shared ? 1 : grp < kGateRows ? grp : kGateRows;
   if (rows > kGateScores / dm.nb) rows = kGateScores / dm.nb;
   const int chunks = dm.shared ? 1 : (grp + rows - 1) / rows;
-  // CTAs a cluster: 16 to 32 blocks each and more, up to four a warp
+  // CTAs a cluster: eight shorten the scoring of one request's many blocks (4 queries, 32
+  // heads; four CTAs, eight: 256 blocks 55.0, 54.4 us, 512 blocks 61.6, 56.4), four leave
+  // more clusters room at once (48 requests, shared: 128 blocks 31.0, 45.7; above the limit
+  // too, 256 blocks 33.3, 49.5).
   const int cs = dm.nb > 128 ? 8 : 4;
   const int64_t grid = (int64_t)dm.T * dm.Hkv * chunks * cs;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;

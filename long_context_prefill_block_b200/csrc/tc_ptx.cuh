@@ -282,10 +282,8 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, 
 }
 // The same for code that the whole warp runs: `on` is non-zero in the one
 // lane that issues. With the issue predicated instead of branched around, the
-// operands are warp-uniform values in straight-line code; inside a one-lane
-// branch each instruction first moves its six operand words to uniform
-// registers, which took about 125 clocks an instruction (eight of them 1000,
-// against 512 of execution).
+// whole warp computes the operands. The gradient of 4 x 8192 tokens, 16 heads:
+// 4.04 ms with a one-lane branch around each group of products, 3.66 without.
 __device__ __forceinline__ void mma_ss_on(uint32_t on, uint32_t d, uint64_t a, uint64_t b,
                                           uint32_t idesc, uint32_t accumulate) {
   asm volatile(

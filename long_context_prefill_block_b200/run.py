@@ -7,7 +7,8 @@
 Draws the workload's inputs on cuda:0, then makes --iters calls of one entry
 point through the public binding (forward, gate, backward, decode, the dense
 forward and its gradient, or the write, read and decode of an 8-bit cache that
-holds the workload's K and V in pages in random order) and prints the mean time per call (CUDA events) and the device status word. The
+holds the workload's K and V in pages in random order) and prints the mean
+time per call (CUDA events) and the device status word. The
 shape options override the named workload, so that a profiler can capture a
 kernel on a case a few GB in size that keeps the per-row work of the full
 workload (e.g. the million-token gate's 256 blocks at 131,072 tokens with
@@ -50,7 +51,8 @@ def main():
     ap.add_argument("--tokens", type=int, default=None, help="one sequence of this length")
     ap.add_argument("--block-size", type=int, default=None)
     ap.add_argument("--topk", type=int, default=None)
-    ap.add_argument("--call", default="forward", choices=["forward", "gate", "backward", "decode", "dense", "dense_backward",
+    ap.add_argument("--call", default="forward",
+                    choices=["forward", "gate", "backward", "decode", "dense", "dense_backward",
                              "cache_write", "cache_read", "cache_decode"])
     ap.add_argument("--queries", type=int, default=1, help="cache_decode: queries per request")
     ap.add_argument("--page-size", type=int, default=64, help="of the 8-bit cache")
