@@ -639,3 +639,67 @@ def test_blocks_far_longer_than_any_request(bound, shared, dtype):
     assert torch.cuda.max_memory_allocated() - held < 1 << 20
     assert moba.moba_device_status() == 0
     check_decode(q, pool, lens, nq, B, 2, shared, *got)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,shared", [(512, False), (64, True)])
+def test_captured_long_calls_replayed_on_other_inputs(B, shared, dtype):
+    """A write that leaves sums for its means, and a decode whose choice is a launch of its own, both
+    overlapped launches, in two graphs replayed in turn: the same bits as eager calls."""
+    lens, heads, d, page, topk = [9000, 34000], 8, 64, 64, 6
+    pool = Pool(lens, page, heads, d, seed=3)
+    drawn = [x.to(DEV) for x in pool.bits()]  # rows that no request has keep these
+    kbar = torch.zeros(2, -(-max(lens) // B), heads, d, device=DEV)
+    args = (pool.table, i32(lens))
+    g = torch.Generator(device=DEV).manual_seed(7)
+    draw = lambda n, h: (torch.randn(n, h, d, generator=g, device=DEV) * 0.7).to(dtype)  # noqa: E731
+    k, v, q = draw(sum(lens), heads), draw(sum(lens), heads), draw(4, 16)
+    write = lambda: moba.moba_cache_write(pool.cache, k, v, *args, offsets_w, kbar, B)  # noqa: E731
+    decode = lambda: moba.moba_decode_cache(q, pool.cache, *args, offsets_q, kbar, B, topk,  # noqa: E731
+                                            shared_routing=shared, return_lse=True, return_idx=True)
+    offsets_w, offsets_q = offsets(lens), offsets([1, 3])
+    write(), decode()
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    with torch.cuda.graph(graphs[0]):
+        write()
+    with torch.cuda.graph(graphs[1]):
+        got = decode()
+    for _ in range(3):
+        for x in (k, v, q):
+            x.copy_(draw(*x.shape[:2]))
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        bits, means, res = pool.bits(), kbar.clone(), [x.clone() for x in got]
+        for x, y in zip(pool.cache, drawn):
+            x.view(torch.uint8).copy_(y)
+        kbar.zero_()
+        write()
+        assert all(torch.equal(a, b) for a, b in zip(pool.bits(), bits))
+        assert torch.equal(kbar, means) and all(torch.equal(a, b) for a, b in zip(decode(), res))
+    assert moba.moba_device_status() == 0
+    if dtype == torch.float32:  # one look at the definition, too: 34000 keys of 8 heads on the CPU
+        check_decode(q, pool, lens, [1, 3], B, topk, shared, *res)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_calls_without_rows(dtype):
+    pool, kbar = filled([40, 3], 2, 64, 16, 16, seed=2)
+    before, means = pool.bits(), kbar.clone()
+    none, lens = offsets([0, 0]), i32([40, 3])
+    x = torch.empty(0, 2, 64, dtype=dtype, device=DEV)
+    moba.moba_cache_write(pool.cache, x, x, pool.table, lens, none, kbar, 16)
+    k, v = moba.moba_cache_read(pool.cache, pool.table, lens, none, 0, dtype=dtype)
+    out, lse, idx = moba.moba_decode_cache(x.new_empty(0, 4, 64), pool.cache, pool.table, lens, none,
+                                           kbar, 16, 3, return_lse=True, return_idx=True)
+    assert k.shape == v.shape == (0, 2, 64) and out.shape == (0, 4, 64)
+    assert lse.shape == (0, 4) and idx.shape == (0, 4, 3)
+    # rows that no request owns
+    y = torch.ones(5, 2, 64, dtype=dtype, device=DEV)
+    moba.moba_cache_write(pool.cache, y, y, pool.table, lens, none, kbar, 16)
+    moba.moba_cache_read(pool.cache, pool.table, lens, none, 5, dtype=dtype, k=y)
+    q = torch.ones(5, 4, 64, dtype=dtype, device=DEV)
+    out = moba.moba_decode_cache(q, pool.cache, pool.table, lens, none, kbar, 16, 3,
+                                 out=torch.full_like(q, 9.0))
+    assert moba.moba_device_status() == 0 and (y == 1).all() and (out == 9).all()
+    assert all(torch.equal(a, b) for a, b in zip(pool.bits(), before)) and torch.equal(kbar, means)
