@@ -368,8 +368,8 @@ MOBA_API moba_status moba_decode_cache(const moba_params* p, const void* q, cons
 
 /* Synchronises `stream`, returns the device status word of the current
  * device (MOBA_OK, MOBA_ERR_TIMEOUT, MOBA_ERR_BAD_INDICES, MOBA_ERR_INVALID_ARG
- * for a sequence longer than max_seqlen, or in the checked build
- * MOBA_ERR_CHECK) and clears it if `clear` is non-zero. The first error
+ * for a sequence longer than max_seqlen or a sequence or request that a call
+ * skipped, or in the checked build MOBA_ERR_CHECK) and clears it if `clear` is non-zero. The first error
  * recorded wins. */
 MOBA_API moba_status moba_device_status(void* stream, int clear);
 

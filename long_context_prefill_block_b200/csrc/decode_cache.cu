@@ -33,10 +33,10 @@ constexpr int kMaxPages = kMaxKeys / 16 + 2 * kMaxSlots;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // How a row's keys are divided. Its slots are the topk - 1 places for chosen
-// earlier blocks (no more than there can be such blocks) and, last, the own block, which with shared routing is one
-// slot among them and else is read apart, once for all heads of a group. Split
-// x: of group x / parts of `slots` slots, part x % parts of each block (parts
-// > 1 only where a group is one slot).
+// earlier blocks (no more than there can be such blocks) and, last, the own
+// block, which with shared routing is one slot among them and else is read apart,
+// once for all heads of a group. Split x: of group x / parts of `slots` slots,
+// part x % parts of each block (parts > 1 only where a group is one slot).
 struct Split {
   int keys;    // of a part
   int parts;   // of a block
